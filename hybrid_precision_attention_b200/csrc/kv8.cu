@@ -1,0 +1,313 @@
+// kv8.cu — writing the 8-bit block cache and reading it back.
+//
+// A block of 64 positions x 128 values of one (sequence, kv head), K and V
+// apart, has one float32 scale: s = amax / 448 (e4m3) or amax / 127 (int8),
+// code = round(x / s).  A block is quantised once all its positions are there,
+// from their 16-bit values; until then they stand in the tail, which keeps the
+// two newest blocks so that up to 64 positions can be taken back.
+//
+// Both kernels are bound by memory: an append reads each new row once and
+// writes its codes once, a read-back the other way round.
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "kv8.cuh"
+
+namespace hq {
+namespace {
+
+constexpr int TS = D + 4;  // row stride of the staged tile in floats: the V order's accesses (4 rows x 8 columns a step) hit 32 banks
+static_assert(D == 128, "the page orders are written for 128");
+
+struct AppendArgs {
+  hq_kv8_cache c;
+  const void* x[2];
+  int64_t tok[2], head[2];
+  int N;
+  const int32_t* cu;
+  const int32_t* kv_len;
+};
+
+template <class E>
+__device__ __forceinline__ void load8(const E* p, float (&x)[8]) {
+  E e[8];
+  *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = to_float(e[i]);
+}
+
+// One CTA per (block that new tokens touch, kv head, K or V).  Sequence b's
+// blocks are CTAs s_b, s_b + 1, .. with s_b = cu[b] / 64 + 2 b: n tokens touch
+// at most n / 64 + 2 blocks, so the ranges do not overlap and the host needs to
+// know N and B only.
+template <class E, int FMT>
+__global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ __align__(16) float tile[KV8_BLOCK * TS];
+  __shared__ int sh_b;
+  __shared__ uint32_t sh_amax;
+  const hq_kv8_cache& c = a.c;
+  const int h = blockIdx.y, which = blockIdx.z, tid = threadIdx.x, item = blockIdx.x;
+  if (tid == 0) {
+    sh_b = -1;
+    sh_amax = 0;
+  }
+  __syncthreads();
+  for (int b = tid; b < c.B; b += 256) {
+    const int lo = a.cu[b] / KV8_BLOCK + 2 * b, hi = a.cu[b + 1] / KV8_BLOCK + 2 * b + 2;
+    if (lo <= item && item < hi) sh_b = b;  // one b at most when cu ascends; any of them otherwise
+  }
+  __syncthreads();
+  const int b = sh_b;
+  Kv8Seq s;
+  if (item == 0 && h == 0 && which == 0)  // one CTA says which sequences are skipped
+    for (int i = tid; i < c.B; i += 256) kv8_seq(c, a.cu, a.kv_len, a.N, a.N, i, true, s);
+  if (b < 0 || !kv8_seq(c, a.cu, a.kv_len, a.N, a.N, b, false, s) || s.n == 0) return;
+  const int first_blk = s.first / KV8_BLOCK, last_blk = (s.len - 1) / KV8_BLOCK;
+  const int blk = first_blk + item - (s.row0 / KV8_BLOCK + 2 * b);
+  if (blk > last_blk) return;
+  const size_t bh = static_cast<size_t>(b) * c.Hkv + h;
+  const E* src = static_cast<const E*>(a.x[which]) + static_cast<int64_t>(s.row0 - s.first) * a.tok[which] +
+                 h * a.head[which];  // + position * tok: that position's row
+  uint16_t* tail = (which ? c.tail_v : c.tail_k) + bh * HQ_KV8_TAIL * D;
+  float* tail_scale = c.tail_scale + (bh * 2 + which) * HQ_KV8_TAIL;
+  const int p0 = blk * KV8_BLOCK, half = blk & 1;
+
+  if (p0 + KV8_BLOCK <= s.len) {
+    // the block is complete: its rows into the tile, new ones from the input,
+    // earlier ones from the tail
+    uint32_t amax = 0;
+#pragma unroll
+    for (int it = 0; it < KV8_BLOCK * D / 8 / 256; ++it) {
+      const int e = it * 256 + tid, r = e / (D / 8), d = e % (D / 8) * 8, p = p0 + r;
+      float x[8];
+      if (p >= s.first) {
+        load8(src + static_cast<int64_t>(p) * a.tok[which] + d, x);
+      } else {
+        const float sc = tail_scale[half * KV8_BLOCK + r];
+        const uint16_t* t = tail + half * KV8_BLOCK * D;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          x[i] = __half2float(__ushort_as_half(t[which ? HQ_KV8_V_INDEX(r, d + i) : HQ_KV8_K_INDEX(r, d + i)])) * sc;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
+      float4* q = reinterpret_cast<float4*>(tile + r * TS + d);
+      q[0] = make_float4(x[0], x[1], x[2], x[3]);
+      q[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    if ((tid & 31) == 0) atomicMax(&sh_amax, amax);
+    __syncthreads();
+    const float scale = kv8_scale(sh_amax, FMT);
+    const long long idx = kv8_page_index(c, bh, blk);
+    if (idx < 0) {
+      if (tid == 0) kv8_err(c, b, HQ_DEVERR_PAGE);
+    } else {
+      uint8_t* page = c.pages + static_cast<size_t>(idx) * HQ_KV8_PAGE_BYTES;
+#pragma unroll
+      for (int it = 0; it < KV8_BLOCK * D / 16 / 256; ++it) {
+        const int e = it * 256 + tid;  // 16-byte chunk of the page's codes
+        uint32_t w[4];
+        float x[4];
+        if (which) {
+          // V: words of one d and tokens r, r + 1, r + 8, r + 9
+          const int r = e / 128 * 16 + (e & 3) * 2, d = e / 32 % 4 * 32 + e / 4 % 8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float* t = tile + r * TS + d + 8 * i;
+            x[0] = t[0];
+            x[1] = t[TS];
+            x[2] = t[8 * TS];
+            x[3] = t[9 * TS];
+            w[i] = kv8_codes4<FMT>(x, scale);
+          }
+        } else {
+          // K: 16 consecutive d of one token
+          const int r = e / 64 * 8 + e / 4 % 8, d = e / 32 % 2 * 64 + (e & 3) * 16;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(tile + r * TS + d + 4 * i);
+            w[i] = kv8_codes4<FMT>(x, scale);
+          }
+        }
+        reinterpret_cast<uint4*>(page + (which ? HQ_KV8_V : 0))[e] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (tid == 0) *reinterpret_cast<float*>(page + (which ? HQ_KV8_VSCALE : HQ_KV8_KSCALE)) = scale;
+    }
+  }
+  // The tail's half of this block's parity is written by one CTA alone, the
+  // first touched block of that parity: it is the only one that may have read
+  // earlier rows there (above; the barrier orders the two), and it writes the
+  // new rows of the last touched block of that parity.
+  if (blk > first_blk + 1) return;
+  __syncthreads();
+  const int t0 = (last_blk - ((last_blk - blk) & 1)) * KV8_BLOCK;
+  const int warp = tid / 32, lane = tid % 32;
+  for (int p = max(t0, s.first) + warp; p < min(t0 + KV8_BLOCK, s.len); p += 8) {
+    const E* x = src + static_cast<int64_t>(p) * a.tok[which] + lane * 4;
+    E e[4];
+    *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(x);
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) amax = max(amax, __float_as_uint(to_float(e[i])) & 0x7fffffffu);
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    float sc = 1.0f;
+    if (amax >= 0x7f800000u) {
+      sc = __uint_as_float(0x7fc00000u);
+    } else if (IsBf16<E>::value && amax != 0) {
+      // the power of two that brings amax to [2^14, 2^15), itself a normal number
+      const int ex = max(static_cast<int>(amax >> 23) - 127 - 14, -126);
+      sc = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+    }
+    uint16_t* t = tail + half * KV8_BLOCK * D;
+    const int r = p % KV8_BLOCK;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = lane * 4 + i;
+      // the division by a power of two is exact, the rounding is to fp16 (exact for fp16 rows)
+      const __half v = sc == sc ? __float2half_rn(to_float(e[i]) / sc) : __float2half_rn(0.f);
+      t[which ? HQ_KV8_V_INDEX(r, d) : HQ_KV8_K_INDEX(r, d)] = __half_as_ushort(v);
+    }
+    if (lane == 0) tail_scale[p % HQ_KV8_TAIL] = sc;
+  }
+}
+
+struct ReadArgs {
+  hq_kv8_cache c;
+  const int32_t* kv_len;
+  int start, n, zero_rest;
+  void* out[2];
+  int64_t batch, head, tok;
+};
+
+// One CTA per (block, kv head and K or V, sequence): the page's 16-byte chunks
+// are dequantised into a row-major tile and its rows written out.
+template <class E, int FMT>
+__global__ void __launch_bounds__(256) kv8_read_kernel(const __grid_constant__ ReadArgs a) {
+  __shared__ __align__(16) float tile[KV8_BLOCK * TS];
+  const hq_kv8_cache& c = a.c;
+  const int h = blockIdx.y >> 1, which = blockIdx.y & 1, b = blockIdx.z, tid = threadIdx.x;
+  const int blk = a.start / KV8_BLOCK + blockIdx.x, p0 = blk * KV8_BLOCK;
+  int len = a.kv_len[b];
+  if (len > c.cap || len < 0) {
+    if (tid == 0) kv8_err(c, b, len < 0 ? HQ_DEVERR_ROWS : HQ_DEVERR_CAPACITY);
+    len = 0;
+  }
+  const size_t bh = static_cast<size_t>(b) * c.Hkv + h;
+  if (p0 + KV8_BLOCK <= len) {
+    const uint8_t* page = kv8_page(c, bh, blk);
+    const float scale = *reinterpret_cast<const float*>(page + (which ? HQ_KV8_VSCALE : HQ_KV8_KSCALE));
+#pragma unroll
+    for (int it = 0; it < KV8_BLOCK * D / 16 / 256; ++it) {
+      const int e = it * 256 + tid;
+      const uint4 u = reinterpret_cast<const uint4*>(page + (which ? HQ_KV8_V : 0))[e];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t lo, hi;
+        kv8_half4<FMT>(w[i], lo, hi);
+        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+        const float x[4] = {f0.x * scale, f0.y * scale, f1.x * scale, f1.y * scale};
+        if (which) {
+          const int r = e / 128 * 16 + (e & 3) * 2, d = e / 32 % 4 * 32 + e / 4 % 8 + 8 * i;
+          float* t = tile + r * TS + d;
+          t[0] = x[0];
+          t[TS] = x[1];
+          t[8 * TS] = x[2];
+          t[9 * TS] = x[3];
+        } else {
+          const int r = e / 64 * 8 + e / 4 % 8, d = e / 32 % 2 * 64 + (e & 3) * 16 + 4 * i;
+          *reinterpret_cast<float4*>(tile + r * TS + d) = make_float4(x[0], x[1], x[2], x[3]);
+        }
+      }
+    }
+  } else if (p0 < len) {
+    const uint16_t* t = (which ? c.tail_v : c.tail_k) + (bh * 2 + (blk & 1)) * KV8_BLOCK * D;
+    const float* sc = c.tail_scale + (bh * 2 + which) * HQ_KV8_TAIL + (blk & 1) * KV8_BLOCK;
+    for (int e = tid; e < (len - p0) * D; e += 256) {
+      const int r = e / D, d = e % D;
+      tile[r * TS + d] = __half2float(__ushort_as_half(t[which ? HQ_KV8_V_INDEX(r, d) : HQ_KV8_K_INDEX(r, d)])) * sc[r];
+    }
+  }
+  __syncthreads();
+  E* out = static_cast<E*>(a.out[which]) + b * a.batch + h * a.head;
+  constexpr int V = 16 / sizeof(E);
+  for (int e = tid; e < KV8_BLOCK * D / V; e += 256) {
+    const int r = e / (D / V), d = e % (D / V) * V, p = p0 + r;
+    if (p < a.start || p >= a.start + a.n || (p >= len && !a.zero_rest)) continue;
+    E y[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) y[i] = from_float<E>(p < len ? tile[r * TS + d + i] : 0.f);
+    *reinterpret_cast<uint4*>(out + static_cast<int64_t>(p - a.start) * a.tok + d) = *reinterpret_cast<const uint4*>(y);
+  }
+}
+
+bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+hq_status kv8_validate(const hq_kv8_cache* c) {
+  if (!c) return HQ_ERR_INVALID;
+  if (c->D != HQ_HEAD_DIM) return HQ_ERR_UNSUPPORTED;
+  if (c->B <= 0 || c->Hkv <= 0 || c->cap <= 0 || c->cap % 128 != 0) return HQ_ERR_INVALID;
+  if (c->fmt != HQ_KV8_E4M3 && c->fmt != HQ_KV8_INT8) return HQ_ERR_INVALID;
+  if (c->B > HQ_KV8_MAX_BATCH || c->Hkv > HQ_KV8_MAX_HEADS) return HQ_ERR_UNSUPPORTED;
+  if (!aligned16(c->pages) || !aligned16(c->tail_k) || !aligned16(c->tail_v) || !aligned16(c->tail_scale) || !aligned4(c->err))
+    return HQ_ERR_INVALID;
+  if (c->page_table != nullptr && (!aligned4(c->page_table) || c->n_pages < 1)) return HQ_ERR_INVALID;
+  return HQ_OK;
+}
+
+}  // namespace hq
+
+extern "C" {
+
+hq_status hq_kv8_validate(const hq_kv8_cache* c) { return hq::kv8_validate(c); }
+
+hq_status hq_kv8_append(const hq_kv8_cache* c, int32_t dtype, const void* k, int64_t k_tok, int64_t k_head, const void* v,
+                        int64_t v_tok, int64_t v_head, int32_t N, const int32_t* cu, const int32_t* kv_len,
+                        hq_stream_t stream) {
+  const hq_status st = hq::kv8_validate(c);
+  if (st != HQ_OK) return st;
+  if ((dtype != HQ_F16 && dtype != HQ_BF16) || N < 0 || !hq::aligned4(cu) || !hq::aligned4(kv_len)) return HQ_ERR_INVALID;
+  if (N == 0) return HQ_OK;
+  if (!hq::aligned16(k) || !hq::aligned16(v) || (k_tok | k_head | v_tok | v_head) % 8) return HQ_ERR_INVALID;
+  hq::AppendArgs a = {*c, {k, v}, {k_tok, v_tok}, {k_head, v_head}, N, cu, kv_len};
+  const dim3 grid(static_cast<unsigned>(N) / hq::KV8_BLOCK + 2u * c->B, c->Hkv, 2);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == HQ_F16) {
+    if (c->fmt == HQ_KV8_E4M3) hq::kv8_append_kernel<__half, HQ_KV8_E4M3><<<grid, 256, 0, s>>>(a);
+    else hq::kv8_append_kernel<__half, HQ_KV8_INT8><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (c->fmt == HQ_KV8_E4M3) hq::kv8_append_kernel<__nv_bfloat16, HQ_KV8_E4M3><<<grid, 256, 0, s>>>(a);
+    else hq::kv8_append_kernel<__nv_bfloat16, HQ_KV8_INT8><<<grid, 256, 0, s>>>(a);
+  }
+  return hq::cuda_status(cudaGetLastError(), "kv8 append launch");
+}
+
+hq_status hq_kv8_read(const hq_kv8_cache* c, int32_t dtype, const int32_t* kv_len, int32_t start, int32_t n, void* k_out,
+                      void* v_out, int64_t o_batch, int64_t o_head, int64_t o_tok, int32_t zero_rest, hq_stream_t stream) {
+  const hq_status st = hq::kv8_validate(c);
+  if (st != HQ_OK) return st;
+  if (dtype < HQ_F16 || dtype > HQ_F32 || start < 0 || n < 0 || !hq::aligned4(kv_len)) return HQ_ERR_INVALID;
+  if (n == 0) return HQ_OK;
+  if (start > c->cap || n > c->cap - start) return HQ_ERR_CAPACITY;
+  if (!hq::aligned16(k_out) || !hq::aligned16(v_out) || (o_batch | o_head | o_tok) % 8) return HQ_ERR_INVALID;
+  hq::ReadArgs a = {*c, kv_len, start, n, zero_rest, {k_out, v_out}, o_batch, o_head, o_tok};
+  const dim3 grid((start + n - 1) / hq::KV8_BLOCK - start / hq::KV8_BLOCK + 1, 2 * c->Hkv, c->B);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  auto go = [&](auto fmt) {
+    constexpr int F = decltype(fmt)::value;
+    if (dtype == HQ_F16) hq::kv8_read_kernel<__half, F><<<grid, 256, 0, s>>>(a);
+    else if (dtype == HQ_BF16) hq::kv8_read_kernel<__nv_bfloat16, F><<<grid, 256, 0, s>>>(a);
+    else hq::kv8_read_kernel<float, F><<<grid, 256, 0, s>>>(a);
+  };
+  if (c->fmt == HQ_KV8_E4M3) go(std::integral_constant<int, HQ_KV8_E4M3>{});
+  else go(std::integral_constant<int, HQ_KV8_INT8>{});
+  return hq::cuda_status(cudaGetLastError(), "kv8 read launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,120 @@
+// kv8.cuh — what the kernels of the 8-bit block cache share: element types,
+// page addressing, and the quantisers of a block.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace hq {
+
+constexpr int KV8_BLOCK = 64;                      // positions of a page
+constexpr int KV8_COPY = HQ_KV8_KSCALE + 16;       // bytes of a page that are copied: codes, scales, padding to 16
+
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(float x) { return x; }
+template <class E>
+__device__ __forceinline__ E from_float(float x);
+template <>
+__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ float from_float<float>(float x) { return x; }
+
+template <class E>
+struct IsBf16 {
+  static constexpr bool value = false;
+};
+template <>
+struct IsBf16<__nv_bfloat16> {
+  static constexpr bool value = true;
+};
+
+// Pool index of page j of (b, kv head) bh, -1 when the table's entry lies outside the pool.
+__device__ __forceinline__ long long kv8_page_index(const hq_kv8_cache& c, size_t bh, int j) {
+  const size_t npg = static_cast<size_t>(c.cap / KV8_BLOCK);
+  if (c.page_table == nullptr) return static_cast<long long>(bh * npg + j);
+  const int idx = c.page_table[bh * npg + j];
+  return (idx >= 0 && idx < c.n_pages) ? idx : -1;
+}
+__device__ __forceinline__ void kv8_err(const hq_kv8_cache& c, int b, uint32_t bit) {
+  atomicOr(reinterpret_cast<unsigned int*>(c.err + b), bit);
+}
+// For readers: an entry outside the pool is flagged and pool page 0 is read instead.
+__device__ __forceinline__ const uint8_t* kv8_page(const hq_kv8_cache& c, size_t bh, int j) {
+  const long long idx = kv8_page_index(c, bh, j);
+  if (idx < 0) {
+    kv8_err(c, static_cast<int>(bh / c.Hkv), HQ_DEVERR_PAGE);
+    return c.pages;
+  }
+  return c.pages + static_cast<size_t>(idx) * HQ_KV8_PAGE_BYTES;
+}
+
+// The new tokens of sequence b: n rows from row0, the first at position first,
+// len positions in all.  False (flagged, when `flag`) when the numbers do not
+// fit together or the cache; n == 0 is fine and has nothing to do.
+struct Kv8Seq {
+  int row0, n, first, len;
+};
+__device__ __forceinline__ bool kv8_seq(const hq_kv8_cache& c, const int32_t* cu, const int32_t* kv_len, int N, int max_new,
+                                        int b, bool flag, Kv8Seq& s) {
+  const int lo = cu[b], hi = cu[b + 1];
+  s.len = kv_len[b];
+  s.row0 = lo;
+  s.n = 0;
+  s.first = s.len;
+  uint32_t bad = 0;
+  if (lo < 0 || hi < lo || hi > N || hi - lo > max_new || s.len < hi - lo) bad = HQ_DEVERR_ROWS;
+  else if (s.len > c.cap) bad = HQ_DEVERR_CAPACITY;
+  if (bad) {
+    if (flag) kv8_err(c, b, bad);
+    return false;
+  }
+  s.n = hi - lo;
+  s.first = s.len - s.n;
+  return true;
+}
+
+// scale of a block from the bits of its largest magnitude (an infinity's or
+// NaN's bits are the largest of all); float32 division, as the format says
+__device__ __forceinline__ float kv8_scale(uint32_t amax_bits, int fmt) {
+  if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
+  if (amax_bits == 0u) return 1.0f;
+  return __fdiv_rn(__uint_as_float(amax_bits), fmt == HQ_KV8_E4M3 ? 448.0f : 127.0f);
+}
+// codes of four values, lowest byte first; `scale` NaN: zeros
+template <int FMT>
+__device__ __forceinline__ uint32_t kv8_codes4(const float (&x)[4], float scale) {
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = __fdiv_rn(x[i], scale);
+  if (FMT == HQ_KV8_E4M3) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+    return scale == scale ? (lo | hi << 16) : 0u;
+  }
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r |= (static_cast<uint32_t>(min(max(__float2int_rn(y[i]), -127), 127)) & 0xFFu) << (8 * i);
+  return scale == scale ? r : 0u;
+}
+
+// four codes -> two pairs of fp16, exact in both formats
+template <int FMT>
+__device__ __forceinline__ void kv8_half4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (FMT == HQ_KV8_E4M3) {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  } else {
+    // a byte with its sign bit flipped, under the exponent of 1024: 1024 + 128 + code
+    const uint32_t u = w ^ 0x80808080u;
+    lo = hsub2_u(prmt(u, 0x64646464u, 0x4140u), 0x64806480u);
+    hi = hsub2_u(prmt(u, 0x64646464u, 0x4342u), 0x64806480u);
+  }
+}
+
+}  // namespace hq

@@ -27,6 +27,13 @@ STATE_T, STATE_NPACKED, STATE_NVL, STATE_NQ, STATE_KSEL, STATE_ERR = range(6)
 STATE_WORDS = 8
 OP_SELECT, OP_MERGE, OP_DECODE = 0, 1, 2
 DEVERR_STAGING_FULL, DEVERR_CAPACITY, DEVERR_VL_CAPACITY, DEVERR_TIMEOUT, DEVERR_PAGE = 1, 2, 4, 8, 16
+DEVERR_ROWS = 32
+F16, BF16, F32 = 0, 1, 2
+_DTYPE = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN, ROPE_BANDS = range(5)
+KV8_E4M3, KV8_INT8 = 0, 1
+KV8_PAGE_BYTES, KV8_TAIL = 16448, 128
 
 
 class HqError(RuntimeError):
@@ -89,9 +96,43 @@ PREFILL_E4M3, PREFILL_INT8_QK = 0, 1
 _lib.hq_diag_stream_read.restype = _I
 _lib.hq_diag_stream_read.argtypes = [_P, _S, _P, _I, _P]
 
+
+
+class HqRopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("x_batch", "x_tok", "x_head", "y_batch", "y_tok", "y_head")
+    ] + [("H", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class HqKv8CacheStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Hkv", "D", "cap", "fmt", "n_pages")] + [
+        (n, ctypes.c_void_p) for n in ("pages", "page_table", "tail_k", "tail_v", "tail_scale", "err")]
+
+
+_L = ctypes.c_int64
+_F = ctypes.c_float
+_DBL = ctypes.c_double
+_KP = ctypes.POINTER(HqKv8CacheStruct)
+_RP = ctypes.POINTER(HqRopeTensor)
+_lib.hq_rope_freqs.restype = _I
+_lib.hq_rope_freqs.argtypes = [_I, _DBL, _I, _DBL, _DBL, _DBL, _DBL, _P, ctypes.POINTER(_F)]
+_lib.hq_rope.restype = _I
+_lib.hq_rope.argtypes = [_I, _I, _I, _I, _I, _I, _I, _RP, _RP, _P, _P, _F, _P]
+_lib.hq_kv8_validate.restype = _I
+_lib.hq_kv8_validate.argtypes = [_KP]
+_lib.hq_kv8_append.restype = _I
+_lib.hq_kv8_append.argtypes = [_KP, _I, _P, _L, _L, _P, _L, _L, _I, _P, _P, _P]
+_lib.hq_kv8_read.restype = _I
+_lib.hq_kv8_read.argtypes = [_KP, _I, _P, _I, _I, _P, _P, _L, _L, _L, _I, _P]
+_lib.hq_kv8_attn_workspace_bytes.restype = _S
+_lib.hq_kv8_attn_workspace_bytes.argtypes = [_KP, _I, _I]
+_lib.hq_kv8_attn.restype = _I
+_lib.hq_kv8_attn.argtypes = [_KP, _I, _P, _L, _L, _I, _I, _P, _P, _I, _I, _F, _P, _L, _L, _P, _P, _S, _P]
+
 EXPORTED = ("hq_abi_version", "hq_status_str", "hq_last_error", "hq_cache_validate", "hq_workspace_bytes", "hq_cache_reset",
             "hq_select_vlines", "hq_pack_merge", "hq_decode_attn", "hq_decode_attn_noalloc",
-            "hq_prefill_workspace_bytes", "hq_prefill_attn", "hq_diag_stream_read")
+            "hq_prefill_workspace_bytes", "hq_prefill_attn", "hq_rope_freqs", "hq_rope", "hq_kv8_validate", "hq_kv8_append",
+            "hq_kv8_read", "hq_kv8_attn_workspace_bytes", "hq_kv8_attn", "hq_diag_stream_read")
 
 
 def _check(st: int, what: str):
@@ -383,6 +424,227 @@ def hq_prefill_attn(q, k, v, vl_pos, n_vl: int, W: int, sm_scale: float = None, 
                                 qk_format, ctypes.c_float(sm_scale), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
            "hq_prefill_attn")
     return out
+
+
+# ----------------------------------------------------------------------------- rotary positions, 8-bit block cache
+
+class _On:
+    """The launch stream of a call (default: the current one of the tensors' device),
+    made current with its device, so that what the call allocates belongs to it."""
+
+    def __init__(self, device, stream):
+        self.enter = None
+        if stream is None:
+            if device.index is not None and device.index != torch.cuda.current_device():
+                self.enter = torch.cuda.device(device)
+                self.enter.__enter__()
+            self.ptr = torch.cuda.current_stream(device).cuda_stream
+        else:
+            if stream.device != device:
+                raise HqError(f"stream of {stream.device} for tensors on {device}")
+            self.enter = torch.cuda.stream(stream)
+            self.enter.__enter__()
+            self.ptr = stream.cuda_stream
+
+    def __enter__(self):
+        return self.ptr
+
+    def __exit__(self, *exc):
+        if self.enter is not None:
+            self.enter.__exit__(*exc)
+
+
+def _rows(t, device, shape, name, dtypes=(torch.float16, torch.bfloat16)):
+    """A CUDA tensor of that shape (None: any size), its last dimension contiguous."""
+    if t.device != device or t.dtype not in dtypes or t.dim() != len(shape) or t.stride(-1) != 1 and t.shape[-1] > 1 or \
+            any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise HqError(f"{name}: expected {'/'.join(str(d) for d in dtypes)} {tuple(shape)} on {device} with contiguous "
+                      f"rows, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+
+
+def _ints(t, device, shape, name):
+    if t.device != device or t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise HqError(f"{name}: expected contiguous {torch.int32} {shape} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+class RopeTable:
+    """Frequencies of ``rot`` rotated elements (include/hq.h, hq_rope_freqs), on the device."""
+
+    def __init__(self, rot: int, base: float = 10000.0, kind: int = ROPE_PLAIN, factor: float = 1.0, orig_len: float = 0,
+                 low: float = 0, high: float = 0, device="cuda"):
+        f = np.zeros(max(rot, 0) // 2, dtype=np.uint64)
+        amp = _F()
+        _check(_lib.hq_rope_freqs(rot, base, kind, factor, orig_len, low, high, f.ctypes.data, ctypes.byref(amp)), "hq_rope_freqs")
+        self.rot, self.amp = rot, amp.value
+        self.freqs = torch.from_numpy(f.view(np.int64)).to(device)
+
+
+def hq_rope(q, k, pos, table: RopeTable, layout: int = ROPE_HALF, grad: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary positions of q [B, T, Hq, D] and k [B, T, Hkv, D] (or None) at pos int32 [B, T]; without a batch
+    dimension [T, H, D] and [T].  Strided views are taken as they are; q_out, k_out may be q, k themselves.
+    ``grad``: the transposed rotation (gradients of q and k from those of the outputs).  Returns (q_out, k_out)."""
+    dev = table.freqs.device
+    n = q.dim()
+    if n not in (3, 4):
+        raise HqError(f"q: expected [B, T, H, D] or [T, H, D], got {tuple(q.shape)}")
+    lead, D = tuple(q.shape[:-2]), q.shape[-1]
+    B, T = lead if n == 4 else (1,) + lead
+    _ints(pos, dev, lead, "pos")
+    with _On(dev, stream) as s:
+        sides = []
+        for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+            if x is None:
+                sides.append((None, None))
+                continue
+            _rows(x, dev, lead + (None, D), name, (q.dtype,) if q.dtype in _DTYPE else tuple(_DTYPE))
+            if y is None:
+                y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            else:
+                _rows(y, dev, tuple(x.shape), name + "_out", (q.dtype,))
+            xs, ys = x.stride(), y.stride()
+            if n == 3:
+                xs, ys = (0,) + xs, (0,) + ys
+            sides.append((y, HqRopeTensor(x.data_ptr(), y.data_ptr(), xs[0], xs[1], xs[2], ys[0], ys[1], ys[2], x.shape[-2], 0)))
+        (yq, a), (yk, b) = sides
+        _check(_lib.hq_rope(_DTYPE[q.dtype], B, T, D, table.rot, layout, 1 if grad else 0, a, b, pos.data_ptr(),
+                            table.freqs.data_ptr(), table.amp, s), "hq_rope")
+    return yq, yk
+
+
+class Kv8Cache:
+    """Device buffers of one layer's 8-bit block cache (layout: include/hq.h, struct hq_kv8_cache).
+
+    ``paged=True`` keeps the blocks in a pool of ``n_pages`` pages (default: what the batch can use) with a page
+    table [B, Hkv, cap/64] (``page_order`` fills it, else in order).  ``pages``, ``page_table``, ``tail_k``,
+    ``tail_v`` and ``tail_scale`` may be given as tensors of the documented layout instead."""
+
+    def __init__(self, B: int, Hkv: int, cap: int, fmt: int = KV8_E4M3, device="cuda", D: int = HQ_HEAD_DIM,
+                 paged: bool = False, n_pages: int = None, page_order=None, pages=None, page_table=None, tail_k=None,
+                 tail_v=None, tail_scale=None):
+        cap = ((cap + 127) // 128) * 128
+        self.B, self.Hkv, self.D, self.cap, self.fmt, self.npg = B, Hkv, D, cap, fmt, cap // PAGE_POSITIONS
+        dev = pages.device if pages is not None else torch.device(device)
+        z = lambda shape, dt: torch.zeros(shape, dtype=dt, device=dev)
+        if page_table is None and paged:
+            n_pages = n_pages if n_pages is not None else B * Hkv * self.npg
+            order = torch.arange(B * Hkv * self.npg, dtype=torch.int32) if page_order is None else \
+                torch.as_tensor(page_order, dtype=torch.int32)
+            page_table = order.reshape(B, Hkv, self.npg).to(dev).contiguous()
+        if pages is None:
+            pages = z((n_pages if n_pages is not None else B * Hkv * self.npg, KV8_PAGE_BYTES), torch.uint8) \
+                if page_table is not None else z((B, Hkv, self.npg, KV8_PAGE_BYTES), torch.uint8)
+        self.pages, self.page_table = pages, page_table
+        dev = pages.device
+        if page_table is not None:
+            _ints(page_table, dev, (B, Hkv, self.npg), "page_table")
+            _need(pages, torch.uint8, (pages.shape[0], KV8_PAGE_BYTES), "pages")
+        else:
+            _need(pages, torch.uint8, (B, Hkv, self.npg, KV8_PAGE_BYTES), "pages")
+        self.tail_k = tail_k if tail_k is not None else z((B, Hkv, 2, 64 * D), torch.float16)
+        self.tail_v = tail_v if tail_v is not None else z((B, Hkv, 2, 64 * D), torch.float16)
+        self.tail_scale = tail_scale if tail_scale is not None else z((B, Hkv, 2, KV8_TAIL), torch.float32)
+        _need(self.tail_k, torch.float16, (B, Hkv, 2, 64 * D), "tail_k")
+        _need(self.tail_v, torch.float16, (B, Hkv, 2, 64 * D), "tail_v")
+        _need(self.tail_scale, torch.float32, (B, Hkv, 2, KV8_TAIL), "tail_scale")
+        self.err = z((B,), torch.int32)
+        self.device = dev = self.err.device
+        self.c = HqKv8CacheStruct(B, Hkv, D, cap, fmt, pages.shape[0] if page_table is not None else 0, *[
+            None if t is None else t.data_ptr() for t in (pages, page_table, self.tail_k, self.tail_v, self.tail_scale, self.err)])
+        self.ref = ctypes.byref(self.c)
+        _check(_lib.hq_kv8_validate(self.ref), "hq_kv8_validate")
+        self._ws, self._ws_bytes = {}, {}
+
+    def errors(self) -> list:
+        """Every sequence's DEVERR_* bits."""
+        return self.err.cpu().tolist()
+
+    def workspace(self, Hq: int, max_new: int, stream_ptr: int) -> torch.Tensor:
+        """Zeroed scratch of an attention call, one per launch stream: calls on different streams may run at the
+        same time.  A captured graph gets its own from its memory pool, cleared in the graph: replays of two graphs
+        share nothing."""
+        n = self._ws_bytes.get((Hq, max_new))
+        if n is None:
+            n = int(_lib.hq_kv8_attn_workspace_bytes(self.ref, Hq, max_new))
+            if n == 0:
+                raise HqError(f"hq_kv8_attn: {Hq} query heads over {self.Hkv} kv heads, {max_new} new tokens")
+            self._ws_bytes[(Hq, max_new)] = n
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(n, dtype=torch.uint8, device=self.device)
+        w = self._ws.get(stream_ptr)
+        if w is None or w.numel() < n:
+            w = self._ws[stream_ptr] = torch.zeros(n, dtype=torch.uint8, device=self.device)
+        return w
+
+
+def hq_kv8_append(cache: Kv8Cache, k, v, cu, kv_len, stream=None):
+    """Append rows cu[b] .. cu[b+1]-1 of k, v [N, Hkv, D] (fp16 or bf16) to sequence b as its positions
+    kv_len[b] - n_b .. kv_len[b] - 1; cu int32 [B+1], kv_len int32 [B] (new tokens included)."""
+    dev = cache.device
+    _rows(k, dev, (None, cache.Hkv, cache.D), "k")
+    _rows(v, dev, tuple(k.shape), "v", (k.dtype,))
+    _ints(cu, dev, (cache.B + 1,), "cu")
+    _ints(kv_len, dev, (cache.B,), "kv_len")
+    ks, vs = k.stride(), v.stride()
+    with _On(dev, stream) as s:
+        _check(_lib.hq_kv8_append(cache.ref, _DTYPE[k.dtype], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+                                  k.shape[0], cu.data_ptr(), kv_len.data_ptr(), s), "hq_kv8_append")
+
+
+def hq_kv8_read(cache: Kv8Cache, kv_len, start: int = 0, n: int = None, dtype=torch.float16, k_out=None, v_out=None,
+                zero_rest: bool = True, stream=None):
+    """Positions start .. start+n-1 (default: to the capacity) of every sequence, dequantised: (k, v), each
+    [B, Hkv, n, D].  Rows at or past kv_len[b] are zeroed, or with zero_rest=False left as they are."""
+    dev = cache.device
+    if n is None:
+        n = cache.cap - start
+    _ints(kv_len, dev, (cache.B,), "kv_len")
+    with _On(dev, stream) as s:
+        if (k_out is None) != (v_out is None):
+            raise HqError("hq_kv8_read: give both of k_out, v_out or neither")
+        if k_out is None:
+            if not zero_rest:
+                raise HqError("hq_kv8_read: zero_rest=False needs k_out, v_out")
+            if n < 0:
+                raise HqError(f"hq_kv8_read: {n} positions")
+            both = torch.empty((2, cache.B, cache.Hkv, n, cache.D), dtype=dtype, device=dev)
+            k_out, v_out = both[0], both[1]
+        _rows(k_out, dev, (cache.B, cache.Hkv, n, cache.D), "k_out", tuple(_DTYPE))
+        _rows(v_out, dev, tuple(k_out.shape), "v_out", (k_out.dtype,))
+        if k_out.stride() != v_out.stride():
+            raise HqError("hq_kv8_read: k_out and v_out need the same strides")
+        os_ = k_out.stride()
+        _check(_lib.hq_kv8_read(cache.ref, _DTYPE[k_out.dtype], kv_len.data_ptr(), start, n, k_out.data_ptr(),
+                                v_out.data_ptr(), os_[0], os_[1], os_[2], 1 if zero_rest else 0, s), "hq_kv8_read")
+    return k_out, v_out
+
+
+def hq_kv8_attn(cache: Kv8Cache, q, cu, kv_len, max_new: int, sm_scale: float = None, window: int = 0, out=None,
+                lse=None, return_lse: bool = False, ws=None, stream=None):
+    """Attention of the newest tokens (appended before): q [N, Hq, D] holds sequence b's queries as rows
+    cu[b] .. cu[b+1]-1, at most max_new of them, at its last positions; causal, with window > 0 over that many
+    positions.  Returns out [N, Hq, D], with return_lse (out, lse float [N, Hq], base 2)."""
+    dev = cache.device
+    _rows(q, dev, (None, None, cache.D), "q")
+    _ints(cu, dev, (cache.B + 1,), "cu")
+    _ints(kv_len, dev, (cache.B,), "kv_len")
+    N, Hq = q.shape[0], q.shape[1]
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        else:
+            _rows(out, dev, tuple(q.shape), "out", (q.dtype,))
+        if lse is None and return_lse:
+            lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
+        elif lse is not None:
+            _need(lse, torch.float32, (N, Hq), "lse")
+        if ws is None:
+            ws = cache.workspace(Hq, max_new, s)
+        qs, os_ = q.stride(), out.stride()
+        _check(_lib.hq_kv8_attn(cache.ref, _DTYPE[q.dtype], q.data_ptr(), qs[0], qs[1], Hq, N, cu.data_ptr(),
+                                kv_len.data_ptr(), max_new, window, cache.D ** -0.5 if sm_scale is None else sm_scale,
+                                out.data_ptr(), os_[0], os_[1], None if lse is None else lse.data_ptr(), ws.data_ptr(),
+                                ws.numel() * ws.element_size(), s), "hq_kv8_attn")
+    return (out, lse) if return_lse else out
 
 
 def hq_diag_stream_read(buf, sink, ctas_per_sm: int = 2, stream=None):

@@ -348,6 +348,189 @@ HQ_API hq_status hq_prefill_attn(int32_t B, int32_t Hq, int32_t Hkv, int32_t L, 
 HQ_API hq_status hq_decode_attn_noalloc(const hq_cache* c, const uint16_t* q, const uint16_t* k_new,
                                         const uint16_t* v_new, uint16_t* out, float sm_scale, hq_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions, and a plain 8-bit cache with its attention.  They have no
+ * counterpart in the method: they are what a serving layer needs around it
+ * (rotated queries and keys go into every attention call of this library) and
+ * the uniform low-precision cache that the hybrid one is weighed against.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of the calls below (f16: IEEE binary16, bf16: bfloat16). */
+enum { HQ_F16 = 0, HQ_BF16 = 1, HQ_F32 = 2 };
+
+/* Which elements of a head form a pair: (i, i + rot/2), or (2i, 2i + 1). */
+enum { HQ_ROPE_HALF = 0, HQ_ROPE_INTERLEAVED = 1 };
+
+/* Frequencies of the rot/2 pairs, w_i radians per position.  With
+ * w_i = base^(-2i/rot), f = factor and t_i = orig_len * w_i / 2 pi (the turns
+ * pair i makes in the original context):
+ *   PLAIN   w_i
+ *   LINEAR  w_i / f                               (position interpolation)
+ *   NTK     the base is base * f^(rot/(rot-2))    (rot > 2)
+ *   YARN    (1 - r_i) w_i + r_i w_i / f, r_i = clamp((i - a)/max(c - a, 0.001), 0, 1),
+ *           a = max(floor(d(high)), 0), c = min(ceil(d(low)), rot - 1),
+ *           d(x) = rot ln(orig_len / (2 pi x)) / (2 ln base); amp = 1 + 0.1 ln f for f > 1
+ *           (Peng et al. 2023, "YaRN"; defaults high = 32, low = 1)
+ *   BANDS   (1 - r_i) w_i / f + r_i w_i, r_i = clamp((t_i - low)/(high - low), 0, 1)
+ *           (defaults high = 4, low = 1)
+ */
+enum { HQ_ROPE_PLAIN = 0, HQ_ROPE_LINEAR = 1, HQ_ROPE_NTK = 2, HQ_ROPE_YARN = 3, HQ_ROPE_BANDS = 4 };
+
+/*
+ * Host-only: the table that hq_rope reads, written to HOST memory; the caller
+ * copies it to the device once.  freqs[i] = the fraction of a turn that pair i
+ * makes per position, as a 64-bit fixed-point fraction (unit 2^-64), so that
+ * position * freqs[i] modulo 2^64 is the angle modulo one turn, exact for any
+ * position.  *amp receives the factor of the rotated values (1 except YARN).
+ * low, high: 0 = the kind's default.  Requires rot even, 2 <= rot <= 65536,
+ * base > 1, factor >= 1, orig_len > 0 for YARN and BANDS, 0 < low < high there.
+ */
+HQ_API hq_status hq_rope_freqs(int32_t rot, double base, int32_t kind, double factor, double orig_len, double low,
+                               double high, uint64_t* freqs, float* amp);
+
+#define HQ_ROPE_MAX_DIM 512
+
+/* One tensor of a hq_rope call: x, y [B, T, H, D] with strides in elements, D contiguous. */
+typedef struct hq_rope_tensor {
+  const void* x;
+  void* y;
+  int64_t x_batch, x_tok, x_head;
+  int64_t y_batch, y_tok, y_head;
+  int32_t H;
+  int32_t reserved; /* 0 */
+} hq_rope_tensor;
+
+/*
+ * Rotary positions of q and (optionally, k != NULL) k in one launch: for each
+ * pair (u, v) of the first `rot` elements of a head,
+ *     (u, v) -> amp * (u cos a - v sin a, v cos a + u sin a),  a = w_i * pos[b, t],
+ * and elements rot .. D-1 are copied.  grad != 0 applies the transposed
+ * rotation instead (a -> -a): the gradient of x from that of y.
+ *   dtype HQ_F16, HQ_BF16 or HQ_F32 (the arithmetic is float32)
+ *   pos   int32 [B, T] contiguous, any sign; freqs uint64 [rot/2] on the device
+ * y may equal x with the same strides (in place); otherwise they must not
+ * overlap.  D <= HQ_ROPE_MAX_DIM, rot even, 0 < rot <= D.  B, T or H of 0: nothing
+ * is done.  Any element-aligned pointers and strides are accepted; 16-byte
+ * alignment of rows, D % 8 == 0 and rot % 16 == 0 (4 and 8 for f32) take the
+ * 16-byte path.
+ */
+HQ_API hq_status hq_rope(int32_t dtype, int32_t B, int32_t T, int32_t D, int32_t rot, int32_t layout, int32_t grad,
+                         const hq_rope_tensor* q, const hq_rope_tensor* k, const int32_t* pos, const uint64_t* freqs,
+                         float amp, hq_stream_t stream);
+
+/* 8-bit block cache: code formats.  Over the 64 x D values of a block (64
+ * positions of one sequence and kv head; K and V apart), in float32:
+ *   E4M3  s = amax / 448, code = e4m3_RN_sat(x / s)
+ *   INT8  s = amax / 127, code = clamp(rint_even(x / s), -127, 127)
+ * s = 1 when amax is 0; a block holding an infinity or NaN gets s = NaN (and
+ * codes 0): what reads it sees NaN. */
+enum { HQ_KV8_E4M3 = 0, HQ_KV8_INT8 = 1 };
+
+/* Page of 64 positions of one (sequence, kv head).  Element (r, d) of K stands
+ * at byte HQ_KV8_K_INDEX(r, d), of V at HQ_KV8_V + HQ_KV8_V_INDEX(r, d): the
+ * orders in which the matrix instructions of hq_kv8_attn take them, 16 bytes a
+ * thread. */
+#define HQ_KV8_PAGE_BYTES 16448
+#define HQ_KV8_V 8192
+#define HQ_KV8_KSCALE 16384 /* float32 */
+#define HQ_KV8_VSCALE 16388 /* float32; the bytes from 16392 on are padding */
+#define HQ_KV8_MAX_BATCH 4096
+#define HQ_KV8_MAX_HEADS 1024
+#define HQ_KV8_TAIL 128     /* positions of the 16-bit tail: the two newest blocks */
+#define HQ_KV8_K_INDEX(r, d) (((((r) / 8) * 2 + (d) / 64) * 8 + (r) % 8) * 64 + (d) % 64)
+#define HQ_KV8_V_INDEX(r, d)                                                                                     \
+  (((r) / 16) * 2048 + ((d) / 32) * 512 + (((d) % 8) * 4 + (r) % 8 / 2) * 16 + ((d) / 16 % 2) * 8 + ((d) / 8 % 2) * 4 + \
+   ((r) / 8 % 2) * 2 + (r) % 2)
+
+/*
+ * The 8-bit block cache of one attention layer (caller-owned device memory).
+ * Lengths are not part of it: every call takes them, since all layers of a
+ * model share them.
+ *   pages      uint8 [B, Hkv, cap/64, HQ_KV8_PAGE_BYTES] (page_table == NULL) or
+ *              a pool [n_pages, HQ_KV8_PAGE_BYTES], 16-byte aligned
+ *   page_table int32 [B, Hkv, cap/64] or NULL: pool page of positions 64 j .. 64 j + 63;
+ *              entries that no position reaches are not read.  Pages that an append
+ *              completes must belong to one (b, h) only; full pages may be shared.
+ *   tail_k, tail_v fp16 [B, Hkv, 2, 64 * D]: position p of the two newest blocks, in
+ *              half (p / 64) % 2 in the page's element order; zero-filled before first use
+ *   tail_scale float [B, Hkv, 2, 128]: (K, V) scale of the tail's row of position p at p % 128.
+ *              A row's value is fp16 * scale: scale is 1 for fp16 rows; for bf16 rows the
+ *              power of two that brings the row's largest magnitude to [2^14, 2^15), so that
+ *              every bit of a bf16 row within 2^-29 of its largest value is kept; NaN (and
+ *              zeros in the row) when the row holds an infinity or NaN
+ *   err        int32 [B]: HQ_DEVERR_* bits, OR-ed; zero-filled by the caller
+ * Positions of a block that is complete (all 64 cached) are read from its page,
+ * those of the incomplete last block from the tail.  Codes always come from the
+ * 16-bit values, however the tokens were split over appends.
+ * Limits: D == 128, cap a positive multiple of 128, B <= HQ_KV8_MAX_BATCH,
+ * Hkv <= HQ_KV8_MAX_HEADS.
+ */
+typedef struct hq_kv8_cache {
+  int32_t B, Hkv, D, cap;
+  int32_t fmt;     /* HQ_KV8_E4M3 or HQ_KV8_INT8 */
+  int32_t n_pages; /* pool pages (page_table != NULL) */
+  uint8_t* pages;
+  int32_t* page_table;
+  uint16_t* tail_k;
+  uint16_t* tail_v;
+  float* tail_scale;
+  int32_t* err;
+} hq_kv8_cache;
+
+/* device-side error bit of the calls below: cu is not ascending within [0, N], a sequence
+ * has more new tokens than max_new, or kv_len is smaller than its new tokens */
+#define HQ_DEVERR_ROWS 0x20u
+
+HQ_API hq_status hq_kv8_validate(const hq_kv8_cache* c);
+
+/*
+ * Append: sequence b's new tokens are rows cu[b] .. cu[b+1]-1 of k, v [N, Hkv, D]
+ * (HQ_F16 or HQ_BF16; strides in elements, multiples of 8; D contiguous) and take
+ * positions kv_len[b] - n_b .. kv_len[b] - 1, n_b = cu[b+1] - cu[b]: kv_len counts the
+ * new tokens.  Blocks that become complete are quantised into their pages, the newest
+ * two blocks' rows stand in the tail.  A call may start up to 64 positions before the
+ * end of what was appended (drafted tokens that were rejected): the rows from there on
+ * are replaced.  cu int32 [B+1], kv_len int32 [B] (device).  A sequence with
+ * kv_len > cap (HQ_DEVERR_CAPACITY) or inconsistent rows (HQ_DEVERR_ROWS) is left as it is.
+ */
+HQ_API hq_status hq_kv8_append(const hq_kv8_cache* c, int32_t dtype, const void* k, int64_t k_tok, int64_t k_head,
+                               const void* v, int64_t v_tok, int64_t v_head, int32_t N, const int32_t* cu,
+                               const int32_t* kv_len, hq_stream_t stream);
+
+/*
+ * Read back: positions start .. start+n-1 of every sequence, dequantised (code * scale
+ * in float32, rounded once), as k_out, v_out [B, Hkv, n, D] of dtype HQ_F16, HQ_BF16 or
+ * HQ_F32 (one set of strides in elements for both, multiples of 8; D contiguous).  Rows
+ * at or past kv_len[b] are left as they are, or zeroed with zero_rest != 0.
+ */
+HQ_API hq_status hq_kv8_read(const hq_kv8_cache* c, int32_t dtype, const int32_t* kv_len, int32_t start, int32_t n,
+                             void* k_out, void* v_out, int64_t o_batch, int64_t o_head, int64_t o_tok,
+                             int32_t zero_rest, hq_stream_t stream);
+
+/* Device workspace of hq_kv8_attn for these sizes (0: invalid).  It starts with
+ * counters: zero-fill it once before its first use; the kernels return them to zero.  A
+ * workspace must not be shared by calls that can run at the same time. */
+HQ_API size_t hq_kv8_attn_workspace_bytes(const hq_kv8_cache* c, int32_t Hq, int32_t max_new);
+
+/*
+ * Attention of each sequence's newest tokens over its cache (they must have been
+ * appended): query row cu[b] + i (i < n_b <= max_new) sits at position
+ * t = kv_len[b] - n_b + i and attends to positions j <= t, with window > 0 only to
+ * j > t - window:
+ *     out[row, h] = sum_j p_j v_j,  p = softmax_j(q[row, h] . k_j * sm_scale),
+ * each key and value as cached (read through the page table; no 16-bit copy is made).
+ * Query head h reads kv head h / (Hq / Hkv).
+ *   q, out [N, Hq, D] HQ_F16 or HQ_BF16, strides in elements (multiples of 8), D contiguous
+ *   lse    float [N, Hq] contiguous or NULL: log2 of the softmax's denominator,
+ *          log2 sum_j 2^(s_j), s_j = q.k_j * sm_scale * log2 e
+ * Rows outside [cu[0], cu[B]) and rows of a sequence that is skipped
+ * (HQ_DEVERR_CAPACITY, HQ_DEVERR_ROWS) are left as they are.
+ */
+HQ_API hq_status hq_kv8_attn(const hq_kv8_cache* c, int32_t dtype, const void* q, int64_t q_tok, int64_t q_head,
+                             int32_t Hq, int32_t N, const int32_t* cu, const int32_t* kv_len, int32_t max_new,
+                             int32_t window, float sm_scale, void* out, int64_t o_tok, int64_t o_head, float* lse,
+                             void* ws, size_t ws_bytes, hq_stream_t stream);
+
 /*
  * Measurement helper (no counterpart in the method): reads `bytes` (a multiple
  * of 16) of device memory at `src` (16-byte aligned) with 16-byte streaming

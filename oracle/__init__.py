@@ -18,5 +18,7 @@ Modules
   attention  decode attention over a hybrid cache, hybrid causal prefill
   hybrid     the hybrid KV-cache state machine (prefix init, decode steps,
              reselection every 64 tokens, staging -> hybrid merge)
+  rope       rotary positions and their scaled frequencies
+  kv8        the 8-bit block cache and attention over it
 """
-from . import formats, select, attention, hybrid  # noqa: F401
+from . import formats, select, attention, hybrid, rope, kv8  # noqa: F401

@@ -1,0 +1,629 @@
+"""The 8-bit block cache on the GPU against the float64 oracle.
+
+Codes, scales and the 16-bit tail are exact.  Read back: code * scale is one
+float32 product (2^-24), then half a step of the output type.
+
+Attention, for row r with weights p and values v:
+    |out - want| <= eps(t)/2 |want| + (2^-11 + 2^-15 + 3 dS) sum_j p_j |v_j|
+  eps(t)/2   the output's rounding
+  2^-11      the weights' rounding to fp16
+  2^-15      float32 sums of the weights and products, the exponentials' 2^-22
+             and the running references' rescalings, a few per block
+  dS         a score's error in nats: 128 float32 products and sums of size at
+             most S = sum_d |q_d k_d| sm_scale, 2^-18 S with the scales' and the
+             base-2 factor's roundings; a weight's relative error is twice that
+             (its own and the denominator's), and half as much again for the bound's
+             own slack
+The denominator's log: (dS + 2^-15) / ln 2 and its own rounding.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv8 as okv
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def _hq():
+    from hybrid_precision_attention_b200 import hq
+    return hq
+
+
+def _fmt(fmt):
+    return {"e4m3": _hq().KV8_E4M3, "int8": _hq().KV8_INT8}[fmt]
+
+
+def _ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Pair:
+    """A cache on the GPU and its sequences' oracles, fed the same rows."""
+
+    def __init__(self, B, Hkv, cap, fmt="e4m3", dtype="f16", paged=True, seed=0, spread=1.0):
+        hq = _hq()
+        self.rng = np.random.default_rng(seed)
+        self.B, self.Hkv, self.fmt, self.dtype, self.spread = B, Hkv, fmt, dtype, spread
+        order = self.rng.permutation(B * Hkv * ((cap + 127) // 128 * 2)) if paged else None
+        self.c = hq.Kv8Cache(B, Hkv, cap, fmt=_fmt(fmt), paged=paged, page_order=order)
+        self.ref = [okv.Kv8Ref(Hkv, fmt) for _ in range(B)]
+
+    def rows(self, n):
+        x = self.rng.standard_normal((n, self.Hkv, 128)) * self.spread
+        return torch.from_numpy(x).to(TYPES[self.dtype])
+
+    def append(self, news, at=None, k=None, v=None, stream=None):
+        """news[b] rows to each sequence; at[b]: position of the first (default: the end)."""
+        hq = _hq()
+        N = sum(news)
+        k = self.rows(N) if k is None else k
+        v = self.rows(N) if v is None else v
+        cu = np.concatenate(([0], np.cumsum(news)))
+        for b, n in enumerate(news):
+            self.ref[b].append(k[cu[b]:cu[b + 1]].double().numpy(), v[cu[b]:cu[b + 1]].double().numpy(), None if at is None else at[b])
+        self.cu, self.len = _ints(cu.tolist()), _ints([r.len for r in self.ref])
+        hq.hq_kv8_append(self.c, k.cuda(), v.cuda(), self.cu, self.len, stream=stream)
+
+    def check_stored(self):
+        """Codes, scales and tail of every position, exactly."""
+        hq = _hq()
+        pages = self.c.pages.reshape(-1, hq.KV8_PAGE_BYTES).cpu().numpy()
+        table = self.c.page_table.cpu().numpy() if self.c.page_table is not None else \
+            np.arange(self.B * self.Hkv * self.c.npg).reshape(self.B, self.Hkv, -1)
+        tails = [self.c.tail_k.cpu().numpy(), self.c.tail_v.cpu().numpy()]
+        unit = self.c.tail_scale.cpu().numpy()
+        r, d = np.arange(64)[:, None], np.arange(128)[None]
+        for b, ref in enumerate(self.ref):
+            for which in range(2):
+                codes, scales = ref.blocks(which)
+                full = codes.shape[1]
+                p = pages[table[b, :, :full]]
+                got = okv.code_values(okv.page_rows(p[..., 8192 * which:8192 * which + 8192], which), self.fmt)
+                s = np.ascontiguousarray(p[..., 16384 + 4 * which:16388 + 4 * which]).view(np.float32)[..., 0]
+                assert np.array_equal(s, scales, equal_nan=True) and np.array_equal(got, codes)
+                x = ref.x[which][:, full * 64:]
+                n = x.shape[1]
+                if n:
+                    t = tails[which][b, :, full % 2][:, (okv.k_index, okv.v_index)[which](r, d)][:, :n].astype(np.float64)
+                    u = unit[b, :, which, full % 2 * 64:full % 2 * 64 + n].astype(np.float64)
+                    fine = np.isfinite(x).all(-1)
+                    assert np.array_equal(np.isfinite(u), fine) and np.isfinite(t).all() and not t[~fine].any()
+                    assert np.array_equal((t * np.where(fine, u, 0)[..., None])[fine], x[fine])
+                    if self.dtype == "f16":
+                        assert (u[fine] == 1).all()
+
+    def attend(self, G, n, window=0, q=None, check=True, sm=None, **kw):
+        """The newest n[b] positions of each sequence attend; compared with the oracle."""
+        hq = _hq()
+        N, Hq = sum(n), G * self.Hkv
+        cu = np.concatenate(([0], np.cumsum(n)))
+        if q is None:
+            q = torch.from_numpy(self.rng.standard_normal((N, Hq, 128))).to(TYPES[self.dtype])
+        sm = 128 ** -0.5 if sm is None else sm
+        out, lse = hq.hq_kv8_attn(self.c, q.cuda(), _ints(cu.tolist()), _ints([r.len for r in self.ref]), max(n), sm_scale=sm,
+                                  window=window, return_lse=True, **kw)
+        torch.cuda.synchronize()
+        assert not any(self.c.errors())
+        if check:
+            for b, ref in enumerate(self.ref):
+                if n[b]:
+                    check_rows(out[cu[b]:cu[b + 1]], lse[cu[b]:cu[b + 1]], ref, q[cu[b]:cu[b + 1]].double().numpy(), sm, window,
+                               self.dtype)
+        return q, out, lse
+
+
+def check_rows(out, lse, ref, q, sm, window, dtype):
+    want, wlse, mass, size = ref.attend(q, sm, window)
+    got, glse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    dS = 2.0 ** -18 * size
+    nan = np.isnan(want)
+    assert np.array_equal(np.isnan(got), nan)
+    tol = torch.finfo(TYPES[dtype]).eps / 2 * np.abs(want) + (2.0 ** -11 + 2.0 ** -15 + 3 * dS[..., None]) * mass + 2.0 ** -25
+    err = np.abs(got - want)
+    assert (err[~nan] <= tol[~nan]).all(), (err / tol)[~nan].max()
+    fine = ~np.isnan(wlse)
+    assert np.array_equal(~np.isnan(glse), fine)
+    ltol = (dS + 2.0 ** -15) * 1.4427 + 2.0 ** -22 * np.abs(wlse)
+    assert (np.abs(glse - wlse)[fine] <= ltol[fine]).all()
+
+
+FORMS = [("e4m3", "f16"), ("int8", "f16"), ("e4m3", "bf16"), ("int8", "bf16")]
+
+
+# ----------------------------------------------------------------------------- write and read back
+
+@pytest.mark.parametrize("fmt,dtype", FORMS)
+@pytest.mark.parametrize("paged", [True, False])
+def test_append_in_any_split(fmt, dtype, paged):
+    """The same store whatever the calls: single tokens, odd runs, runs over several blocks from mid-block, none."""
+    p = Pair(5, 3, 700, fmt, dtype, paged, seed=1, spread=3.0)
+    p.append([64, 1, 0, 200, 130])
+    p.check_stored()
+    p.append([1, 62, 3, 0, 129])
+    p.check_stored()
+    p.append([63, 1, 250, 327, 5])
+    p.check_stored()
+    for n in ([1, 1, 1, 1, 1], [1, 0, 1, 0, 0], [5, 2, 8, 61, 127], [60, 100, 300, 5, 64]):
+        p.append(n)
+        p.check_stored()
+    assert not any(p.c.errors())
+
+
+@pytest.mark.parametrize("fmt,dtype", FORMS)
+def test_token_by_token(fmt, dtype):
+    p = Pair(2, 2, 256, fmt, dtype, seed=2, spread=0.01)
+    for i in range(200):
+        p.append([1, i % 2])
+        if i % 21 == 0 or i in (62, 63, 64, 127, 128, 199):
+            p.check_stored()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_take_back_drafted_tokens(dtype):
+    """An append that starts up to 64 positions before the end replaces what followed, over block borders too."""
+    p = Pair(4, 2, 512, "e4m3", dtype, seed=3)
+    p.append([100, 130, 64, 191])
+    p.append([8, 8, 8, 64])
+    p.append([5, 61, 3, 3], at=[103, 131, 64, 192])
+    p.check_stored()
+    p.append([64, 1, 64, 1], at=[104, 128, 3, 192])
+    p.check_stored()
+    p.append([30, 70, 1, 130])
+    p.check_stored()
+    assert not any(p.c.errors())
+
+
+def test_values_at_the_edges_of_the_types():
+    """Zero blocks, subnormals, the largest values, one outlier a block; scales from 2^-30 to 2^7."""
+    for dtype in ("f16", "bf16"):
+        for fmt in ("e4m3", "int8"):
+            p = Pair(1, 1, 640, fmt, dtype, seed=4)
+            big = torch.finfo(TYPES[dtype]).max
+            x = torch.zeros(640, 1, 128, dtype=torch.float64)
+            g = torch.Generator().manual_seed(5)
+            r = torch.randn(640, 1, 128, generator=g, dtype=torch.float64)
+            x[64:128] = r[64:128] * 2.0 ** -24
+            x[128:192] = r[128:192].clamp(-1, 1) * (60000.0 if dtype == "f16" else 1e30)
+            x[192:256] = r[192:256]
+            x[200, 0, 5] = big if dtype == "f16" else 3e38
+            x[256:320] = torch.sign(r[256:320]) * 2.0 ** -14
+            x[320:384] = r[320:384] * 2.0 ** torch.randint(-12, 8, (64, 1, 1), generator=g)
+            x[384:448, 0, 0] = 448.0
+            x[384:448, 0, 1:100] = torch.arange(99) * 0.5 + 0.25          # ties of both formats' codes
+            x[448:600] = r[448:600] * 1e-3
+            x = x.to(TYPES[dtype])
+            p.append([600], k=x[:600], v=-x[:600])
+            p.check_stored()
+
+
+def test_not_finite_rows_mark_their_block():
+    p = Pair(2, 2, 256, "e4m3", "f16", seed=6)
+    k, v = p.rows(200 + 70), p.rows(200 + 70)
+    k[3, 1, 7], v[130, 0, 100] = float("inf"), float("nan")
+    v[200 + 66, 1, 0] = float("-inf")                                    # in the second sequence's tail
+    p.append([200, 70], k=k, v=v)
+    p.check_stored()
+    hq = _hq()
+    K, V = hq.hq_kv8_read(p.c, p.len, n=200)
+    bad = torch.isnan(K[0]).any(-1).nonzero().tolist()
+    assert bad == [[1, i] for i in range(64)]
+    assert torch.isnan(V[0]).any(-1).nonzero().tolist() == [[0, i] for i in range(128, 192)]
+    assert torch.isnan(V[1]).any(-1).nonzero().tolist() == [[1, 66]]
+    p.append([0, 58])                                                     # the tail's row makes its block NaN
+    p.check_stored()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("out", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("start,n", [(0, 300), (0, 1), (37, 200), (64, 64), (250, 6), (299, 1), (0, 0), (383, 1)])
+def test_read_back(fmt, out, start, n):
+    hq = _hq()
+    p = Pair(4, 2, 384, fmt, "f16", seed=7)
+    p.append([300, 0, 64, 129])
+    want = [[r.cached(i) for i in range(2)] for r in p.ref]
+    K, V = hq.hq_kv8_read(p.c, p.len, start=start, n=n, dtype=TYPES[out])
+    # into the caller's own padded buffers, the rest left as it is
+    buf = torch.full((2, 4, n, 3, 136), 9.0, dtype=TYPES[out], device="cuda")
+    k2, v2 = buf[0, :, :, :2, :128].transpose(1, 2), buf[1, :, :, :2, :128].transpose(1, 2)
+    hq.hq_kv8_read(p.c, p.len, start=start, n=n, k_out=k2, v_out=v2, zero_rest=False)
+    for which, (x, y) in enumerate(((K, k2), (V, v2))):
+        for b in range(4):
+            w = want[b][which][:, start:start + n]
+            m = w.shape[1]
+            got = x[b].double().cpu().numpy()
+            tol = (torch.finfo(TYPES[out]).eps / 2 + 2.0 ** -24) * np.abs(w) * (1 + 2.0 ** -9) + 2.0 ** -25
+            assert (np.abs(got[:, :m] - w) <= tol).all() and not got[:, m:].any()
+            assert torch.equal(y[b, :, :m], x[b, :, :m]) and (y[b, :, m:] == 9).all()
+    assert (buf[..., 2, :] == 9).all() and (buf[..., 128:] == 9).all()
+    assert not any(p.c.errors())
+
+
+def test_strided_rows_of_the_fused_projection():
+    hq = _hq()
+    row = torch.randn(75, 8 + 2 * 2, 128, device="cuda").half()
+    c = hq.Kv8Cache(2, 2, 128)
+    cu, n = _ints([0, 70, 75]), _ints([70, 5])
+    hq.hq_kv8_append(c, row[:, 8:10], row[:, 10:], cu, n)
+    d = hq.Kv8Cache(2, 2, 128)
+    hq.hq_kv8_append(d, row[:, 8:10].contiguous(), row[:, 10:].contiguous(), cu, n)
+    assert torch.equal(c.pages, d.pages) and torch.equal(c.tail_k, d.tail_k) and torch.equal(c.tail_v, d.tail_v)
+    q = row[:, :8]
+    buf = torch.full((75, 10, 128), 3.0, device="cuda").half()
+    o = hq.hq_kv8_attn(c, q, cu, n, 70, out=buf[:, 1:9])
+    assert torch.equal(o, hq.hq_kv8_attn(d, q.contiguous(), cu, n, 70)) and (buf[:, [0, 9]] == 3).all()
+
+
+# ----------------------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("fmt,dtype", FORMS)
+@pytest.mark.parametrize("Hkv,G", [(1, 1), (2, 2), (3, 4), (1, 5), (2, 8), (1, 16)])
+def test_single_tokens(fmt, dtype, Hkv, G):
+    """One token of each sequence, at lengths around the block borders."""
+    lens = [1, 2, 15, 16, 17, 63, 64, 65, 100, 127, 128, 129, 192, 333, 0, 640]
+    p = Pair(len(lens), Hkv, 640, fmt, dtype, seed=8)
+    p.append(lens)
+    p.attend(G, [min(n, 1) for n in lens])
+
+
+@pytest.mark.parametrize("fmt,dtype", FORMS)
+@pytest.mark.parametrize("G,n", [(1, 2), (4, 2), (8, 1), (4, 5), (8, 8), (3, 7), (1, 17), (2, 40)])
+def test_drafted_tokens(fmt, dtype, G, n):
+    lens = [n, n + 1, 63, 64, 65, 70, 128, 131, 200, 0]
+    lens = [0 if m == 0 else max(m, n) for m in lens]
+    p = Pair(len(lens), 2, 256, fmt, dtype, seed=9)
+    p.append(lens)
+    p.attend(G, [min(m, max(1, n - b)) for b, m in enumerate(lens)])
+
+
+@pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 100, 1000])
+@pytest.mark.parametrize("n", [1, 6, 70])
+def test_window(window, n):
+    lens = [n, 64 + n, 128, 300, 257]
+    lens = [max(m, n) for m in lens]
+    p = Pair(len(lens), 2, 384, "e4m3", "f16", seed=10)
+    p.append(lens)
+    p.attend(4, [n] * len(lens), window=window)
+
+
+@pytest.mark.parametrize("fmt,dtype", FORMS)
+@pytest.mark.parametrize("L,n,G", [(128, 128, 4), (200, 200, 2), (333, 150, 8), (700, 300, 1), (1111, 129, 4)])
+def test_chunks(fmt, dtype, L, n, G):
+    """Chunks of a prompt: from the first position, from inside a block, alone and beside a shorter one."""
+    p = Pair(2, 1, 1152, fmt, dtype, seed=11)
+    p.append([L, L // 2])
+    p.attend(G, [n, min(n, L // 2) // 3 + 1])
+
+
+@pytest.mark.parametrize("fmt,dtype", [("e4m3", "f16"), ("int8", "bf16")])
+def test_long_contexts_split_over_the_grid(fmt, dtype):
+    p = Pair(2, 2, 9000, fmt, dtype, seed=12)
+    p.append([8999, 4100])
+    p.attend(4, [1, 1])
+    p.attend(4, [3, 1])
+    p.attend(8, [2, 16], window=5000)
+
+
+def test_sharp_and_flat_softmax():
+    """Scores far apart (one key takes all the weight) and all alike, at several scales."""
+    for sm in (1e-6, 0.05, 2.0):
+        p = Pair(2, 1, 512, "e4m3", "f16", seed=13, spread=2.0)
+        p.append([500, 321])
+        p.attend(4, [2, 2], sm=sm)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_blocks_whose_scales_lie_far_apart(dtype):
+    """Values of 2^-20 in some blocks and 2^12 in others, the weight on either: the accumulators keep both."""
+    p = Pair(1, 1, 512, "e4m3", dtype, seed=14)
+    k, v = p.rows(400).double(), p.rows(400).double()
+    q = torch.zeros(1, 4, 128, dtype=torch.float64)
+    q[0, :, 0] = torch.tensor([6.0, -6.0, 3.0, 0.0])
+    k[:, 0, 0] = torch.where(torch.arange(400) // 64 % 2 == 0, 30.0, -30.0)
+    v = v * torch.where(torch.arange(400) // 64 % 2 == 0, 2.0 ** -13, 2.0 ** 12)[:, None, None]
+    p.append([400], k=k.to(TYPES[dtype]), v=v.to(TYPES[dtype]))
+    p.attend(4, [1], q=q.to(TYPES[dtype]))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_large_and_small_queries(dtype):
+    p = Pair(1, 1, 256, "int8", dtype, seed=15)
+    p.append([200])
+    q = torch.from_numpy(p.rng.standard_normal((3, 4, 128)))
+    q[:, 1] *= 2.0 ** -14
+    q[:, 2] *= 1000.0 if dtype == "f16" else 1e6
+    q[:, 3] = 0
+    p.attend(4, [3], q=q.to(TYPES[dtype]))
+    if dtype == "bf16":
+        q = torch.from_numpy(p.rng.standard_normal((1, 4, 128)))
+        q[0, 0] *= 1e30
+        q[0, 1] *= 1e-38
+        p.attend(4, [1], q=q.to(torch.bfloat16), sm=1e-30)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_not_finite_values_behind_the_mask(fmt):
+    """Rows that a query must not see (later drafted tokens, positions before its window) do not reach it; rows that
+    it sees do."""
+    p = Pair(1, 1, 512, fmt, "f16", seed=16)
+    k, v = p.rows(330), p.rows(330)
+    k[10, 0, 3], v[20, 0, 5] = float("nan"), float("inf")                # block 0
+    k[328, 0, 1], v[329, 0, 2] = float("inf"), float("nan")              # the last two of four new tokens
+    p.append([330], k=k, v=v)
+    _, out, lse = p.attend(4, [4], window=100)
+    assert torch.isfinite(out[:2]).all() and torch.isnan(out[2:]).all()
+    _, out, _ = p.attend(4, [4])
+    assert torch.isnan(out).all()
+    # a window that starts inside the marked block: the block's scale marks all its rows
+    p2 = Pair(1, 1, 512, fmt, "f16", seed=17)
+    k, v = p2.rows(130), p2.rows(130)
+    v[0, 0, 0] = float("inf")
+    p2.append([130], k=k, v=v)
+    _, out, _ = p2.attend(2, [1], window=66)
+    assert torch.isfinite(out).all()
+    _, out, _ = p2.attend(2, [1], window=67)
+    assert torch.isnan(out).all()
+
+
+def test_a_query_that_is_not_finite_stays_alone():
+    p = Pair(1, 1, 256, "e4m3", "bf16", seed=18)
+    p.append([150])
+    q = torch.from_numpy(p.rng.standard_normal((2, 4, 128))).bfloat16()
+    q[0, 1, 5], q[1, 2, 0] = float("nan"), float("nan")
+    _, out, lse = p.attend(4, [2], q=q, check=False)
+    bad = torch.isnan(out).all(-1)
+    assert bad.nonzero().tolist() == [[0, 1], [1, 2]] and torch.equal(torch.isnan(lse), bad)
+    assert torch.equal(torch.isnan(out).any(-1), bad)
+
+
+def test_rows_that_no_sequence_has_are_left():
+    """Rows before cu[0], behind cu[B], and of sequences that are refused keep what they held."""
+    hq = _hq()
+    p = Pair(4, 2, 256, "e4m3", "f16", seed=19)
+    p.append([100, 60, 30, 200])
+    q = torch.randn(20, 8, 128, device="cuda").half()
+    out, lse = torch.full_like(q, 5.0), torch.full((20, 8), 5.0, device="cuda")
+    cu = _ints([2, 4, 4, 10, 13])
+    hq.hq_kv8_attn(p.c, q, cu, _ints([100, 60, 5, 257]), 6, out=out, lse=lse)
+    assert p.c.errors() == [0, 0, hq.DEVERR_ROWS, hq.DEVERR_CAPACITY]
+    keep = [0, 1] + list(range(4, 20))
+    assert (out[keep] == 5).all() and (lse[keep] == 5).all() and (out[2:4] != 5).any()
+    check_rows(out[2:4], lse[2:4], p.ref[0], q[2:4].double().cpu().numpy(), 128 ** -0.5, 0, "f16")
+
+
+def test_inconsistent_rows_are_refused_on_the_device():
+    hq = _hq()
+    p = Pair(3, 1, 256, "e4m3", "f16", seed=20)
+    p.append([64, 64, 64])
+    before = [t.clone() for t in (p.c.pages, p.c.tail_k, p.c.tail_v, p.c.tail_scale)]
+    k = torch.randn(6, 1, 128, device="cuda").half()
+    q = torch.randn(6, 2, 128, device="cuda").half()
+    for cu, lens, want in (([0, 7, 7, 7], [70, 64, 64], [32, 32, 32]), ([0, 3, 1, 6], [67, 64, 69], [0, 32, 0]),
+                           ([-4, 2, 2, 2], [70, 64, 64], [32, 0, 0]), ([0, 2, 4, 6], [1, -5, 300], [32, 32, 2])):
+        p.c.err.zero_()
+        out = torch.full_like(q, 5.0)
+        hq.hq_kv8_attn(p.c, q, _ints(cu), _ints(lens), 6, out=out)
+        assert p.c.errors() == want
+        if 0 not in want:
+            assert (out == 5).all()
+        p.c.err.zero_()
+        if 0 in want:                      # the sequences that fit are written: only the flags are compared
+            d = hq.Kv8Cache(3, 1, 256)
+            hq.hq_kv8_append(d, k, k, _ints(cu), _ints(lens))
+            assert d.errors() == want
+        else:
+            hq.hq_kv8_append(p.c, k, k, _ints(cu), _ints(lens))
+            assert p.c.errors() == want
+            assert all(torch.equal(a, b) for a, b in zip(before, (p.c.pages, p.c.tail_k, p.c.tail_v, p.c.tail_scale)))
+    p.c.err.zero_()                        # more new tokens than the call allows
+    out = torch.full_like(q, 5.0)
+    hq.hq_kv8_attn(p.c, q, _ints([0, 2, 4, 6]), _ints([64, 64, 64]), 1, out=out)
+    assert p.c.errors() == [32, 32, 32] and (out == 5).all()
+
+
+def test_bad_page_entries():
+    hq = _hq()
+    c = hq.Kv8Cache(2, 1, 256, paged=True, n_pages=8)
+    c.page_table[0, 0, 1], c.page_table[1, 0, 0] = 8, -1
+    k = torch.randn(260, 1, 128, device="cuda").half()
+    pages = c.pages.clone()
+    hq.hq_kv8_append(c, k, k, _ints([0, 130, 260]), _ints([130, 130]))
+    assert c.errors() == [hq.DEVERR_PAGE] * 2
+    changed = (c.pages != pages).any(-1).nonzero().flatten().tolist()
+    assert changed == [0, 5]               # the good entries' pages alone
+    c.err.zero_()
+    hq.hq_kv8_read(c, _ints([130, 130]), n=130)
+    assert c.errors() == [hq.DEVERR_PAGE] * 2
+    c.err.zero_()
+    hq.hq_kv8_attn(c, torch.randn(2, 2, 128, device="cuda").half(), _ints([0, 1, 2]), _ints([130, 130]), 1)
+    assert c.errors() == [hq.DEVERR_PAGE] * 2
+
+
+def test_pages_beyond_two_gigabytes():
+    """A pool whose last pages start past 2^31 bytes."""
+    hq = _hq()
+    n = (1 << 31) // hq.KV8_PAGE_BYTES + 40
+    p = Pair(1, 2, 512, "e4m3", "f16", paged=False, seed=21)
+    p.c = hq.Kv8Cache(1, 2, 512, paged=True, n_pages=n, page_order=list(range(n - 16, n)))
+    p.append([450])
+    p.check_stored()
+    p.attend(4, [1])
+    p.attend(4, [30])
+    K, _ = hq.hq_kv8_read(p.c, p.len, n=450, dtype=torch.float32)
+    assert np.abs(K[0].double().cpu().numpy() - p.ref[0].cached(0)).max() <= 2.0 ** -20
+
+
+def test_many_sequences():
+    lens = [(37 * i) % 150 for i in range(600)]
+    p = Pair(600, 1, 256, "int8", "f16", seed=22)
+    p.append(lens)
+    p.check_stored()
+    _, out, _ = p.attend(2, [min(1, n) for n in lens])
+    p.append([1] * 600)
+    p.attend(2, [1] * 600)
+
+
+def test_shared_full_pages():
+    """Two sequences over the same prefix pages, each with its own continuation."""
+    hq = _hq()
+    p = Pair(2, 1, 256, "e4m3", "f16", seed=23)
+    k, v = p.rows(128), p.rows(128)
+    p.c.page_table[0, 0] = _ints([0, 1, 2, 3])
+    p.c.page_table[1, 0] = _ints([0, 1, 4, 5])
+    p.append([128, 0], k=k, v=v)
+    p.ref[1].append(k.double().numpy(), v.double().numpy())
+    p.append([70, 5])
+    p.check_stored()
+    p.attend(4, [2, 1])
+
+
+# ----------------------------------------------------------------------------- streams, graphs, repeated calls
+
+def test_repeated_calls_give_the_same_bits():
+    p = Pair(3, 2, 4096, "e4m3", "f16", seed=24)
+    p.append([4000, 1500, 70])
+    for n in ([1, 1, 1], [5, 3, 1], [200, 64, 70]):
+        q, out, lse = p.attend(4, n, check=False)
+        for _ in range(5):
+            _, o, z = p.attend(4, n, q=q, check=False)
+            assert torch.equal(o, out) and torch.equal(z, lse)
+
+
+def test_two_streams_at_once():
+    p = Pair(2, 4, 8192, "e4m3", "f16", seed=25)
+    p.append([8000, 5001])
+    q, out, _ = p.attend(4, [1, 1], check=False)
+    q2, out2, _ = p.attend(4, [4, 4], check=False)
+    hq = _hq()
+    cu, cu2, n = _ints([0, 1, 2]), _ints([0, 4, 8]), _ints([8000, 5001])
+    qd, qd2 = q.cuda(), q2.cuda()
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        got[0].append(hq.hq_kv8_attn(p.c, qd, cu, n, 1, stream=s[0]))
+        got[1].append(hq.hq_kv8_attn(p.c, qd2, cu2, n, 4, stream=s[1]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, out) for x in got[0]) and all(torch.equal(x, out2) for x in got[1])
+
+
+def test_captured_steps():
+    """A decode step (append and attend) captured once and replayed as the lengths advance; two graphs replayed at the
+    same time share no scratch."""
+    hq = _hq()
+    p = Pair(3, 2, 512, "e4m3", "f16", seed=26)
+    p.append([62, 130, 1])
+    k, v = torch.empty(3, 2, 128, device="cuda").half(), torch.empty(3, 2, 128, device="cuda").half()
+    q = torch.randn(3, 8, 128, device="cuda").half()
+    cu, n = _ints([0, 1, 2, 3]), p.len.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        n += 1
+        hq.hq_kv8_append(p.c, k, v, cu, n)
+        out, lse = hq.hq_kv8_attn(p.c, q, cu, n, 1, return_lse=True)
+    for _ in range(5):
+        x, y = p.rows(3), p.rows(3)
+        k.copy_(x)
+        v.copy_(y)
+        for b in range(3):
+            p.ref[b].append(x[b:b + 1].double().numpy(), y[b:b + 1].double().numpy())
+        graph.replay()
+        torch.cuda.synchronize()
+        for b in range(3):
+            check_rows(out[b:b + 1], lse[b:b + 1], p.ref[b], q[b:b + 1].double().cpu().numpy(), 128 ** -0.5, 0, "f16")
+    p.check_stored()
+    both, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for g in both:
+        with torch.cuda.graph(g):
+            outs.append(hq.hq_kv8_attn(p.c, q, cu, n, 1))
+    want = hq.hq_kv8_attn(p.c, q, cu, n, 1)
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for g, st in zip(both, s):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+
+
+def test_workspace_of_the_caller():
+    hq = _hq()
+    p = Pair(1, 2, 4096, "e4m3", "f16", seed=27)
+    p.append([4000])
+    q, out, _ = p.attend(4, [1], check=False)
+    need = hq._lib.hq_kv8_attn_workspace_bytes(p.c.ref, 8, 1)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        assert torch.equal(hq.hq_kv8_attn(p.c, q.cuda(), _ints([0, 1]), p.len, 1, ws=ws), out)
+    with pytest.raises(hq.HqError, match="workspace"):
+        hq.hq_kv8_attn(p.c, q.cuda(), _ints([0, 1]), p.len, 1, ws=ws[:-16])
+
+
+def test_refusals_of_the_binding():
+    hq = _hq()
+    c = hq.Kv8Cache(2, 2, 128)
+    k = torch.randn(4, 2, 128, device="cuda").half()
+    q = torch.randn(4, 4, 128, device="cuda").half()
+    cu, n = _ints([0, 2, 4]), _ints([2, 2])
+    for a in ((k.float(), k.float(), cu, n), (k, k.bfloat16(), cu, n), (k[:, :1], k[:, :1], cu, n), (k, k[:3], cu, n),
+              (k, k, cu.long(), n), (k, k, cu[:2], n), (k, k, cu, n.cpu()), (k.transpose(1, 2), k, cu, n), (k.cpu(), k.cpu(), cu, n)):
+        with pytest.raises(hq.HqError):
+            hq.hq_kv8_append(c, *a)
+    for a, kw in (((q.float(), cu, n, 2), {}), ((q[:, :3], cu, n, 2), {}), ((q, cu, n, -1), {}), ((q, cu, n, 2), dict(window=-1)),
+                  ((q, cu, n, 2), dict(out=q[:3])), ((q, cu, n, 2), dict(out=q.bfloat16())), ((q, cu, n, 2), dict(sm_scale=0.0)),
+                  ((q, cu, n, 2), dict(lse=torch.empty(4, 3, device="cuda"))), ((q[..., :64], cu, n, 2), {})):
+        with pytest.raises(hq.HqError):
+            hq.hq_kv8_attn(c, *a, **kw)
+    for kw in (dict(n=129), dict(start=-1), dict(n=-2), dict(zero_rest=False), dict(k_out=k), dict(start=128, n=1)):
+        with pytest.raises(hq.HqError):
+            hq.hq_kv8_read(c, n, **kw)
+    with pytest.raises(hq.HqError):
+        hq.Kv8Cache(2, 2, 128, D=64)
+    with pytest.raises(hq.HqError):
+        hq.Kv8Cache(2, 2, 128, page_table=_ints([0]))
+    hq.hq_kv8_append(c, k[:0], k[:0], _ints([0, 0, 0]), _ints([0, 0]))
+    assert hq.hq_kv8_attn(c, q[:0], _ints([0, 0, 0]), _ints([0, 0]), 1).shape == (0, 4, 128)
+    assert not any(c.errors())
+
+
+# ----------------------------------------------------------------------------- together
+
+@pytest.mark.parametrize("fmt,dtype", [("e4m3", "f16"), ("int8", "bf16")])
+def test_a_layer_generates(fmt, dtype):
+    """Rotary positions, append and attention as a serving loop calls them: two ragged prompts in chunks, then decode
+    steps with drafted tokens, some of them taken back; each output against the oracle fed the rotated rows."""
+    hq = _hq()
+    Hq, Hkv, t = 8, 2, TYPES[dtype]
+    p = Pair(2, Hkv, 512, fmt, dtype, seed=28)
+    table = hq.RopeTable(64, 10000.0, kind=hq.ROPE_YARN, factor=4.0, orig_len=256)
+    at = [0, 0]
+    for news, kept in (([100, 37], [100, 37]), ([130, 0], [130, 0]), ([1, 1], [1, 1]), ([4, 4], [2, 4]), ([4, 4], [1, 1]), ([1, 64], [1, 64])):
+        N = sum(news)
+        row = torch.from_numpy(p.rng.standard_normal((N, Hq + 2 * Hkv, 128))).to(t).cuda()
+        pos = _ints([at[b] + i for b in range(2) for i in range(news[b])])
+        q, k = hq.hq_rope(row[:, :Hq], row[:, Hq:Hq + Hkv], pos, table)
+        p.append(news, at=at, k=k.cpu(), v=row[:, Hq + Hkv:].cpu())
+        p.attend(Hq // Hkv, news, q=q.cpu())
+        at = [a + n for a, n in zip(at, kept)]
+        for b in range(2):
+            for i in range(2):
+                p.ref[b].x[i] = p.ref[b].x[i][:, :at[b]]
+    assert not any(p.c.errors())
+
+
+def test_read_back_installs_a_hybrid_cache():
+    """The read-back rows are the dense prefix that the hybrid cache's selection and install take."""
+    hq = _hq()
+    p = Pair(1, 2, 512, "e4m3", "f16", seed=29)
+    p.append([400])
+    K, V = hq.hq_kv8_read(p.c, p.len, n=400)
+    h = hq.HybridCache(1, 8, 2, 512, W=64)
+    q_tail = torch.randn(1, 8, 64, 128, device="cuda").half()
+    hq.hq_select_vlines(h, K, q_tail)
+    hq.hq_pack_merge(h, K, V)
+    st = h.state()
+    assert st["T"] == 400 and st["err"] == 0
+    assert torch.equal(h.kr[0, :, 399 % h.R], K[0, :, 399]) and torch.equal(h.vr[0, :, 399 % h.R], V[0, :, 399])
