@@ -20,17 +20,24 @@
 // end and cut into gridDim equal runs.  A task that one CTA holds whole is
 // finished there; the pieces of the others go to the workspace and the CTA that
 // delivers a task's last piece joins them in order, so that results do not
-// depend on timing.  Within a CTA a producer warp keeps a ring of pages in
-// flight and NG groups of 4 warps take every NG-th block, 16 tokens a warp, each
-// warp with its own running maximum, sum and accumulators.
+// depend on timing.  Within a CTA NG groups of 4 warps take every NG-th block of
+// a task, 16 tokens a warp.  Each warp keeps a ring of its own 4 KB slices in
+// flight by bulk copies (a slice is free again as soon as it is in registers, and
+// no other warp is waited for) and its own running references, sums and
+// accumulators.
 //
-// Two running references per row, both powers of two exponents: m, the maximum
-// score, for the sum of weights; E, the maximum of score + log2(value scale),
-// for the accumulators, whose weights p * vscale enter the product as fp16 at
-// 2^14 * 2^(s + log2 vscale - E): the largest is 2^14, and the smallest normal
-// one is 2^-28 of it, whatever the ratios of the blocks' scales.
+// Two running references per row: m for the scores and, for the accumulators, E
+// for score + log2(value scale), so that blocks whose scales lie far apart keep
+// their precision.  A weight 2^(s - m) is summed in float32; its product with the
+// value scale enters the matrix product as fp16 at 2^(s + log2 vscale - E + 6).
+// The references are the exact maxima when they are set and stay as they are
+// until a score passes m by 2^8 or a scale its reference by 2: the common block
+// costs one comparison per score and one vote, and no cross-lane maximum.  The
+// largest fp16 weight is then 2^15 and the smallest normal one 2^-20 of the
+// reference.
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <type_traits>
 
 #include "kv8.cuh"
@@ -38,18 +45,26 @@
 namespace hq {
 namespace {
 
-constexpr float P_BIAS = 14.0f;  // log2 of the largest fp16 weight
-constexpr int OS = D + 4;        // row stride (floats) of accumulators in shared memory: 4 rows of a store step 8 banks apart
+constexpr float P_BIAS = 6.0f;     // log2 of the fp16 weight at both references
+constexpr float P_SLACK = 8.0f;    // how far (log2) a score may pass m
+constexpr float V_LIMIT = 128.0f;  // 2^(P_BIAS + 1): how far a value scale may pass its reference; 2^8 * 2^7 < 65504
+constexpr int OS = D + 4;          // row stride (floats) of accumulators in shared memory: 4 rows of a store step 8 banks apart
+constexpr int SLICE = 16 * D;      // bytes of one warp's 16 tokens of a page's K (or V) codes
+constexpr int SLOT = 2 * SLICE + 16;  // K slice, V slice, scales
 
-template <int NB, int NG>
+template <int NB>
 struct Cfg {
-  static constexpr int R = 8 * NB;            // rows of a task
-  static constexpr int WARPS = 4 * NG;        // consumers
-  static constexpr int THREADS = WARPS * 32 + 32;
-  static constexpr int OBUF = WARPS * R * OS * 4;
-  static constexpr int RED = WARPS * R * 16;  // (m, E, l) of each warp's rows
-  static constexpr int FIXED = OBUF + RED + 256;
-  static constexpr int STAGE_MAX = 12;
+  static constexpr int R = 8 * NB;              // rows of a task
+  // 12 warps while a thread's accumulators and query operands (48 NB registers)
+  // leave room in 168 registers, else 8 warps of up to 255
+  static constexpr int NG = NB <= 2 ? 3 : 2;
+  static constexpr int WARPS = 4 * NG;
+  static constexpr int THREADS = WARPS * 32;
+  static constexpr int OBUF = WARPS * 8 * OS * 4;  // accumulators of 8 rows at a time
+  static constexpr int RED = WARPS * R * 16;       // (m, E, l) of each warp's rows
+  static constexpr int SLOTS = NB <= 2 ? 3 : 5;    // ring of a warp
+  static constexpr int RING = WARPS * SLOTS * SLOT;
+  static constexpr int FIXED = OBUF + RED + RING + WARPS * SLOTS * 8 + 128;
 };
 
 struct AttnArgs {
@@ -59,7 +74,6 @@ struct AttnArgs {
   float* lse;
   int64_t q_tok, q_head, o_tok, o_head;
   int Hq, G, N, max_new, window, groups;  // groups: tasks of a (sequence, kv head)
-  int stages;
   const int32_t* cu;
   const int32_t* kv_len;
   float scale;  // sm_scale * log2 e
@@ -73,9 +87,7 @@ __device__ __forceinline__ void seq_blocks(const Kv8Seq& s, int window, int& beg
   end = s.n > 0 ? (s.len + KV8_BLOCK - 1) / KV8_BLOCK : begin;
 }
 
-__device__ __forceinline__ float log2_acc(float x) { return log2f(x); }
-
-// Bounded wait on a page of the ring; a copy that does not land within about a
+// Bounded wait on a slice of the ring; a copy that does not land within about a
 // second sets the sequence's error bit and ends the CTA's work.
 __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, int32_t* err, volatile int* stop) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -91,68 +103,71 @@ __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, int32_
   return true;
 }
 
-template <class E, int FMT, int NB, int NG>
-__global__ void __launch_bounds__(Cfg<NB, NG>::THREADS, 1) kv8_attn_kernel(const __grid_constant__ AttnArgs a) {
-  using C = Cfg<NB, NG>;
-  constexpr int R = C::R, CT = C::WARPS * 32;
+template <class E, int FMT, int NB>
+__global__ void __launch_bounds__(Cfg<NB>::THREADS, 1) kv8_attn_kernel(const __grid_constant__ AttnArgs a) {
+  using C = Cfg<NB>;
+  constexpr int R = C::R, NG = C::NG, SLOTS = C::SLOTS;
   extern __shared__ __align__(128) uint8_t sm[];
-  float* obuf = reinterpret_cast<float*>(sm);                    // [warp][row][OS]
-  float4* red = reinterpret_cast<float4*>(sm + C::OBUF);         // [warp][row] (m, E, l, -)
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::OBUF + C::RED);
-  uint64_t* empty = full + C::STAGE_MAX;
-  int* flags = reinterpret_cast<int*>(empty + C::STAGE_MAX);     // stop, last, total lo, hi
-  int* prefix = reinterpret_cast<int*>(sm + C::FIXED);           // blocks of the sequences before b (per task)
+  float* obuf = reinterpret_cast<float*>(sm);                       // [warp][row of 8][OS]
+  float4* red = reinterpret_cast<float4*>(sm + C::OBUF);            // [warp][row] (m, E, l, -)
+  uint8_t* rings = sm + C::OBUF + C::RED;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(rings + C::RING);
+  int* flags = reinterpret_cast<int*>(bars + C::WARPS * SLOTS);     // stop, last; 16.. warp totals of the plan
+  int* prefix = reinterpret_cast<int*>(sm + C::FIXED);              // blocks (per task) of the sequences before b
   const int B = a.c.B;
-  uint8_t* ring = sm + C::FIXED + ((B + 1) * 4 + 127) / 128 * 128;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const hq_kv8_cache& c = a.c;
 
   // ---------------------------------------------------------------- plan
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < a.stages; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 4);
-    }
+  uint64_t* full = bars + warp * SLOTS;
+  if (lane == 0) {
+    for (int i = 0; i < SLOTS; ++i) mbar_init(full + i, 1);
     fence_mbar_init();
-    flags[0] = 0;
   }
-  if (warp == 0) {
-    int sum = 0;
-    for (int b0 = 0; b0 < B; b0 += 32) {
-      int n = 0;
-      if (b0 + lane < B) {
-        Kv8Seq s;
-        kv8_seq(c, a.cu, a.kv_len, a.N, a.max_new, b0 + lane, blockIdx.x == 0, s);
-        int begin, end;
-        seq_blocks(s, a.window, begin, end);
-        n = end - begin;
-      }
-      int x = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (b0 + lane < B) prefix[b0 + lane] = sum + x - n;
-      sum += __shfl_sync(0xffffffffu, x, 31);
+  if (threadIdx.x == 0) flags[0] = 0;
+  int carry = 0;
+  for (int b0 = 0; b0 < B; b0 += C::THREADS) {
+    const int b = b0 + threadIdx.x;
+    int n = 0;
+    if (b < B) {
+      Kv8Seq s;
+      kv8_seq(c, a.cu, a.kv_len, a.N, a.max_new, b, blockIdx.x == 0, s);
+      int begin, end;
+      seq_blocks(s, a.window, begin, end);
+      n = end - begin;
     }
-    if (lane == 0) prefix[B] = sum;
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) flags[16 + warp] = x;
+    __syncthreads();
+    int before = carry;
+#pragma unroll
+    for (int w = 0; w < C::WARPS; ++w) {
+      const int y = flags[16 + w];
+      if (w < warp) before += y;
+      carry += y;
+    }
+    if (b < B) prefix[b] = before + x - n;
+    __syncthreads();
   }
-  __syncthreads();
   const int per_seq = c.Hkv * a.groups;  // tasks of a sequence
-  const long long total = static_cast<long long>(prefix[B]) * per_seq;
+  const long long total = static_cast<long long>(carry) * per_seq;
   const long long parts = min(total, static_cast<long long>(gridDim.x));  // CTAs with work: each has a block at least
   if (blockIdx.x >= parts) return;
   const long long u0 = total * blockIdx.x / parts, u1 = total * (blockIdx.x + 1) / parts;
   volatile int* stop = flags;
 
-  // Walks the CTA's run task by task: [t0, t1) of the task's blocks are ours.
+  // A task of the CTA's run: [t0, t1) of its blocks are ours.
   struct Task {
     int b, h, grp, begin, blocks, t0, t1;
     Kv8Seq s;
   };
   auto task_at = [&](long long u, Task& k) {
-    const long long want = u / per_seq;  // the sequence holding unit u: prefix[b] <= u / per_seq < prefix[b + 1]
+    const long long want = u / per_seq;  // the sequence holding unit u: prefix[b] <= want < prefix[b + 1]
     int lo = 0, hi = B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -163,51 +178,66 @@ __global__ void __launch_bounds__(Cfg<NB, NG>::THREADS, 1) kv8_attn_kernel(const
     int end;
     seq_blocks(k.s, a.window, k.begin, end);
     k.blocks = end - k.begin;
-    const long long rel = u - static_cast<long long>(prefix[lo]) * per_seq;
-    const int task = static_cast<int>(rel / k.blocks);
+    const int rel = static_cast<int>(u - static_cast<long long>(prefix[lo]) * per_seq);
+    const int task = rel / k.blocks;
     k.h = task / a.groups;
     k.grp = task - k.h * a.groups;
-    k.t0 = static_cast<int>(rel - static_cast<long long>(task) * k.blocks);
+    k.t0 = rel - task * k.blocks;
     k.t1 = static_cast<int>(min(static_cast<long long>(k.blocks), k.t0 + (u1 - u)));
   };
 
-  if (warp == C::WARPS) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int n = 0;
-      bool ok = true;
-      for (long long u = u0; ok && u < u1;) {
-        Task k;
-        task_at(u, k);
-        const size_t bh = static_cast<size_t>(k.b) * c.Hkv + k.h;
-        for (int t = k.t0; ok && t < k.t1; ++t) {
-          const int blk = k.begin + t;
-          if ((blk + 1) * KV8_BLOCK > k.s.len) continue;  // the tail is read where it lies
-          const int st = n % a.stages;
-          const uint8_t* page = kv8_page(c, bh, blk);
-          if (n >= a.stages) ok = ring_wait(empty + st, (n / a.stages - 1) & 1, c.err + k.b, stop);
-          if (!ok) break;
-          mbar_arrive_expect_tx(full + st, KV8_COPY);
-          bulk_g2s(ring + st * HQ_KV8_PAGE_BYTES, page, KV8_COPY, full + st);
-          ++n;
-        }
-        u += k.t1 - k.t0;
-      }
-      // no copy may be in flight when the CTA's shared memory is given up; the
-      // consumers have waited for all of them unless they stopped early
-      if (*stop) {
-        int never = 0;
-        for (int i = max(0, n - a.stages); i < n; ++i) ring_wait(full + i % a.stages, (i / a.stages) & 1, c.err, &never);
-      }
-    }
-    return;
-  }
-
-  // -------------------------------------------------------------- consumers
-  const int grp4 = warp >> 2, tt = warp & 3;  // group of 4 warps; the warp's 16 tokens of a block
+  const int g4 = warp >> 2, tt = warp & 3;  // group of 4 warps; the warp's 16 tokens of a block
   const int g = lane >> 2, t4 = lane & 3;
-  int n_ring = 0, turn = 0;  // pages taken from the ring, blocks seen: by all groups together
+
+  // ------------------------------------------------------------ the warp's copies, SLOTS ahead
+  // Blocks t = first, first + NG, .. of each task go to this group; the first
+  // rotates with the task's number within the run.
+  uint8_t* ring = rings + warp * SLOTS * SLOT;
+  struct Cursor {
+    long long u;              // units before the next task
+    int t, end, b, ordinal;   // next block of the task (relative to its begin), end of the complete ones
+    int batch, looked;        // pages of blocks batch, batch + NG, ..: lane i holds that of batch + i NG
+    uint64_t page;
+    size_t bh;
+    int begin;
+  } cur = {u0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+  auto first_of = [&](int t0, int ordinal) { return t0 + (g4 + ordinal) % NG; };
+  auto issue = [&](int slot) {  // the next block's slice into the slot; false at the end of the run
+    while (cur.t >= cur.end) {
+      if (cur.u >= u1) return false;
+      Task k;
+      task_at(cur.u, k);
+      cur.u += k.t1 - k.t0;
+      cur.t = first_of(k.t0, cur.ordinal++);
+      cur.end = min(k.t1, k.s.len / KV8_BLOCK - k.begin);  // the incomplete block is read where it lies
+      cur.b = k.b;
+      cur.bh = static_cast<size_t>(k.b) * c.Hkv + k.h;
+      cur.begin = k.begin;
+      cur.looked = 0;
+    }
+    if (cur.looked == 0 || cur.t >= cur.batch + 32 * NG) {
+      cur.batch = cur.t;
+      cur.looked = 1;
+      const int t = cur.t + lane * NG;
+      cur.page = t < cur.end ? reinterpret_cast<uint64_t>(kv8_page(c, cur.bh, cur.begin + t)) : 0;
+    }
+    const uint8_t* page = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, cur.page, (cur.t - cur.batch) / NG));
+    cur.t += NG;
+    if (lane == 0) {
+      uint8_t* dst = ring + slot * SLOT;
+      mbar_arrive_expect_tx(full + slot, SLOT);
+      bulk_g2s(dst, page + tt * SLICE, SLICE, full + slot);
+      bulk_g2s(dst + SLICE, page + HQ_KV8_V + tt * SLICE, SLICE, full + slot);
+      bulk_g2s(dst + 2 * SLICE, page + HQ_KV8_KSCALE, 16, full + slot);
+    }
+    return true;
+  };
+  int issued = 0;
+  while (issued < SLOTS && issue(issued)) ++issued;
+  int slot = 0, phase = 0, taken = 0;
   bool ok = true;
+
+  int ordinal = 0;
   for (long long u = u0; u < u1;) {
     Task k;
     task_at(u, k);
@@ -219,7 +249,8 @@ __global__ void __launch_bounds__(Cfg<NB, NG>::THREADS, 1) kv8_attn_kernel(const
     // 16-byte chunk t4 of half j gives at that step
     uint32_t qf[NB][16];
     float qs[NB][2];   // multiplier of the scores of rows 2 t4, 2 t4 + 1
-    int qp[NB][2];     // their positions, -1: no such row
+    int qp[NB][2];     // their positions (rows past the last: where they see all)
+    float m_run[NB][2], e_run[NB][2], l_run[NB][2], ef[NB][2];  // ef = 2^(m - E + P_BIAS)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int r = row0 + 8 * nb + g;
@@ -258,25 +289,30 @@ __global__ void __launch_bounds__(Cfg<NB, NG>::THREADS, 1) kv8_attn_kernel(const
       for (int i = 0; i < 2; ++i) {
         qs[nb][i] = __shfl_sync(0xffffffffu, mul, (2 * t4 + i) * 4) * a.scale;
         const int rr = row0 + 8 * nb + 2 * t4 + i;
-        qp[nb][i] = rr < rows ? k.s.first + rr / a.G : -1;
+        // rows past the last have zero queries: their reference starts at their
+        // score, 0, and no tile of theirs is ever masked or out of range
+        qp[nb][i] = rr < rows ? k.s.first + rr / a.G : INT_MAX;
+        m_run[nb][i] = rr < rows ? -INFINITY : 0.f;
+        e_run[nb][i] = -INFINITY;
+        l_run[nb][i] = ef[nb][i] = 0.f;
       }
     }
+    // positions of the task's first and last real rows
+    const int q_lo = k.s.first + row0 / a.G, q_hi = k.s.first + (min(row0 + R, rows) - 1) / a.G;
 
     float o[NB][8][4];
-    float m_run[NB][2], e_run[NB][2], l_run[NB][2];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[nb][mt][i] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) m_run[nb][i] = e_run[nb][i] = -INFINITY, l_run[nb][i] = 0.f;
-    }
 
     // one 16-token tile: kf, vf give the A operands of step s / output rows 16 mt
-    // .. 16 mt + 15; ks, vs the scales of tokens g, g + 8; pos the first token's position
-    auto tile = [&](auto kf, auto vf, const float (&ks)[2], const float (&vs)[2], float vtop, int pos) {
+    // .. 16 mt + 15; ks, vs the scales of tokens g, g + 8 (vtop: the largest vs of
+    // the tile); pos the first token's position
+    auto tile = [&](auto masked, auto kf, auto vf, const float (&ks)[2], const float (&vs)[2], float vtop, int pos) {
+      constexpr bool MASK = decltype(masked)::value;
       float sc[NB][4];
       {
         float s2[NB][4];
@@ -294,51 +330,69 @@ __global__ void __launch_bounds__(Cfg<NB, NG>::THREADS, 1) kv8_attn_kernel(const
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[nb][i] += s2[nb][i];
+          for (int i = 0; i < 4; ++i) sc[nb][i] = (sc[nb][i] + s2[nb][i]) * (qs[nb][i & 1] * ks[i >> 1]);
       }
-      const float lv = log2_acc(vtop);
+      if (MASK) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // how far the token lies behind the query
+            const int d = qp[nb][i & 1] - (pos + g + 8 * (i >> 1));
+            if (d < 0 || (a.window > 0 && d >= a.window && qp[nb][i & 1] != INT_MAX)) sc[nb][i] = -INFINITY;
+          }
+      }
+      bool far = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) far |= sc[nb][i] - m_run[nb][i & 1] > P_SLACK;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) far |= fmaxf(ef[nb][0], ef[nb][1]) * vtop > V_LIMIT;
+      if (__any_sync(0xffffffffu, far)) {
+        const float lv = log2f(vtop);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float ao[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float mt = fmaxf(sc[nb][i], sc[nb][2 + i]);
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+            const float m_new = fmaxf(m_run[nb][i], mt), e_new = fmaxf(e_run[nb][i], mt + lv);
+            const float mb = m_new == -INFINITY ? 0.f : m_new, eb = e_new == -INFINITY ? 0.f : e_new;
+            l_run[nb][i] *= ex2(m_run[nb][i] - mb);
+            ao[i] = ex2(e_run[nb][i] - eb);
+            m_run[nb][i] = m_new;
+            e_run[nb][i] = e_new;
+            // bounded, so that a weight that underflowed stays 0 beside a far larger earlier score
+            ef[nb][i] = e_new == -INFINITY ? 0.f : ex2(fminf(mb - eb + P_BIAS, 100.f));
+          }
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[nb][mt][i] *= ao[i & 1];
+        }
+      }
       uint32_t pf[NB][2];
-      bool moved = false;
-      float ao[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         float p[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {  // rows 2 t4 + i
-          const float mul = qs[nb][i];
-          const int d0 = qp[nb][i] - (pos + g), d1 = d0 - 8;  // how far the tokens lie behind the query
-          const bool in0 = d0 >= 0 && (a.window <= 0 || d0 < a.window), in1 = d1 >= 0 && (a.window <= 0 || d1 < a.window);
-          const float s0 = in0 ? sc[nb][i] * (mul * ks[0]) : -INFINITY;
-          const float s1 = in1 ? sc[nb][2 + i] * (mul * ks[1]) : -INFINITY;
-          float mt = fmaxf(s0, s1);
-          mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
-          mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
-          mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-          const float m_new = fmaxf(m_run[nb][i], mt), e_new = fmaxf(e_run[nb][i], mt + lv);
-          const float mb = m_new == -INFINITY ? 0.f : m_new, eb = e_new == -INFINITY ? 0.f : e_new;
-          const float al = ex2(m_run[nb][i] - mb);
-          ao[nb][i] = ex2(e_run[nb][i] - eb);
-          moved |= e_new > e_run[nb][i];
-          m_run[nb][i] = m_new;
-          e_run[nb][i] = e_new;
-          const float p0 = ex2(s0 - mb), p1 = ex2(s1 - mb);
-          l_run[nb][i] = l_run[nb][i] * al + (p0 + p1);
-          // p * vscale at 2^14 / 2^E; the exponent is bounded so that a weight that
-          // underflowed to 0 stays 0 beside a far larger earlier score
-          const float f = ex2(fminf(mb - eb + P_BIAS + lv, 100.f));
-          p[i] = in0 ? p0 * (f * vs[0]) : 0.f;
-          p[2 + i] = in1 ? p1 * (f * vs[1]) : 0.f;
+        for (int i = 0; i < 4; ++i) {
+          p[i] = ex2(sc[nb][i] - m_run[nb][i & 1]);
+          if (MASK && sc[nb][i] == -INFINITY) p[i] = 0.f;  // also while m is -inf
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) l_run[nb][i] += p[i] + p[2 + i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[i] *= ef[nb][i & 1] * vs[i >> 1];
+          if (MASK && sc[nb][i] == -INFINITY) p[i] = 0.f;  // a scale that is NaN stays behind the mask
         }
         pf[nb][0] = movmatrix_t(pack_f16x2(p[0], p[1]));
         pf[nb][1] = movmatrix_t(pack_f16x2(p[2], p[3]));
-      }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[nb][mt][i] *= ao[nb][i & 1];
       }
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) {
@@ -349,80 +403,79 @@ __global__ void __launch_bounds__(Cfg<NB, NG>::THREADS, 1) kv8_attn_kernel(const
       }
     };
 
-    for (int t = k.t0; t < k.t1; ++t) {
-      const int blk = k.begin + t, p0 = blk * KV8_BLOCK;
-      const bool mine = turn % NG == grp4;
-      ++turn;
+    for (int t = first_of(k.t0, ordinal); t < k.t1; t += NG) {
+      const int p0 = (k.begin + t) * KV8_BLOCK, pos = p0 + tt * 16;
       if (p0 + KV8_BLOCK <= k.s.len) {
-        const int st = n_ring % a.stages, ph = (n_ring / a.stages) & 1;
-        ++n_ring;
-        if (!mine || !ok) continue;
-        ok = ring_wait(full + st, ph, c.err + k.b, stop);
+        ok = ok && ring_wait(full + slot, phase, c.err + k.b, stop);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) continue;
-        const uint8_t* page = ring + st * HQ_KV8_PAGE_BYTES;
-        const float2 sc = *reinterpret_cast<const float2*>(page + HQ_KV8_KSCALE);
+        if (!ok) break;
+        const uint8_t* src = ring + slot * SLOT;
         uint4 kw[4], vw[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) kw[i] = reinterpret_cast<const uint4*>(page + tt * 2048 + i * 512)[lane];
+        for (int i = 0; i < 4; ++i) kw[i] = reinterpret_cast<const uint4*>(src + i * 512)[lane];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vw[i] = reinterpret_cast<const uint4*>(page + HQ_KV8_V + tt * 2048 + i * 512)[lane];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty + st);
+        for (int i = 0; i < 4; ++i) vw[i] = reinterpret_cast<const uint4*>(src + SLICE + i * 512)[lane];
+        const float2 sc = *reinterpret_cast<const float2*>(src + 2 * SLICE);
+        __syncwarp();  // every lane has its part: the slot takes the next slice
+        ++taken;
+        if (issue(slot)) ++issued;
+        if (++slot == SLOTS) slot = 0, phase ^= 1;
         auto word = [](const uint4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; };
-        const float ks[2] = {sc.x, sc.x}, one[2] = {1.f, 1.f};
-        tile(
-            [&](int s, uint32_t (&f)[4]) {
-              // chunk (token half a, d half j) = 2 a + j; word s % 4 of it
-              kv8_half4<FMT>(word(kw[s >> 2], s & 3), f[0], f[2]);
-              kv8_half4<FMT>(word(kw[2 + (s >> 2)], s & 3), f[1], f[3]);
-            },
-            [&](int mt, uint32_t (&f)[4]) {
-              kv8_half4<FMT>(word(vw[mt >> 1], (mt & 1) * 2), f[0], f[2]);
-              kv8_half4<FMT>(word(vw[mt >> 1], (mt & 1) * 2 + 1), f[1], f[3]);
-            },
-            ks, one, sc.y, p0 + tt * 16);
-      } else {
+        auto kf = [&](int s, uint32_t (&f)[4]) {
+          // chunk (token half a, d half j) = 2 a + j; word s % 4 of it
+          kv8_half4<FMT>(word(kw[s >> 2], s & 3), f[0], f[2]);
+          kv8_half4<FMT>(word(kw[2 + (s >> 2)], s & 3), f[1], f[3]);
+        };
+        auto vf = [&](int mt, uint32_t (&f)[4]) {
+          kv8_half4<FMT>(word(vw[mt >> 1], (mt & 1) * 2), f[0], f[2]);
+          kv8_half4<FMT>(word(vw[mt >> 1], (mt & 1) * 2 + 1), f[1], f[3]);
+        };
+        const float ks[2] = {sc.x, sc.x}, vs[2] = {sc.y, sc.y};
+        // seen whole by every row?
+        if (pos + 15 <= q_lo && (a.window <= 0 || pos > q_hi - a.window))
+          tile(std::false_type{}, kf, vf, ks, vs, sc.y, pos);
+        else
+          tile(std::true_type{}, kf, vf, ks, vs, sc.y, pos);
+      } else if (pos < k.s.len) {
         // the incomplete block, in 16 bits: rows past the length hold finite
         // values of earlier blocks or zeros and are masked
-        if (!mine || p0 + tt * 16 >= k.s.len) continue;
-        const int half = blk & 1;
+        const int half = (k.begin + t) & 1;
         const uint4* tk = reinterpret_cast<const uint4*>(c.tail_k + (bh * 2 + half) * KV8_BLOCK * D + tt * 2048);
         const uint4* tv = reinterpret_cast<const uint4*>(c.tail_v + (bh * 2 + half) * KV8_BLOCK * D + tt * 2048);
         const float* ts = c.tail_scale + bh * 2 * HQ_KV8_TAIL + half * KV8_BLOCK + tt * 16 + g;
-        const bool in0 = p0 + tt * 16 + g < k.s.len, in1 = p0 + tt * 16 + g + 8 < k.s.len;
+        const bool in0 = pos + g < k.s.len, in1 = pos + g + 8 < k.s.len;
         const float ks[2] = {in0 ? ts[0] : 1.f, in1 ? ts[8] : 1.f};
-        float vs[2] = {in0 ? ts[HQ_KV8_TAIL] : 0.f, in1 ? ts[HQ_KV8_TAIL + 8] : 0.f};
+        const float vs[2] = {in0 ? ts[HQ_KV8_TAIL] : 0.f, in1 ? ts[HQ_KV8_TAIL + 8] : 0.f};
         float vtop = fmaxf(vs[0], vs[1]);  // ignores NaN
         vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 4));
         vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 8));
         vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 16));
         if (!(vtop > 0.f)) vtop = 1.f;
-        vs[0] = vs[0] / vtop;
-        vs[1] = vs[1] / vtop;
         uint32_t kw[4][8], vw[4][8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           *reinterpret_cast<uint4*>(&kw[i][0]) = tk[(i * 32 + lane) * 2];
           *reinterpret_cast<uint4*>(&kw[i][4]) = tk[(i * 32 + lane) * 2 + 1];
+        }
+        auto kf = [&](int s, uint32_t (&f)[4]) {
+          f[0] = kw[s >> 2][(s & 3) * 2];
+          f[2] = kw[s >> 2][(s & 3) * 2 + 1];
+          f[1] = kw[2 + (s >> 2)][(s & 3) * 2];
+          f[3] = kw[2 + (s >> 2)][(s & 3) * 2 + 1];
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           *reinterpret_cast<uint4*>(&vw[i][0]) = tv[(i * 32 + lane) * 2];
           *reinterpret_cast<uint4*>(&vw[i][4]) = tv[(i * 32 + lane) * 2 + 1];
         }
-        tile(
-            [&](int s, uint32_t (&f)[4]) {
-              f[0] = kw[s >> 2][(s & 3) * 2];
-              f[2] = kw[s >> 2][(s & 3) * 2 + 1];
-              f[1] = kw[2 + (s >> 2)][(s & 3) * 2];
-              f[3] = kw[2 + (s >> 2)][(s & 3) * 2 + 1];
-            },
-            [&](int mt, uint32_t (&f)[4]) {
-              const int w = (mt & 1) * 4;
-              f[0] = vw[mt >> 1][w];
-              f[2] = vw[mt >> 1][w + 1];
-              f[1] = vw[mt >> 1][w + 2];
-              f[3] = vw[mt >> 1][w + 3];
-            },
-            ks, vs, vtop, p0 + tt * 16);
+        auto vf = [&](int mt, uint32_t (&f)[4]) {
+          const int w = (mt & 1) * 4;
+          f[0] = vw[mt >> 1][w];
+          f[2] = vw[mt >> 1][w + 1];
+          f[1] = vw[mt >> 1][w + 2];
+          f[3] = vw[mt >> 1][w + 3];
+        };
+        tile(std::true_type{}, kf, vf, ks, vs, vtop, pos);
       }
     }
 
@@ -437,110 +490,92 @@ __global__ void __launch_bounds__(Cfg<NB, NG>::THREADS, 1) kv8_attn_kernel(const
         l += __shfl_xor_sync(0xffffffffu, l, 16);
         if (g == 0) red[warp * R + 8 * nb + 2 * t4 + i] = make_float4(m_run[nb][i], e_run[nb][i], l, 0.f);
       }
-    asm volatile("bar.sync 1, %0;" ::"n"(CT) : "memory");
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 8 * nb + 2 * t4 + i;
-        float e = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) e = fmaxf(e, red[w * R + r].y);
-        const float f = e == -INFINITY ? 1.f : ex2(e_run[nb][i] - e);
-#pragma unroll
-        for (int mt = 0; mt < 8; ++mt) {
-          obuf[(warp * R + r) * OS + mt * 16 + g] = o[nb][mt][i] * f;
-          obuf[(warp * R + r) * OS + mt * 16 + g + 8] = o[nb][mt][2 + i] * f;
-        }
-      }
-    // this thread's outputs: rows warp, warp + WARPS, .., elements 4 lane .. 4 lane + 3
-    constexpr int RPW = (R + C::WARPS - 1) / C::WARPS;
-    float rm[RPW], re[RPW], rl[RPW];
-#pragma unroll
-    for (int i = 0; i < RPW; ++i) {
-      const int r = warp + i * C::WARPS;
-      rm[i] = re[i] = -INFINITY;
-      rl[i] = 0.f;
-      if (r < R) {
-#pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) {
-          const float4 x = red[w * R + r];
-          rm[i] = fmaxf(rm[i], x.x);
-          re[i] = fmaxf(re[i], x.y);
-        }
-        const float mb = rm[i] == -INFINITY ? 0.f : rm[i];
-#pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) {
-          const float4 x = red[w * R + r];
-          rl[i] += x.z * ex2(x.x - mb);
-        }
-      }
-    }
-    asm volatile("bar.sync 1, %0;" ::"n"(CT) : "memory");
-    float4 acc[RPW];
-#pragma unroll
-    for (int i = 0; i < RPW; ++i) {
-      const int r = warp + i * C::WARPS;
-      acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < R) {
-#pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) {
-          const float4 x = *reinterpret_cast<const float4*>(obuf + (w * R + r) * OS + 4 * lane);
-          acc[i].x += x.x;
-          acc[i].y += x.y;
-          acc[i].z += x.z;
-          acc[i].w += x.w;
-        }
-      }
-    }
+    const bool whole = k.t1 - k.t0 == k.blocks;
+    // Pieces of a task that CTAs share lie in the workspace, slot 2 cta (+ 1 for
+    // the task's first piece): the two pieces a CTA may deliver do not meet.  The
+    // task's pieces come from CTAs c0 .. c1 and are counted by c0's counter: one
+    // task at most begins in a CTA without ending there.
+    constexpr int PART = R * (D + 4);
+    float* part = a.parts + static_cast<size_t>(2 * blockIdx.x + (k.t0 == 0)) * PART;
     auto finish = [&](int r, float m, float e, float l, float4 x) {
       const int rr = row0 + r;
       if (rr >= rows) return;
-      // weights are at 2^(14 - E) * 2^s, the sum at 2^-m: the quotient's exponent
+      // accumulators are at 2^(P_BIAS - E), the sum at 2^-m: the quotient's exponent
       const float f = m == -INFINITY ? 0.f : ex2(e - m - P_BIAS) / l;
       const int64_t tok = k.s.row0 + rr / a.G;
       const int head = k.h * a.G + rr % a.G;
       E y[4] = {from_float<E>(x.x * f), from_float<E>(x.y * f), from_float<E>(x.z * f), from_float<E>(x.w * f)};
       *reinterpret_cast<uint2*>(static_cast<E*>(a.out) + tok * a.o_tok + head * a.o_head + 4 * lane) =
           *reinterpret_cast<const uint2*>(y);
-      if (a.lse != nullptr && lane == 0) a.lse[tok * a.Hq + head] = m + log2_acc(l);
+      if (a.lse != nullptr && lane == 0) a.lse[tok * a.Hq + head] = m + log2f(l);
     };
-    if (k.t1 - k.t0 == k.blocks) {
 #pragma unroll
-      for (int i = 0; i < RPW; ++i)
-        if (warp + i * C::WARPS < R) finish(warp + i * C::WARPS, rm[i], re[i], rl[i], acc[i]);
-    } else {
-      // Piece to the workspace: slot 2 cta (+ 1 for the task's first piece), so
-      // that the two pieces a CTA may deliver do not meet.  The task's pieces lie
-      // in CTAs c0 .. c1; its counter is that of c0, where only one task can
-      // begin without ending.
-      const long long k0 = u - k.t0, k1 = k0 + k.blocks;  // the task's units
-      const int c0 = static_cast<int>(((k0 + 1) * parts - 1) / total), c1 = static_cast<int>((k1 * parts - 1) / total);
-      constexpr int PART = R * (D + 4);
-      float* part = a.parts + static_cast<size_t>(2 * blockIdx.x + (k.t0 == 0)) * PART;
+    for (int nb = 0; nb < NB; ++nb) {
+      __syncthreads();  // red is there; the buffer's earlier readers are done
 #pragma unroll
-      for (int i = 0; i < RPW; ++i) {
-        const int r = warp + i * C::WARPS;
-        if (r < R) {
-          reinterpret_cast<float4*>(part + r * D)[lane] = acc[i];
-          if (lane == 0) reinterpret_cast<float4*>(part + R * D)[r] = make_float4(rm[i], re[i], rl[i], 0.f);
+      for (int i = 0; i < 2; ++i) {
+        const int r = 2 * t4 + i;
+        float e = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) e = fmaxf(e, red[w * R + 8 * nb + r].y);
+        const float f = e == -INFINITY ? 1.f : ex2(e_run[nb][i] - e);
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          obuf[(warp * 8 + r) * OS + mt * 16 + g] = o[nb][mt][i] * f;
+          obuf[(warp * 8 + r) * OS + mt * 16 + g + 8] = o[nb][mt][2 + i] * f;
         }
       }
+      // row 8 nb + warp of the first 8 warps: elements 4 lane .. 4 lane + 3
+      float m = -INFINITY, e = -INFINITY, l = 0.f;
+      if (warp < 8) {
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) {
+          const float4 x = red[w * R + 8 * nb + warp];
+          m = fmaxf(m, x.x);
+          e = fmaxf(e, x.y);
+        }
+        const float mb = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) {
+          const float4 x = red[w * R + 8 * nb + warp];
+          l += x.z * ex2(x.x - mb);
+        }
+      }
+      __syncthreads();
+      if (warp < 8) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) {
+          const float4 x = *reinterpret_cast<const float4*>(obuf + (w * 8 + warp) * OS + 4 * lane);
+          s.x += x.x;
+          s.y += x.y;
+          s.z += x.z;
+          s.w += x.w;
+        }
+        const int r = 8 * nb + warp;
+        if (whole) {
+          finish(r, m, e, l, s);
+        } else {
+          reinterpret_cast<float4*>(part + r * D)[lane] = s;
+          if (lane == 0) reinterpret_cast<float4*>(part + R * D)[r] = make_float4(m, e, l, 0.f);
+        }
+      }
+    }
+    if (!whole) {
+      const long long k0 = u - k.t0, k1 = k0 + k.blocks;  // the task's units
+      const int c0 = static_cast<int>(((k0 + 1) * parts - 1) / total), c1 = static_cast<int>((k1 * parts - 1) / total);
       __threadfence();
-      asm volatile("bar.sync 1, %0;" ::"n"(CT) : "memory");
+      __syncthreads();
       if (threadIdx.x == 0) {
         const unsigned int before = atom_add_acq_rel_gpu(a.counters + c0, 1u);
         const bool last = before == static_cast<unsigned int>(c1 - c0);
         if (last) a.counters[c0] = 0u;
         flags[1] = last;
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(CT) : "memory");
+      __syncthreads();
       if (flags[1]) {
         fence_acq_rel_gpu();
-#pragma unroll
-        for (int i = 0; i < RPW; ++i) {
-          const int r = warp + i * C::WARPS;
-          if (r >= R) continue;
+        for (int r = warp; r < R; r += C::WARPS) {
           float m = -INFINITY, e = -INFINITY, l = 0.f;
           for (int p = c0; p <= c1; ++p) {
             const float* q = a.parts + static_cast<size_t>(2 * p + (p == c0)) * PART;
@@ -565,42 +600,47 @@ __global__ void __launch_bounds__(Cfg<NB, NG>::THREADS, 1) kv8_attn_kernel(const
         }
       }
     }
+    ++ordinal;
     u += k.t1 - k.t0;
+  }
+  // copies that were not waited for (after a wait that gave up) land before the
+  // CTA gives its shared memory back
+  if (!ok && lane == 0) {
+    int never = 0;
+    for (; taken < issued; ++taken) ring_wait(full + taken % SLOTS, (taken / SLOTS) & 1, c.err, &never);
   }
 }
 
 constexpr int SMEM_MAX = 227 * 1024;
 
-template <int NB, int NG>
-int stage_count(int B) {
-  using C = Cfg<NB, NG>;
-  const int left = SMEM_MAX - C::FIXED - ((B + 1) * 4 + 127) / 128 * 128;
-  const int n = left / HQ_KV8_PAGE_BYTES;
-  return n < C::STAGE_MAX ? n : C::STAGE_MAX;
-}
-
-template <class E, int FMT, int NB, int NG>
+template <class E, int FMT, int NB>
 hq_status launch(AttnArgs& a, int sms, cudaStream_t st) {
-  using C = Cfg<NB, NG>;
+  using C = Cfg<NB>;
+  static_assert(C::FIXED + (HQ_KV8_MAX_BATCH + 1) * 4 <= SMEM_MAX, "shared memory of the largest batch");
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "kv8 attention setup");
   static DeviceOnce attrs;
   e = attrs.run(dev, [] {
-    return cudaFuncSetAttribute(kv8_attn_kernel<E, FMT, NB, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
+    return cudaFuncSetAttribute(kv8_attn_kernel<E, FMT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
   });
   if (e != cudaSuccess) return cuda_fail(e, "kv8 attention setup");
-  a.stages = stage_count<NB, NG>(a.c.B);
   a.groups = (a.G * a.max_new + C::R - 1) / C::R;
-  const size_t smem = C::FIXED + ((a.c.B + 1) * 4 + 127) / 128 * 128 + static_cast<size_t>(a.stages) * HQ_KV8_PAGE_BYTES;
-  kv8_attn_kernel<E, FMT, NB, NG><<<sms, C::THREADS, smem, st>>>(a);
+  kv8_attn_kernel<E, FMT, NB><<<sms, C::THREADS, C::FIXED + (a.c.B + 1) * 4, st>>>(a);
   return cuda_status(cudaGetLastError(), "kv8 attention launch");
 }
 
+// Rows of a task, in eights: as many as there are, up to 4; beyond that tasks of 32 rows.
+int row_eights(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }
+
 template <class E, int FMT>
 hq_status launch_f(AttnArgs& a, int sms, cudaStream_t st) {
-  if (a.G * static_cast<int64_t>(a.max_new) <= 8) return launch<E, FMT, 1, 2>(a, sms, st);
-  return launch<E, FMT, 2, 2>(a, sms, st);
+  switch (row_eights(a.G * a.max_new)) {
+    case 1: return launch<E, FMT, 1>(a, sms, st);
+    case 2: return launch<E, FMT, 2>(a, sms, st);
+    case 3: return launch<E, FMT, 3>(a, sms, st);
+    default: return launch<E, FMT, 4>(a, sms, st);
+  }
 }
 
 size_t counters_bytes(int sms) { return (static_cast<size_t>(sms) * 4 + 255) / 256 * 256; }
@@ -616,7 +656,7 @@ hq_status device_sms(int* sms) {
 }
 
 size_t attn_workspace(int rows, int sms) {
-  const int R = rows <= 8 ? 8 : 16;
+  const int R = 8 * row_eights(rows);
   return counters_bytes(sms) + static_cast<size_t>(2) * sms * R * (D + 4) * sizeof(float);
 }
 

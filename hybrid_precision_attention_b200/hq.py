@@ -429,42 +429,50 @@ def hq_prefill_attn(q, k, v, vl_pos, n_vl: int, W: int, sm_scale: float = None, 
 # ----------------------------------------------------------------------------- rotary positions, 8-bit block cache
 
 class _On:
-    """The launch stream of a call (default: the current one of the tensors' device),
-    made current with its device, so that what the call allocates belongs to it."""
+    """Makes a call's launch stream current with its device, so that what the call allocates belongs to it
+    (stream None: the device's current stream)."""
 
-    def __init__(self, device, stream):
-        self.enter = None
+    def __init__(self, index, stream=None):
         if stream is None:
-            if device.index is not None and device.index != torch.cuda.current_device():
-                self.enter = torch.cuda.device(device)
-                self.enter.__enter__()
-            self.ptr = torch.cuda.current_stream(device).cuda_stream
+            self.ctx = torch.cuda.device(index)
         else:
-            if stream.device != device:
-                raise HqError(f"stream of {stream.device} for tensors on {device}")
-            self.enter = torch.cuda.stream(stream)
-            self.enter.__enter__()
-            self.ptr = stream.cuda_stream
+            if stream.device.index != index:
+                raise HqError(f"stream of {stream.device} for tensors on cuda:{index}")
+            self.ctx = torch.cuda.stream(stream)
 
     def __enter__(self):
-        return self.ptr
+        self.ctx.__enter__()
 
     def __exit__(self, *exc):
-        if self.enter is not None:
-            self.enter.__exit__(*exc)
+        self.ctx.__exit__(*exc)
 
 
-def _rows(t, device, shape, name, dtypes=(torch.float16, torch.bfloat16)):
-    """A CUDA tensor of that shape (None: any size), its last dimension contiguous."""
-    if t.device != device or t.dtype not in dtypes or t.dim() != len(shape) or t.stride(-1) != 1 and t.shape[-1] > 1 or \
-            any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise HqError(f"{name}: expected {'/'.join(str(d) for d in dtypes)} {tuple(shape)} on {device} with contiguous "
-                      f"rows, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+# The current device and its current stream's handle, without the Device and
+# Stream objects of the torch.cuda functions (2 us and more of a small call).
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_HALVES = (torch.float16, torch.bfloat16)
+_ALL = tuple(_DTYPE)
 
 
-def _ints(t, device, shape, name):
-    if t.device != device or t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
-        raise HqError(f"{name}: expected contiguous {torch.int32} {shape} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+def _rows(t, index, shape, name, dtypes=_HALVES):
+    """A tensor of that shape (None: any size) on that CUDA device, its last dimension contiguous."""
+    have = t.shape
+    ok = len(have) == len(shape) and t.dtype in dtypes and t.is_cuda and t.get_device() == index and \
+        (t.stride(-1) == 1 or have[-1] <= 1)
+    if ok:
+        for n, m in zip(shape, have):
+            if n != m and n is not None:
+                ok = False
+    if not ok:
+        raise HqError(f"{name}: expected {'/'.join(str(d) for d in dtypes)} {tuple(shape)} on cuda:{index} with contiguous "
+                      f"rows, got {t.dtype} {tuple(have)} strides {t.stride()} on {t.device}")
+
+
+def _ints(t, index, shape, name):
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda or t.get_device() != index:
+        raise HqError(f"{name}: expected contiguous {torch.int32} {tuple(shape)} on cuda:{index}, got {t.dtype} "
+                      f"{tuple(t.shape)} on {t.device}")
 
 
 class RopeTable:
@@ -477,38 +485,53 @@ class RopeTable:
         _check(_lib.hq_rope_freqs(rot, base, kind, factor, orig_len, low, high, f.ctypes.data, ctypes.byref(amp)), "hq_rope_freqs")
         self.rot, self.amp = rot, amp.value
         self.freqs = torch.from_numpy(f.view(np.int64)).to(device)
+        self.index = self.freqs.get_device()
+        self._ptr = self.freqs.data_ptr()
 
 
 def hq_rope(q, k, pos, table: RopeTable, layout: int = ROPE_HALF, grad: bool = False, q_out=None, k_out=None, stream=None):
     """Rotary positions of q [B, T, Hq, D] and k [B, T, Hkv, D] (or None) at pos int32 [B, T]; without a batch
     dimension [T, H, D] and [T].  Strided views are taken as they are; q_out, k_out may be q, k themselves.
     ``grad``: the transposed rotation (gradients of q and k from those of the outputs).  Returns (q_out, k_out)."""
-    dev = table.freqs.device
-    n = q.dim()
-    if n not in (3, 4):
-        raise HqError(f"q: expected [B, T, H, D] or [T, H, D], got {tuple(q.shape)}")
-    lead, D = tuple(q.shape[:-2]), q.shape[-1]
-    B, T = lead if n == 4 else (1,) + lead
+    dev = table.index
+    if dev < 0:
+        raise HqError("hq_rope: the table is not on a CUDA device")
+    if stream is not None or _device() != dev:
+        with _On(dev, stream):
+            return hq_rope(q, k, pos, table, layout, grad, q_out, k_out)
+    shape = q.shape
+    n = len(shape)
+    if n != 4 and n != 3:
+        raise HqError(f"q: expected [B, T, H, D] or [T, H, D], got {tuple(shape)}")
+    lead, D = shape[:-2], shape[-1]
     _ints(pos, dev, lead, "pos")
-    with _On(dev, stream) as s:
-        sides = []
-        for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-            if x is None:
-                sides.append((None, None))
-                continue
-            _rows(x, dev, lead + (None, D), name, (q.dtype,) if q.dtype in _DTYPE else tuple(_DTYPE))
-            if y is None:
-                y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-            else:
-                _rows(y, dev, tuple(x.shape), name + "_out", (q.dtype,))
-            xs, ys = x.stride(), y.stride()
-            if n == 3:
-                xs, ys = (0,) + xs, (0,) + ys
-            sides.append((y, HqRopeTensor(x.data_ptr(), y.data_ptr(), xs[0], xs[1], xs[2], ys[0], ys[1], ys[2], x.shape[-2], 0)))
-        (yq, a), (yk, b) = sides
-        _check(_lib.hq_rope(_DTYPE[q.dtype], B, T, D, table.rot, layout, 1 if grad else 0, a, b, pos.data_ptr(),
-                            table.freqs.data_ptr(), table.amp, s), "hq_rope")
-    return yq, yk
+    dt = q.dtype
+    _rows(q, dev, shape, "q", _ALL)
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    else:
+        _rows(q_out, dev, shape, "q_out", (dt,))
+    a = _rope_side(q, q_out, n)
+    b = None
+    if k is not None:
+        _rows(k, dev, (*lead, None, D), "k", (dt,))
+        if k_out is None:
+            k_out = torch.empty_like(k)
+        else:
+            _rows(k_out, dev, k.shape, "k_out", (dt,))
+        b = _rope_side(k, k_out, n)
+    st = _lib.hq_rope(_DTYPE[dt], lead[0] if n == 4 else 1, lead[-1], D, table.rot, layout, 1 if grad else 0, a, b,
+                      pos.data_ptr(), table._ptr, table.amp, _raw_stream(dev))
+    if st:
+        _check(st, "hq_rope")
+    return q_out, k_out if k is not None else None
+
+
+def _rope_side(x, y, n):
+    xs, ys = x.stride(), y.stride()
+    if n == 3:
+        return HqRopeTensor(x.data_ptr(), y.data_ptr(), 0, xs[0], xs[1], 0, ys[0], ys[1], x.shape[1], 0)
+    return HqRopeTensor(x.data_ptr(), y.data_ptr(), xs[0], xs[1], xs[2], ys[0], ys[1], ys[2], x.shape[2], 0)
 
 
 class Kv8Cache:
@@ -536,7 +559,7 @@ class Kv8Cache:
         self.pages, self.page_table = pages, page_table
         dev = pages.device
         if page_table is not None:
-            _ints(page_table, dev, (B, Hkv, self.npg), "page_table")
+            _ints(page_table, dev.index, (B, Hkv, self.npg), "page_table")
             _need(pages, torch.uint8, (pages.shape[0], KV8_PAGE_BYTES), "pages")
         else:
             _need(pages, torch.uint8, (B, Hkv, self.npg, KV8_PAGE_BYTES), "pages")
@@ -547,7 +570,7 @@ class Kv8Cache:
         _need(self.tail_v, torch.float16, (B, Hkv, 2, 64 * D), "tail_v")
         _need(self.tail_scale, torch.float32, (B, Hkv, 2, KV8_TAIL), "tail_scale")
         self.err = z((B,), torch.int32)
-        self.device = dev = self.err.device
+        self.device, self.index = self.err.device, self.err.get_device()
         self.c = HqKv8CacheStruct(B, Hkv, D, cap, fmt, pages.shape[0] if page_table is not None else 0, *[
             None if t is None else t.data_ptr() for t in (pages, page_table, self.tail_k, self.tail_v, self.tail_scale, self.err)])
         self.ref = ctypes.byref(self.c)
@@ -568,7 +591,7 @@ class Kv8Cache:
             if n == 0:
                 raise HqError(f"hq_kv8_attn: {Hq} query heads over {self.Hkv} kv heads, {max_new} new tokens")
             self._ws_bytes[(Hq, max_new)] = n
-        if torch.cuda.is_current_stream_capturing():
+        if torch._C._cuda_isCurrentStreamCapturing():
             return torch.zeros(n, dtype=torch.uint8, device=self.device)
         w = self._ws.get(stream_ptr)
         if w is None or w.numel() < n:
@@ -579,42 +602,51 @@ class Kv8Cache:
 def hq_kv8_append(cache: Kv8Cache, k, v, cu, kv_len, stream=None):
     """Append rows cu[b] .. cu[b+1]-1 of k, v [N, Hkv, D] (fp16 or bf16) to sequence b as its positions
     kv_len[b] - n_b .. kv_len[b] - 1; cu int32 [B+1], kv_len int32 [B] (new tokens included)."""
-    dev = cache.device
+    dev = cache.index
+    if stream is not None or _device() != dev:
+        with _On(dev, stream):
+            return hq_kv8_append(cache, k, v, cu, kv_len)
     _rows(k, dev, (None, cache.Hkv, cache.D), "k")
-    _rows(v, dev, tuple(k.shape), "v", (k.dtype,))
+    _rows(v, dev, k.shape, "v", (k.dtype,))
     _ints(cu, dev, (cache.B + 1,), "cu")
     _ints(kv_len, dev, (cache.B,), "kv_len")
     ks, vs = k.stride(), v.stride()
-    with _On(dev, stream) as s:
-        _check(_lib.hq_kv8_append(cache.ref, _DTYPE[k.dtype], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-                                  k.shape[0], cu.data_ptr(), kv_len.data_ptr(), s), "hq_kv8_append")
+    st = _lib.hq_kv8_append(cache.ref, _DTYPE[k.dtype], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+                            k.shape[0], cu.data_ptr(), kv_len.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "hq_kv8_append")
 
 
 def hq_kv8_read(cache: Kv8Cache, kv_len, start: int = 0, n: int = None, dtype=torch.float16, k_out=None, v_out=None,
                 zero_rest: bool = True, stream=None):
     """Positions start .. start+n-1 (default: to the capacity) of every sequence, dequantised: (k, v), each
     [B, Hkv, n, D].  Rows at or past kv_len[b] are zeroed, or with zero_rest=False left as they are."""
-    dev = cache.device
+    dev = cache.index
+    if stream is not None or _device() != dev:
+        with _On(dev, stream):
+            return hq_kv8_read(cache, kv_len, start, n, dtype, k_out, v_out, zero_rest)
     if n is None:
         n = cache.cap - start
     _ints(kv_len, dev, (cache.B,), "kv_len")
-    with _On(dev, stream) as s:
-        if (k_out is None) != (v_out is None):
-            raise HqError("hq_kv8_read: give both of k_out, v_out or neither")
-        if k_out is None:
-            if not zero_rest:
-                raise HqError("hq_kv8_read: zero_rest=False needs k_out, v_out")
-            if n < 0:
-                raise HqError(f"hq_kv8_read: {n} positions")
-            both = torch.empty((2, cache.B, cache.Hkv, n, cache.D), dtype=dtype, device=dev)
-            k_out, v_out = both[0], both[1]
-        _rows(k_out, dev, (cache.B, cache.Hkv, n, cache.D), "k_out", tuple(_DTYPE))
-        _rows(v_out, dev, tuple(k_out.shape), "v_out", (k_out.dtype,))
+    if k_out is None and v_out is None:
+        if not zero_rest:
+            raise HqError("hq_kv8_read: zero_rest=False needs k_out, v_out")
+        if n < 0 or dtype not in _DTYPE:
+            raise HqError(f"hq_kv8_read: {n} positions of {dtype}")
+        k_out = torch.empty((cache.B, cache.Hkv, n, cache.D), dtype=dtype, device=cache.device)
+        v_out = torch.empty_like(k_out)
+    elif k_out is None or v_out is None:
+        raise HqError("hq_kv8_read: give both of k_out, v_out or neither")
+    else:
+        _rows(k_out, dev, (cache.B, cache.Hkv, n, cache.D), "k_out", _ALL)
+        _rows(v_out, dev, k_out.shape, "v_out", (k_out.dtype,))
         if k_out.stride() != v_out.stride():
             raise HqError("hq_kv8_read: k_out and v_out need the same strides")
-        os_ = k_out.stride()
-        _check(_lib.hq_kv8_read(cache.ref, _DTYPE[k_out.dtype], kv_len.data_ptr(), start, n, k_out.data_ptr(),
-                                v_out.data_ptr(), os_[0], os_[1], os_[2], 1 if zero_rest else 0, s), "hq_kv8_read")
+    os_ = k_out.stride()
+    st = _lib.hq_kv8_read(cache.ref, _DTYPE[k_out.dtype], kv_len.data_ptr(), start, n, k_out.data_ptr(), v_out.data_ptr(),
+                          os_[0], os_[1], os_[2], 1 if zero_rest else 0, _raw_stream(dev))
+    if st:
+        _check(st, "hq_kv8_read")
     return k_out, v_out
 
 
@@ -623,27 +655,32 @@ def hq_kv8_attn(cache: Kv8Cache, q, cu, kv_len, max_new: int, sm_scale: float = 
     """Attention of the newest tokens (appended before): q [N, Hq, D] holds sequence b's queries as rows
     cu[b] .. cu[b+1]-1, at most max_new of them, at its last positions; causal, with window > 0 over that many
     positions.  Returns out [N, Hq, D], with return_lse (out, lse float [N, Hq], base 2)."""
-    dev = cache.device
+    dev = cache.index
+    if stream is not None or _device() != dev:
+        with _On(dev, stream):
+            return hq_kv8_attn(cache, q, cu, kv_len, max_new, sm_scale, window, out, lse, return_lse, ws)
     _rows(q, dev, (None, None, cache.D), "q")
     _ints(cu, dev, (cache.B + 1,), "cu")
     _ints(kv_len, dev, (cache.B,), "kv_len")
     N, Hq = q.shape[0], q.shape[1]
-    with _On(dev, stream) as s:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        else:
-            _rows(out, dev, tuple(q.shape), "out", (q.dtype,))
-        if lse is None and return_lse:
-            lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
-        elif lse is not None:
-            _need(lse, torch.float32, (N, Hq), "lse")
-        if ws is None:
-            ws = cache.workspace(Hq, max_new, s)
-        qs, os_ = q.stride(), out.stride()
-        _check(_lib.hq_kv8_attn(cache.ref, _DTYPE[q.dtype], q.data_ptr(), qs[0], qs[1], Hq, N, cu.data_ptr(),
-                                kv_len.data_ptr(), max_new, window, cache.D ** -0.5 if sm_scale is None else sm_scale,
-                                out.data_ptr(), os_[0], os_[1], None if lse is None else lse.data_ptr(), ws.data_ptr(),
-                                ws.numel() * ws.element_size(), s), "hq_kv8_attn")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _rows(out, dev, q.shape, "out", (q.dtype,))
+    if lse is None:
+        if return_lse:
+            lse = q.new_empty((N, Hq), dtype=torch.float32)
+    else:
+        _need(lse, torch.float32, (N, Hq), "lse")
+    s = _raw_stream(dev)
+    if ws is None:
+        ws = cache.workspace(Hq, max_new, s)
+    qs, os_ = q.stride(), out.stride()
+    st = _lib.hq_kv8_attn(cache.ref, _DTYPE[q.dtype], q.data_ptr(), qs[0], qs[1], Hq, N, cu.data_ptr(), kv_len.data_ptr(),
+                          max_new, window, cache.D ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), os_[0], os_[1],
+                          None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes, s)
+    if st:
+        _check(st, "hq_kv8_attn")
     return (out, lse) if return_lse else out
 
 
