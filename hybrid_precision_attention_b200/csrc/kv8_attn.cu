@@ -17,12 +17,12 @@
 // shuffle.  P^T comes from S^T by a register transpose (movmatrix).
 //
 // Work: the tasks (sequence, kv head, 8 NB rows) have their blocks laid end to
-// end and cut into gridDim equal runs.  A task that one CTA holds whole is
-// finished there; the pieces of the others go to the workspace and the CTA that
-// delivers a task's last piece joins them in order, so that results do not
-// depend on timing.  Within a CTA NG groups of 4 warps take every NG-th block of
-// a task, 16 tokens a warp.  Each warp keeps a ring of its own 4 KB slices in
-// flight by bulk copies (a slice is free again as soon as it is in registers, and
+// end and cut into gridDim runs, equal to a block.  A task that one CTA holds
+// whole is finished there; the pieces of the others go to the workspace and the
+// CTA that delivers a task's last piece joins them in order, so that results do
+// not depend on timing.  Short tasks are not cut.  Within a CTA NG groups of warps
+// take every NG-th block of a task, 16 or 32 tokens a warp.  Each warp keeps a
+// ring of its own slices of the pages in flight by bulk copies (a slice is free again as soon as it is in registers, and
 // no other warp is waited for) and its own running references, sums and
 // accumulators.
 //
@@ -48,23 +48,30 @@ namespace {
 constexpr float P_BIAS = 6.0f;     // log2 of the fp16 weight at both references
 constexpr float P_SLACK = 8.0f;    // how far (log2) a score may pass m
 constexpr float V_LIMIT = 128.0f;  // 2^(P_BIAS + 1): how far a value scale may pass its reference; 2^8 * 2^7 < 65504
+constexpr int TASK_UNITS = 6;      // what a task costs besides its blocks, in blocks (about 3000 cycles of 500 each)
 constexpr int OS = D + 4;          // row stride (floats) of accumulators in shared memory: 4 rows of a store step 8 banks apart
-constexpr int SLICE = 16 * D;      // bytes of one warp's 16 tokens of a page's K (or V) codes
-constexpr int SLOT = 2 * SLICE + 16;  // K slice, V slice, scales
 
-template <int NB>
+template <int NB, int W>
 struct Cfg {
-  static constexpr int R = 8 * NB;              // rows of a task
-  // 12 warps while a thread's accumulators and query operands (48 NB registers)
-  // leave room in 168 registers, else 8 warps of up to 255
-  static constexpr int NG = NB <= 2 ? 3 : 2;
-  static constexpr int WARPS = 4 * NG;
+  static constexpr int R = 8 * NB;            // rows of a task
+  // 16-token tiles of a page that a warp takes in one step: two while a
+  // thread's accumulators and query operands (48 NB registers) leave room for
+  // their codes (32 registers a tile)
+  static constexpr int MT = NB <= 2 ? 2 : 1;
+  static constexpr int WARPS = W;             // of up to 255 registers
+  static constexpr int CTAS = 8 / W;          // on an SM
   static constexpr int THREADS = WARPS * 32;
-  static constexpr int OBUF = WARPS * 8 * OS * 4;  // accumulators of 8 rows at a time
+  static constexpr int PW = 4 / MT;           // warps of a group, which share a page
+  static constexpr int NG = WARPS / PW;       // groups
+  static constexpr int SLICE = MT * 16 * D;   // bytes of a warp's part of a page's K (or V) codes
+  static constexpr int SLOT = 2 * SLICE + 16; // K slice, V slice, scales
+  static constexpr int SLOTS = MT == 2 ? 2 : 5;    // ring of a warp
+  static constexpr int OW = W < 4 ? W : 4;    // warps whose accumulators are in shared memory at a time
+  static constexpr int OBUF = OW * 8 * OS * 4;     // of 8 rows
   static constexpr int RED = WARPS * R * 16;       // (m, E, l) of each warp's rows
-  static constexpr int SLOTS = NB <= 2 ? 3 : 5;    // ring of a warp
   static constexpr int RING = WARPS * SLOTS * SLOT;
-  static constexpr int FIXED = OBUF + RED + RING + WARPS * SLOTS * 8 + 128;
+  static constexpr int AHEAD = 72;                 // a warp's copy cursor
+  static constexpr int FIXED = OBUF + RED + RING + WARPS * (SLOTS * 8 + AHEAD) + 32 * 8 + 16;
 };
 
 struct AttnArgs {
@@ -103,17 +110,19 @@ __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, int32_
   return true;
 }
 
-template <class E, int FMT, int NB>
-__global__ void __launch_bounds__(Cfg<NB>::THREADS, 1) kv8_attn_kernel(const __grid_constant__ AttnArgs a) {
-  using C = Cfg<NB>;
-  constexpr int R = C::R, NG = C::NG, SLOTS = C::SLOTS;
+template <class E, int FMT, int NB, int W>
+__global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_attn_kernel(const __grid_constant__ AttnArgs a) {
+  using C = Cfg<NB, W>;
+  constexpr int R = C::R, NG = C::NG, SLOTS = C::SLOTS, MT = C::MT, SLICE = C::SLICE, SLOT = C::SLOT;
   extern __shared__ __align__(128) uint8_t sm[];
   float* obuf = reinterpret_cast<float*>(sm);                       // [warp][row of 8][OS]
   float4* red = reinterpret_cast<float4*>(sm + C::OBUF);            // [warp][row] (m, E, l, -)
   uint8_t* rings = sm + C::OBUF + C::RED;
   uint64_t* bars = reinterpret_cast<uint64_t*>(rings + C::RING);
-  int* flags = reinterpret_cast<int*>(bars + C::WARPS * SLOTS);     // stop, last; 16.. warp totals of the plan
-  int* prefix = reinterpret_cast<int*>(sm + C::FIXED);              // blocks (per task) of the sequences before b
+  uint64_t* sums = bars + C::WARPS * SLOTS;                         // the plan's sums and maxima of each warp
+  uint8_t* ahead = reinterpret_cast<uint8_t*>(sums + 32);
+  int* flags = reinterpret_cast<int*>(ahead + C::WARPS * C::AHEAD);  // stop, last
+  uint64_t* prefix = reinterpret_cast<uint64_t*>(sm + C::FIXED);
   const int B = a.c.B;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const hq_kv8_cache& c = a.c;
@@ -124,8 +133,11 @@ __global__ void __launch_bounds__(Cfg<NB>::THREADS, 1) kv8_attn_kernel(const __g
     for (int i = 0; i < SLOTS; ++i) mbar_init(full + i, 1);
     fence_mbar_init();
   }
-  if (threadIdx.x == 0) flags[0] = 0;
-  int carry = 0;
+  if (threadIdx.x < 2) flags[threadIdx.x] = 0;
+  // prefix[b]: units (of one task) of the sequences before b, in the low half,
+  // and those of them that have blocks, in the high half
+  uint64_t carry = 0;
+  int longest = 0;
   for (int b0 = 0; b0 < B; b0 += C::THREADS) {
     const int b = b0 + threadIdx.x;
     int n = 0;
@@ -136,93 +148,186 @@ __global__ void __launch_bounds__(Cfg<NB>::THREADS, 1) kv8_attn_kernel(const __g
       seq_blocks(s, a.window, begin, end);
       n = end - begin;
     }
-    int x = n;
+    const uint64_t mine = n > 0 ? 1ull << 32 | static_cast<uint32_t>(n + TASK_UNITS) : 0ull;
+    uint64_t x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) flags[16 + warp] = x;
+    const int top = __reduce_max_sync(0xffffffffu, n);
+    if (lane == 31) {
+      sums[warp] = x;
+      sums[16 + warp] = top;
+    }
     __syncthreads();
-    int before = carry;
+    uint64_t before = carry;
 #pragma unroll
     for (int w = 0; w < C::WARPS; ++w) {
-      const int y = flags[16 + w];
+      const uint64_t y = sums[w];
       if (w < warp) before += y;
       carry += y;
+      longest = max(longest, static_cast<int>(sums[16 + w]));
     }
-    if (b < B) prefix[b] = before + x - n;
+    if (b < B) prefix[b] = before + x - mine;
     __syncthreads();
   }
-  const int per_seq = c.Hkv * a.groups;  // tasks of a sequence
-  const long long total = static_cast<long long>(carry) * per_seq;
-  const long long parts = min(total, static_cast<long long>(gridDim.x));  // CTAs with work: each has a block at least
+  // The units that are dealt out: a task is its blocks and TASK_UNITS more for
+  // what it costs besides them; or, where every task is short and none need share
+  // a CTA with another, one unit, so that no task is cut (its pieces' way through
+  // the workspace takes longer than 24 blocks).
+  const uint32_t per_seq = c.Hkv * a.groups;  // tasks of a sequence
+  const uint32_t tasks = static_cast<uint32_t>(carry >> 32) * per_seq;
+  const bool uncut = longest <= 24 && tasks <= gridDim.x;
+  const uint32_t total = uncut ? tasks : static_cast<uint32_t>(carry) * per_seq;
+  const uint32_t parts = min(total, gridDim.x);  // CTAs with work: a unit each at least
   if (blockIdx.x >= parts) return;
-  const long long u0 = total * blockIdx.x / parts, u1 = total * (blockIdx.x + 1) / parts;
+  // the first `more` runs have a unit more than the others
+  const uint32_t run = total / parts, more = total - run * parts;
+  const uint32_t u0 = run * blockIdx.x + min(blockIdx.x, more), u1 = u0 + run + (blockIdx.x < more);
+  auto cta_of = [&](uint32_t u) { return u < more * (run + 1) ? u / (run + 1) : more + (u - more * (run + 1)) / run; };
+  auto before_of = [&](int b) { return uncut ? static_cast<uint32_t>(prefix[b] >> 32) : static_cast<uint32_t>(prefix[b]); };
   volatile int* stop = flags;
 
-  // A task of the CTA's run: [t0, t1) of its blocks are ours.
+  // A task of the CTA's run: [t0, t1) of its blocks are ours (none where the run
+  // begins behind them), `units` of the run.
   struct Task {
     int b, h, grp, begin, blocks, t0, t1;
+    uint32_t units;
     Kv8Seq s;
   };
-  auto task_at = [&](long long u, Task& k) {
-    const long long want = u / per_seq;  // the sequence holding unit u: prefix[b] <= want < prefix[b + 1]
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= want) lo = mid; else hi = mid;
-    }
-    k.b = lo;
-    kv8_seq(c, a.cu, a.kv_len, a.N, a.max_new, lo, false, k.s);
+  auto seq_of = [&](Task& k) {
+    kv8_seq(c, a.cu, a.kv_len, a.N, a.max_new, k.b, false, k.s);
     int end;
     seq_blocks(k.s, a.window, k.begin, end);
     k.blocks = end - k.begin;
-    const int rel = static_cast<int>(u - static_cast<long long>(prefix[lo]) * per_seq);
-    const int task = rel / k.blocks;
+  };
+  auto span_of = [&](uint32_t u, Task& k) {
+    k.units = uncut ? 1u : min(static_cast<uint32_t>(k.blocks + TASK_UNITS - k.t0), u1 - u);
+    k.t1 = uncut ? k.blocks : min(k.blocks, k.t0 + static_cast<int>(k.units));
+  };
+  auto task_at = [&](uint32_t u, Task& k) {  // the task that holds unit u
+    const uint32_t want = u / per_seq;       // in the sequence with before_of(b) <= want < before_of(b + 1)
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before_of(mid) <= want) lo = mid; else hi = mid;
+    }
+    k.b = lo;
+    seq_of(k);
+    const uint32_t rel = u - before_of(lo) * per_seq;
+    const uint32_t each = uncut ? 1u : k.blocks + TASK_UNITS, task = rel / each;
     k.h = task / a.groups;
     k.grp = task - k.h * a.groups;
-    k.t0 = rel - task * k.blocks;
-    k.t1 = static_cast<int>(min(static_cast<long long>(k.blocks), k.t0 + (u1 - u)));
+    k.t0 = rel - task * each;
+    span_of(u, k);
+  };
+  auto next_task = [&](uint32_t u, Task& k) {  // the task after k, which begins with unit u < u1
+    k.t0 = 0;
+    if (++k.grp == a.groups) {
+      k.grp = 0;
+      if (++k.h == c.Hkv) {
+        k.h = 0;
+        do {
+          ++k.b;
+          seq_of(k);
+        } while (k.blocks == 0);
+      }
+    }
+    span_of(u, k);
   };
 
-  const int g4 = warp >> 2, tt = warp & 3;  // group of 4 warps; the warp's 16 tokens of a block
+  const int g4 = warp / C::PW, tt = warp % C::PW;  // group; the warp's 16 MT tokens of a block
   const int g = lane >> 2, t4 = lane & 3;
+  uint32_t u_first = u0;
+  Task k;
+  task_at(u0, k);
+  if (k.t0 >= k.blocks) {  // the run begins behind a task's blocks
+    u_first += k.units;
+    if (u_first >= u1) return;
+    next_task(u_first, k);
+  }
+
+  // raw query rows 8 nb + g of a task (elements 16 t4 .. and 64 + 16 t4 ..)
+  auto load_q = [&](const Task& k, int nb, uint4 (&v)[4]) {
+    const int r = k.grp * R + 8 * nb + g;
+    if (r < k.s.n * a.G) {
+      const E* p = static_cast<const E*>(a.q) + static_cast<int64_t>(k.s.row0 + r / a.G) * a.q_tok +
+                   static_cast<int64_t>(k.h * a.G + r % a.G) * a.q_head + 16 * t4;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v[2 * j] = *reinterpret_cast<const uint4*>(p + 64 * j);
+        v[2 * j + 1] = *reinterpret_cast<const uint4*>(p + 64 * j + 8);
+      }
+    } else {
+      v[0] = v[1] = v[2] = v[3] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
 
   // ------------------------------------------------------------ the warp's copies, SLOTS ahead
   // Blocks t = first, first + NG, .. of each task go to this group; the first
   // rotates with the task's number within the run.
   uint8_t* ring = rings + warp * SLOTS * SLOT;
-  struct Cursor {
-    long long u;              // units before the next task
-    int t, end, b, ordinal;   // next block of the task (relative to its begin), end of the complete ones
-    int batch, looked;        // pages of blocks batch, batch + NG, ..: lane i holds that of batch + i NG
-    uint64_t page;
-    size_t bh;
-    int begin;
-  } cur = {u0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+  // The pool pages of the warp's blocks are looked up 32 at a time, lane i the
+  // i-th, and a lookup ahead of their use.  The cursor lies in shared memory: the
+  // warp's registers are full.  Every lane reads the same words.
+  struct Ahead {
+    Task k;
+    uint32_t u;           // first unit of its task
+    int ordinal, t;       // the task's number in the run, the next block to look up
+  };
+  static_assert(sizeof(Ahead) <= C::AHEAD, "the cursor's place");
+  Ahead& ah = *reinterpret_cast<Ahead*>(ahead + warp * C::AHEAD);
+  uint4 qv[NB][4];  // a task's queries are fetched while the one before it is joined, the first's here
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) load_q(k, nb, qv[nb]);
   auto first_of = [&](int t0, int ordinal) { return t0 + (g4 + ordinal) % NG; };
+  struct Pages {
+    int n, at, b;         // how many (0: the run has no more), the next one, their sequence
+    int idx;              // the lane's page, -1: outside the pool
+  } now, then;
+  auto look_up = [&](Pages& x) {
+    while (true) {
+      const int left = min(ah.k.t1, ah.k.s.len / KV8_BLOCK - ah.k.begin) - ah.t;  // the incomplete block is read where it lies
+      if (left > 0) {
+        x.n = min(32, (left + NG - 1) / NG);
+        x.at = 0;
+        x.b = ah.k.b;
+        if (lane < x.n)
+          x.idx = static_cast<int>(kv8_page_index(c, static_cast<size_t>(ah.k.b) * c.Hkv + ah.k.h, ah.k.begin + ah.t + lane * NG));
+        __syncwarp();
+        if (lane == 0) ah.t += 32 * NG;
+        __syncwarp();
+        return;
+      }
+      x.n = x.at = 0;
+      const uint32_t u = ah.u + ah.k.units;
+      if (u >= u1) return;
+      Task n = ah.k;
+      next_task(u, n);
+      const int ordinal = ah.ordinal + 1;
+      __syncwarp();
+      if (lane == 0) ah = Ahead{n, u, ordinal, first_of(n.t0, ordinal)};
+      __syncwarp();
+    }
+  };
+  if (lane == 0) ah = Ahead{k, u_first, 0, first_of(k.t0, 0)};
+  __syncwarp();
+  now = Pages{0, 0, 0, 0};
+  look_up(then);
   auto issue = [&](int slot) {  // the next block's slice into the slot; false at the end of the run
-    while (cur.t >= cur.end) {
-      if (cur.u >= u1) return false;
-      Task k;
-      task_at(cur.u, k);
-      cur.u += k.t1 - k.t0;
-      cur.t = first_of(k.t0, cur.ordinal++);
-      cur.end = min(k.t1, k.s.len / KV8_BLOCK - k.begin);  // the incomplete block is read where it lies
-      cur.b = k.b;
-      cur.bh = static_cast<size_t>(k.b) * c.Hkv + k.h;
-      cur.begin = k.begin;
-      cur.looked = 0;
+    if (now.at == now.n) {
+      if (then.n == 0) return false;
+      now = then;
+      look_up(then);
     }
-    if (cur.looked == 0 || cur.t >= cur.batch + 32 * NG) {
-      cur.batch = cur.t;
-      cur.looked = 1;
-      const int t = cur.t + lane * NG;
-      cur.page = t < cur.end ? reinterpret_cast<uint64_t>(kv8_page(c, cur.bh, cur.begin + t)) : 0;
+    int idx = __shfl_sync(0xffffffffu, now.idx, now.at);
+    ++now.at;
+    if (idx < 0) {
+      if (lane == 0) kv8_err(c, now.b, HQ_DEVERR_PAGE);
+      idx = 0;
     }
-    const uint8_t* page = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, cur.page, (cur.t - cur.batch) / NG));
-    cur.t += NG;
+    const uint8_t* page = c.pages + static_cast<size_t>(idx) * HQ_KV8_PAGE_BYTES;
     if (lane == 0) {
       uint8_t* dst = ring + slot * SLOT;
       mbar_arrive_expect_tx(full + slot, SLOT);
@@ -238,9 +343,7 @@ __global__ void __launch_bounds__(Cfg<NB>::THREADS, 1) kv8_attn_kernel(const __g
   bool ok = true;
 
   int ordinal = 0;
-  for (long long u = u0; u < u1;) {
-    Task k;
-    task_at(u, k);
+  for (uint32_t u = u_first;;) {
     const size_t bh = static_cast<size_t>(k.b) * c.Hkv + k.h;
     const int row0 = k.grp * R, rows = k.s.n * a.G;
 
@@ -253,18 +356,8 @@ __global__ void __launch_bounds__(Cfg<NB>::THREADS, 1) kv8_attn_kernel(const __g
     float m_run[NB][2], e_run[NB][2], l_run[NB][2], ef[NB][2];  // ef = 2^(m - E + P_BIAS)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const int r = row0 + 8 * nb + g;
       float mul = 1.0f;
-      uint4 v[4] = {};
-      if (r < rows) {
-        const E* p = static_cast<const E*>(a.q) + static_cast<int64_t>(k.s.row0 + r / a.G) * a.q_tok +
-                     static_cast<int64_t>(k.h * a.G + r % a.G) * a.q_head + 16 * t4;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          v[2 * j] = *reinterpret_cast<const uint4*>(p + 64 * j);
-          v[2 * j + 1] = *reinterpret_cast<const uint4*>(p + 64 * j + 8);
-        }
-      }
+      const uint4(&v)[4] = qv[nb];
       const E* e = reinterpret_cast<const E*>(v);
       if (IsBf16<E>::value) {
         // bf16 rows become fp16 at a power of two that brings their largest value to [2^14, 2^15)
@@ -308,47 +401,47 @@ __global__ void __launch_bounds__(Cfg<NB>::THREADS, 1) kv8_attn_kernel(const __g
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[nb][mt][i] = 0.f;
 
-    // one 16-token tile: kf, vf give the A operands of step s / output rows 16 mt
-    // .. 16 mt + 15; ks, vs the scales of tokens g, g + 8 (vtop: the largest vs of
-    // the tile); pos the first token's position
-    auto tile = [&](auto masked, auto kf, auto vf, const float (&ks)[2], const float (&vs)[2], float vtop, int pos) {
+    // NT 16-token tiles: kf, vf give the A operands of step s / output rows 16 d
+    // .. 16 d + 15 of tile j; ks, vs the scales of its tokens g, g + 8 (vtop: the
+    // largest vs of all); pos the first token's position
+    auto tiles = [&](auto count, auto masked, auto kf, auto vf, const float (&ks)[2], const float (&vs)[2], float vtop, int pos) {
+      constexpr int NT = decltype(count)::value;
       constexpr bool MASK = decltype(masked)::value;
-      float sc[NB][4];
-      {
-        float s2[NB][4];
+      float sc[NT][NB][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[nb][i] = s2[nb][i] = 0.f;
+          for (int i = 0; i < 4; ++i) sc[j][nb][i] = 0.f;
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
+      for (int s = 0; s < 8; ++s)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
           uint32_t f[4];
-          kf(s, f);
+          kf(j, s, f);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma16816(s & 1 ? s2[nb] : sc[nb], f[0], f[1], f[2], f[3], qf[nb][2 * s], qf[nb][2 * s + 1]);
+          for (int nb = 0; nb < NB; ++nb) mma16816(sc[j][nb], f[0], f[1], f[2], f[3], qf[nb][2 * s], qf[nb][2 * s + 1]);
         }
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[nb][i] = (sc[nb][i] + s2[nb][i]) * (qs[nb][i & 1] * ks[i >> 1]);
-      }
-      if (MASK) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // how far the token lies behind the query
-            const int d = qp[nb][i & 1] - (pos + g + 8 * (i >> 1));
-            if (d < 0 || (a.window > 0 && d >= a.window && qp[nb][i & 1] != INT_MAX)) sc[nb][i] = -INFINITY;
-          }
-      }
       bool far = false;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int nb = 0; nb < NB; ++nb) {
+        far |= fmaxf(ef[nb][0], ef[nb][1]) * vtop > V_LIMIT;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) far |= sc[nb][i] - m_run[nb][i & 1] > P_SLACK;
+        for (int i = 0; i < 4; ++i) {
+          const float mul = qs[nb][i & 1] * ks[i >> 1];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) far |= fmaxf(ef[nb][0], ef[nb][1]) * vtop > V_LIMIT;
+          for (int j = 0; j < NT; ++j) {
+            sc[j][nb][i] *= mul;
+            if (MASK) {
+              // how far the token lies behind the query
+              const int d = qp[nb][i & 1] - (pos + 16 * j + g + 8 * (i >> 1));
+              if (d < 0 || (a.window > 0 && d >= a.window && qp[nb][i & 1] != INT_MAX)) sc[j][nb][i] = -INFINITY;
+            }
+            far |= sc[j][nb][i] - m_run[nb][i & 1] > P_SLACK;
+          }
+        }
+      }
       if (__any_sync(0xffffffffu, far)) {
         const float lv = log2f(vtop);
 #pragma unroll
@@ -356,7 +449,9 @@ __global__ void __launch_bounds__(Cfg<NB>::THREADS, 1) kv8_attn_kernel(const __g
           float ao[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float mt = fmaxf(sc[nb][i], sc[nb][2 + i]);
+            float mt = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mt = fmaxf(mt, fmaxf(sc[j][nb][i], sc[j][nb][2 + i]));
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
@@ -370,113 +465,143 @@ __global__ void __launch_bounds__(Cfg<NB>::THREADS, 1) kv8_attn_kernel(const __g
             ef[nb][i] = e_new == -INFINITY ? 0.f : ex2(fminf(mb - eb + P_BIAS, 100.f));
           }
 #pragma unroll
-          for (int mt = 0; mt < 8; ++mt)
+          for (int d = 0; d < 8; ++d)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[nb][mt][i] *= ao[i & 1];
+            for (int i = 0; i < 4; ++i) o[nb][d][i] *= ao[i & 1];
         }
       }
-      uint32_t pf[NB][2];
+      uint32_t pf[NT][NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        float p[4];
+        float w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[i] = ex2(sc[nb][i] - m_run[nb][i & 1]);
-          if (MASK && sc[nb][i] == -INFINITY) p[i] = 0.f;  // also while m is -inf
+        for (int i = 0; i < 4; ++i) w[i] = ef[nb][i & 1] * vs[i >> 1];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          float p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[i] = ex2(sc[j][nb][i] - m_run[nb][i & 1]);
+            if (MASK && sc[j][nb][i] == -INFINITY) p[i] = 0.f;  // also while m is -inf
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) l_run[nb][i] += p[i] + p[2 + i];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[i] *= w[i];
+            if (MASK && sc[j][nb][i] == -INFINITY) p[i] = 0.f;  // a scale that is NaN stays behind the mask
+          }
+          pf[j][nb][0] = movmatrix_t(pack_f16x2(p[0], p[1]));
+          pf[j][nb][1] = movmatrix_t(pack_f16x2(p[2], p[3]));
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) l_run[nb][i] += p[i] + p[2 + i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[i] *= ef[nb][i & 1] * vs[i >> 1];
-          if (MASK && sc[nb][i] == -INFINITY) p[i] = 0.f;  // a scale that is NaN stays behind the mask
-        }
-        pf[nb][0] = movmatrix_t(pack_f16x2(p[0], p[1]));
-        pf[nb][1] = movmatrix_t(pack_f16x2(p[2], p[3]));
       }
 #pragma unroll
-      for (int mt = 0; mt < 8; ++mt) {
-        uint32_t f[4];
-        vf(mt, f);
+      for (int d = 0; d < 8; ++d)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][mt], f[0], f[1], f[2], f[3], pf[nb][0], pf[nb][1]);
-      }
+        for (int j = 0; j < NT; ++j) {
+          uint32_t f[4];
+          vf(j, d, f);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][d], f[0], f[1], f[2], f[3], pf[j][nb][0], pf[j][nb][1]);
+        }
     };
 
-    for (int t = first_of(k.t0, ordinal); t < k.t1; t += NG) {
-      const int p0 = (k.begin + t) * KV8_BLOCK, pos = p0 + tt * 16;
-      if (p0 + KV8_BLOCK <= k.s.len) {
-        ok = ok && ring_wait(full + slot, phase, c.err + k.b, stop);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint8_t* src = ring + slot * SLOT;
-        uint4 kw[4], vw[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) kw[i] = reinterpret_cast<const uint4*>(src + i * 512)[lane];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) vw[i] = reinterpret_cast<const uint4*>(src + SLICE + i * 512)[lane];
-        const float2 sc = *reinterpret_cast<const float2*>(src + 2 * SLICE);
-        __syncwarp();  // every lane has its part: the slot takes the next slice
-        ++taken;
-        if (issue(slot)) ++issued;
-        if (++slot == SLOTS) slot = 0, phase ^= 1;
-        auto word = [](const uint4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; };
-        auto kf = [&](int s, uint32_t (&f)[4]) {
-          // chunk (token half a, d half j) = 2 a + j; word s % 4 of it
-          kv8_half4<FMT>(word(kw[s >> 2], s & 3), f[0], f[2]);
-          kv8_half4<FMT>(word(kw[2 + (s >> 2)], s & 3), f[1], f[3]);
-        };
-        auto vf = [&](int mt, uint32_t (&f)[4]) {
-          kv8_half4<FMT>(word(vw[mt >> 1], (mt & 1) * 2), f[0], f[2]);
-          kv8_half4<FMT>(word(vw[mt >> 1], (mt & 1) * 2 + 1), f[1], f[3]);
-        };
-        const float ks[2] = {sc.x, sc.x}, vs[2] = {sc.y, sc.y};
-        // seen whole by every row?
-        if (pos + 15 <= q_lo && (a.window <= 0 || pos > q_hi - a.window))
-          tile(std::false_type{}, kf, vf, ks, vs, sc.y, pos);
-        else
-          tile(std::true_type{}, kf, vf, ks, vs, sc.y, pos);
-      } else if (pos < k.s.len) {
-        // the incomplete block, in 16 bits: rows past the length hold finite
-        // values of earlier blocks or zeros and are masked
-        const int half = (k.begin + t) & 1;
-        const uint4* tk = reinterpret_cast<const uint4*>(c.tail_k + (bh * 2 + half) * KV8_BLOCK * D + tt * 2048);
-        const uint4* tv = reinterpret_cast<const uint4*>(c.tail_v + (bh * 2 + half) * KV8_BLOCK * D + tt * 2048);
-        const float* ts = c.tail_scale + bh * 2 * HQ_KV8_TAIL + half * KV8_BLOCK + tt * 16 + g;
-        const bool in0 = pos + g < k.s.len, in1 = pos + g + 8 < k.s.len;
-        const float ks[2] = {in0 ? ts[0] : 1.f, in1 ? ts[8] : 1.f};
-        const float vs[2] = {in0 ? ts[HQ_KV8_TAIL] : 0.f, in1 ? ts[HQ_KV8_TAIL + 8] : 0.f};
-        float vtop = fmaxf(vs[0], vs[1]);  // ignores NaN
-        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 4));
-        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 8));
-        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 16));
-        if (!(vtop > 0.f)) vtop = 1.f;
+    // The incomplete block first, in 16 bits from where it lies, a tile to each of
+    // four warps: rows past the length hold finite values of earlier blocks or
+    // zeros and are masked.
+    const int full_end = min(k.t1, k.s.len / KV8_BLOCK - k.begin);
+    if (full_end < k.t1 && warp % (C::WARPS / 4) == 0) {
+      const int t16 = warp / (C::WARPS / 4), blk = k.begin + full_end, pos = blk * KV8_BLOCK + t16 * 16;
+      if (pos < k.s.len) {
+        const size_t half = bh * 2 + (blk & 1);
+        const uint4* tk = reinterpret_cast<const uint4*>(c.tail_k + half * KV8_BLOCK * D + t16 * 2048);
+        const uint4* tv = reinterpret_cast<const uint4*>(c.tail_v + half * KV8_BLOCK * D + t16 * 2048);
+        const float* ts = c.tail_scale + bh * 2 * HQ_KV8_TAIL + (blk & 1) * KV8_BLOCK + t16 * 16 + g;
         uint32_t kw[4][8], vw[4][8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           *reinterpret_cast<uint4*>(&kw[i][0]) = tk[(i * 32 + lane) * 2];
           *reinterpret_cast<uint4*>(&kw[i][4]) = tk[(i * 32 + lane) * 2 + 1];
         }
-        auto kf = [&](int s, uint32_t (&f)[4]) {
-          f[0] = kw[s >> 2][(s & 3) * 2];
-          f[2] = kw[s >> 2][(s & 3) * 2 + 1];
-          f[1] = kw[2 + (s >> 2)][(s & 3) * 2];
-          f[3] = kw[2 + (s >> 2)][(s & 3) * 2 + 1];
-        };
+        const bool in0 = pos + g < k.s.len, in1 = pos + g + 8 < k.s.len;
+        const float ks[2] = {in0 ? ts[0] : 1.f, in1 ? ts[8] : 1.f};
+        const float vs[2] = {in0 ? ts[HQ_KV8_TAIL] : 0.f, in1 ? ts[HQ_KV8_TAIL + 8] : 0.f};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           *reinterpret_cast<uint4*>(&vw[i][0]) = tv[(i * 32 + lane) * 2];
           *reinterpret_cast<uint4*>(&vw[i][4]) = tv[(i * 32 + lane) * 2 + 1];
         }
-        auto vf = [&](int mt, uint32_t (&f)[4]) {
-          const int w = (mt & 1) * 4;
-          f[0] = vw[mt >> 1][w];
-          f[2] = vw[mt >> 1][w + 1];
-          f[1] = vw[mt >> 1][w + 2];
-          f[3] = vw[mt >> 1][w + 3];
+        float vtop = fmaxf(vs[0], vs[1]);  // ignores NaN
+        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 4));
+        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 8));
+        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 16));
+        if (!(vtop > 0.f)) vtop = 1.f;
+        auto kf = [&](int, int s, uint32_t (&f)[4]) {
+          f[0] = kw[s >> 2][(s & 3) * 2];
+          f[2] = kw[s >> 2][(s & 3) * 2 + 1];
+          f[1] = kw[2 + (s >> 2)][(s & 3) * 2];
+          f[3] = kw[2 + (s >> 2)][(s & 3) * 2 + 1];
         };
-        tile(std::true_type{}, kf, vf, ks, vs, vtop, pos);
+        auto vf = [&](int, int d, uint32_t (&f)[4]) {
+          const int w = (d & 1) * 4;
+          f[0] = vw[d >> 1][w];
+          f[2] = vw[d >> 1][w + 1];
+          f[1] = vw[d >> 1][w + 2];
+          f[3] = vw[d >> 1][w + 3];
+        };
+        tiles(std::integral_constant<int, 1>{}, std::true_type{}, kf, vf, ks, vs, vtop, pos);
       }
+    }
+
+    for (int t = first_of(k.t0, ordinal); t < full_end; t += NG) {
+      const int pos = (k.begin + t) * KV8_BLOCK + tt * 16 * MT;
+      ok = ok && ring_wait(full + slot, phase, c.err + k.b, stop);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint8_t* src = ring + slot * SLOT;
+      uint4 kw[MT][4], vw[MT][4];
+#pragma unroll
+      for (int i = 0; i < 4 * MT; ++i) kw[i / 4][i % 4] = reinterpret_cast<const uint4*>(src + i * 512)[lane];
+      if (MT == 2) {
+#pragma unroll
+        for (int i = 0; i < 4 * MT; ++i) vw[i / 4][i % 4] = reinterpret_cast<const uint4*>(src + SLICE + i * 512)[lane];
+      }
+      const float2 sc = *reinterpret_cast<const float2*>(src + 2 * SLICE);
+      auto release = [&]() {
+        __syncwarp();  // every lane has its part: the slot takes the next slice
+        ++taken;
+        if (issue(slot)) ++issued;
+        if (++slot == SLOTS) slot = 0, phase ^= 1;
+      };
+      if (MT == 2) release();
+      auto word = [](const uint4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; };
+      auto kf = [&](int j, int s, uint32_t (&f)[4]) {
+        // chunk (token half a, d half h) = 2 a + h; word s % 4 of it
+        kv8_half4<FMT>(word(kw[j][s >> 2], s & 3), f[0], f[2]);
+        kv8_half4<FMT>(word(kw[j][2 + (s >> 2)], s & 3), f[1], f[3]);
+      };
+      auto vf = [&](int j, int d, uint32_t (&f)[4]) {
+        // many rows: values from the slot as they are needed, for want of registers
+        if (MT == 1 && (d & 1) == 0) vw[j][d >> 1] = reinterpret_cast<const uint4*>(src + SLICE + (d >> 1) * 512)[lane];
+        kv8_half4<FMT>(word(vw[j][d >> 1], (d & 1) * 2), f[0], f[2]);
+        kv8_half4<FMT>(word(vw[j][d >> 1], (d & 1) * 2 + 1), f[1], f[3]);
+      };
+      const float ks[2] = {sc.x, sc.x}, vs[2] = {sc.y, sc.y};
+      constexpr std::integral_constant<int, MT> all{};
+      // seen whole by every row?
+      if (pos + 16 * MT - 1 <= q_lo && (a.window <= 0 || pos > q_hi - a.window))
+        tiles(all, std::false_type{}, kf, vf, ks, vs, sc.y, pos);
+      else
+        tiles(all, std::true_type{}, kf, vf, ks, vs, sc.y, pos);
+      if (MT == 1) release();
+    }
+
+    const uint32_t u_next = u + k.units;
+    Task k_next = k;
+    if (u_next < u1) {
+      next_task(u_next, k_next);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) load_q(k_next, nb, qv[nb]);
     }
 
     // ------------------------------------------------------------ the CTA's piece of the task
@@ -509,64 +634,79 @@ __global__ void __launch_bounds__(Cfg<NB>::THREADS, 1) kv8_attn_kernel(const __g
           *reinterpret_cast<const uint2*>(y);
       if (a.lse != nullptr && lane == 0) a.lse[tok * a.Hq + head] = m + log2f(l);
     };
+    static_assert(8 % C::WARPS == 0 && C::WARPS % C::OW == 0, "as many of 8 rows to each warp; whole rounds");
+    constexpr int RW = 8 / C::WARPS;  // rows 8 nb + warp + i WARPS, elements 4 lane .. 4 lane + 3
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       __syncthreads();  // red is there; the buffer's earlier readers are done
+      float f[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = 2 * t4 + i;
         float e = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) e = fmaxf(e, red[w * R + 8 * nb + r].y);
-        const float f = e == -INFINITY ? 1.f : ex2(e_run[nb][i] - e);
-#pragma unroll
-        for (int mt = 0; mt < 8; ++mt) {
-          obuf[(warp * 8 + r) * OS + mt * 16 + g] = o[nb][mt][i] * f;
-          obuf[(warp * 8 + r) * OS + mt * 16 + g + 8] = o[nb][mt][2 + i] * f;
-        }
+        for (int w = 0; w < C::WARPS; ++w) e = fmaxf(e, red[w * R + 8 * nb + 2 * t4 + i].y);
+        f[i] = e == -INFINITY ? 1.f : ex2(e_run[nb][i] - e);
       }
-      // row 8 nb + warp of the first 8 warps: elements 4 lane .. 4 lane + 3
-      float m = -INFINITY, e = -INFINITY, l = 0.f;
-      if (warp < 8) {
+      float m[RW], e[RW], l[RW];
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        m[i] = e[i] = -INFINITY;
+        l[i] = 0.f;
 #pragma unroll
         for (int w = 0; w < C::WARPS; ++w) {
-          const float4 x = red[w * R + 8 * nb + warp];
-          m = fmaxf(m, x.x);
-          e = fmaxf(e, x.y);
+          const float4 x = red[w * R + 8 * nb + warp + i * C::WARPS];
+          m[i] = fmaxf(m[i], x.x);
+          e[i] = fmaxf(e[i], x.y);
         }
-        const float mb = m == -INFINITY ? 0.f : m;
+        const float mb = m[i] == -INFINITY ? 0.f : m[i];
 #pragma unroll
         for (int w = 0; w < C::WARPS; ++w) {
-          const float4 x = red[w * R + 8 * nb + warp];
-          l += x.z * ex2(x.x - mb);
+          const float4 x = red[w * R + 8 * nb + warp + i * C::WARPS];
+          l[i] += x.z * ex2(x.x - mb);
         }
       }
-      __syncthreads();
-      if (warp < 8) {
+      // OW warps at a time add theirs to what the ones before left in their place
+#pragma unroll
+      for (int w0 = 0; w0 < C::WARPS; w0 += C::OW) {
+        if (warp / C::OW == w0 / C::OW) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float* row = obuf + (warp % C::OW * 8 + 2 * t4 + i) * OS + g;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              row[d * 16] = (w0 > 0 ? row[d * 16] : 0.f) + o[nb][d][i] * f[i];
+              row[d * 16 + 8] = (w0 > 0 ? row[d * 16 + 8] : 0.f) + o[nb][d][2 + i] * f[i];
+            }
+          }
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        const int r8 = warp + i * C::WARPS, r = 8 * nb + r8;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) {
-          const float4 x = *reinterpret_cast<const float4*>(obuf + (w * 8 + warp) * OS + 4 * lane);
+        for (int w = 0; w < C::OW; ++w) {
+          const float4 x = *reinterpret_cast<const float4*>(obuf + (w * 8 + r8) * OS + 4 * lane);
           s.x += x.x;
           s.y += x.y;
           s.z += x.z;
           s.w += x.w;
         }
-        const int r = 8 * nb + warp;
         if (whole) {
-          finish(r, m, e, l, s);
+          finish(r, m[i], e[i], l[i], s);
         } else {
           reinterpret_cast<float4*>(part + r * D)[lane] = s;
-          if (lane == 0) reinterpret_cast<float4*>(part + R * D)[r] = make_float4(m, e, l, 0.f);
+          if (lane == 0) reinterpret_cast<float4*>(part + R * D)[r] = make_float4(m[i], e[i], l[i], 0.f);
         }
       }
     }
     if (!whole) {
-      const long long k0 = u - k.t0, k1 = k0 + k.blocks;  // the task's units
-      const int c0 = static_cast<int>(((k0 + 1) * parts - 1) / total), c1 = static_cast<int>((k1 * parts - 1) / total);
-      __threadfence();
+      const uint32_t k0 = u - k.t0;  // the task's first unit
+      const int c0 = cta_of(k0), c1 = cta_of(k0 + k.blocks - 1);
       __syncthreads();
       if (threadIdx.x == 0) {
+        // the barrier above puts the CTA's writes before this release
         const unsigned int before = atom_add_acq_rel_gpu(a.counters + c0, 1u);
         const bool last = before == static_cast<unsigned int>(c1 - c0);
         if (last) a.counters[c0] = 0u;
@@ -574,34 +714,63 @@ __global__ void __launch_bounds__(Cfg<NB>::THREADS, 1) kv8_attn_kernel(const __g
       }
       __syncthreads();
       if (flags[1]) {
-        fence_acq_rel_gpu();
+        auto piece = [&](int p) { return a.parts + static_cast<size_t>(2 * p + (p == c0)) * PART; };
+        auto refs = [&](int r, int p) {
+          return p <= c1 ? __ldcg(reinterpret_cast<const float4*>(piece(p) + R * D) + r) : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+        };
         for (int r = warp; r < R; r += C::WARPS) {
+          // lane i holds the references of pieces c0 + i, c0 + i + 32, ..
           float m = -INFINITY, e = -INFINITY, l = 0.f;
-          for (int p = c0; p <= c1; ++p) {
-            const float* q = a.parts + static_cast<size_t>(2 * p + (p == c0)) * PART;
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(q + R * D) + r);
-            m = fmaxf(m, x.x);
-            e = fmaxf(e, x.y);
-          }
-          const float mb = m == -INFINITY ? 0.f : m, eb = e == -INFINITY ? 0.f : e;
           float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int p = c0; p <= c1; ++p) {
-            const float* q = a.parts + static_cast<size_t>(2 * p + (p == c0)) * PART;
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(q + R * D) + r);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(q + r * D) + lane);
-            l += x.z * ex2(x.x - mb);
-            const float f = ex2(x.y - eb);
-            s.x += y.x * f;
-            s.y += y.y * f;
-            s.z += y.z * f;
-            s.w += y.w * f;
+          // 32 pieces at a time, joined to what was there before; 8 pieces' loads in flight
+          for (int p0 = c0; p0 <= c1; p0 += 32) {
+            const int n = min(32, c1 - p0 + 1);
+            const float4 x = refs(r, p0 + lane);
+            float4 y[8];
+            auto fetch = [&](int i0) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                y[i] = i0 + i < n ? __ldcg(reinterpret_cast<const float4*>(piece(p0 + i0 + i) + r * D) + lane)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            };
+            fetch(0);
+            float m_new = fmaxf(m, x.x), e_new = fmaxf(e, x.y);
+#pragma unroll
+            for (int i = 16; i > 0; i >>= 1) {
+              m_new = fmaxf(m_new, __shfl_xor_sync(0xffffffffu, m_new, i));
+              e_new = fmaxf(e_new, __shfl_xor_sync(0xffffffffu, e_new, i));
+            }
+            const float mb = m_new == -INFINITY ? 0.f : m_new, eb = e_new == -INFINITY ? 0.f : e_new;
+            const float fo = ex2(e - eb), f = p0 + lane <= c1 ? ex2(x.y - eb) : 0.f;
+            l = l * ex2(m - mb) + x.z * ex2(x.x - mb);
+            m = m_new;
+            e = e_new;
+            s.x *= fo;
+            s.y *= fo;
+            s.z *= fo;
+            s.w *= fo;
+            for (int i0 = 0; i0 < n; i0 += 8) {
+              if (i0 > 0) fetch(i0);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float fi = __shfl_sync(0xffffffffu, f, i0 + i);
+                s.x += y[i].x * fi;
+                s.y += y[i].y * fi;
+                s.z += y[i].z * fi;
+                s.w += y[i].w * fi;
+              }
+            }
           }
+#pragma unroll
+          for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
           finish(r, m, e, l, s);
         }
       }
     }
+    if (u_next >= u1) break;
+    u = u_next;
+    k = k_next;
     ++ordinal;
-    u += k.t1 - k.t0;
   }
   // copies that were not waited for (after a wait that gave up) land before the
   // CTA gives its shared memory back
@@ -611,39 +780,54 @@ __global__ void __launch_bounds__(Cfg<NB>::THREADS, 1) kv8_attn_kernel(const __g
   }
 }
 
-constexpr int SMEM_MAX = 227 * 1024;
+constexpr int SMEM_MAX = 224 * 1024;  // of an SM: 228 KB less 1 KB for each of up to four CTAs
 
-template <class E, int FMT, int NB>
+template <class E, int FMT, int NB, int W>
 hq_status launch(AttnArgs& a, int sms, cudaStream_t st) {
-  using C = Cfg<NB>;
-  static_assert(C::FIXED + (HQ_KV8_MAX_BATCH + 1) * 4 <= SMEM_MAX, "shared memory of the largest batch");
+  using C = Cfg<NB, W>;
+  static_assert(C::FIXED % 8 == 0 && C::FIXED + HQ_KV8_MAX_BATCH * 8 <= SMEM_MAX / C::CTAS, "shared memory of the largest batch");
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "kv8 attention setup");
   static DeviceOnce attrs;
   e = attrs.run(dev, [] {
-    return cudaFuncSetAttribute(kv8_attn_kernel<E, FMT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
+    return cudaFuncSetAttribute(kv8_attn_kernel<E, FMT, NB, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX / C::CTAS);
   });
   if (e != cudaSuccess) return cuda_fail(e, "kv8 attention setup");
   a.groups = (a.G * a.max_new + C::R - 1) / C::R;
-  kv8_attn_kernel<E, FMT, NB><<<sms, C::THREADS, C::FIXED + (a.c.B + 1) * 4, st>>>(a);
+  // units are counted in 32 bits
+  if (static_cast<double>(a.c.B) * a.c.Hkv * a.groups * (a.c.cap / KV8_BLOCK + TASK_UNITS) >= 4e9) return HQ_ERR_UNSUPPORTED;
+  kv8_attn_kernel<E, FMT, NB, W><<<C::CTAS * sms, C::THREADS, C::FIXED + a.c.B * 8, st>>>(a);
   return cuda_status(cudaGetLastError(), "kv8 attention launch");
 }
 
 // Rows of a task, in eights: as many as there are, up to 4; beyond that tasks of 32 rows.
 int row_eights(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }
 
+// One CTA of 8 warps on an SM, or two of 4.  Where CTAs finish several tasks
+// each, one of two streams while the other joins its warps' results (64
+// sequences of 1K-16K, 8 kv heads: 207 us against 219 us); where tasks are few,
+// twice the pieces are to be joined and twice the plans made (one 32K sequence:
+// 24.8 us against 22.2 us).
+template <class E, int FMT, int NB>
+hq_status launch_w(AttnArgs& a, int sms, cudaStream_t st) {
+  if (static_cast<int64_t>(a.c.B) * a.c.Hkv * ((a.G * a.max_new + 8 * NB - 1) / (8 * NB)) >= 2 * sms)
+    return launch<E, FMT, NB, 4>(a, sms, st);
+  return launch<E, FMT, NB, 8>(a, sms, st);
+}
+
 template <class E, int FMT>
 hq_status launch_f(AttnArgs& a, int sms, cudaStream_t st) {
   switch (row_eights(a.G * a.max_new)) {
-    case 1: return launch<E, FMT, 1>(a, sms, st);
-    case 2: return launch<E, FMT, 2>(a, sms, st);
-    case 3: return launch<E, FMT, 3>(a, sms, st);
-    default: return launch<E, FMT, 4>(a, sms, st);
+    case 1: return launch_w<E, FMT, 1>(a, sms, st);
+    case 2: return launch_w<E, FMT, 2>(a, sms, st);
+    case 3: return launch<E, FMT, 3, 8>(a, sms, st);
+    default: return launch<E, FMT, 4, 8>(a, sms, st);
   }
 }
 
-size_t counters_bytes(int sms) { return (static_cast<size_t>(sms) * 4 + 255) / 256 * 256; }
+constexpr int CTAS = 4;  // most on an SM
+size_t counters_bytes(int sms) { return (static_cast<size_t>(CTAS) * sms * 4 + 255) / 256 * 256; }
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -657,7 +841,7 @@ hq_status device_sms(int* sms) {
 
 size_t attn_workspace(int rows, int sms) {
   const int R = 8 * row_eights(rows);
-  return counters_bytes(sms) + static_cast<size_t>(2) * sms * R * (D + 4) * sizeof(float);
+  return counters_bytes(sms) + static_cast<size_t>(2) * CTAS * sms * R * (D + 4) * sizeof(float);
 }
 
 bool sizes_ok(const hq_kv8_cache* c, int Hq, int max_new) {

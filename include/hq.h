@@ -434,7 +434,7 @@ enum { HQ_KV8_E4M3 = 0, HQ_KV8_INT8 = 1 };
 #define HQ_KV8_V 8192
 #define HQ_KV8_KSCALE 16384 /* float32 */
 #define HQ_KV8_VSCALE 16388 /* float32; the bytes from 16392 on are padding */
-#define HQ_KV8_MAX_BATCH 4096
+#define HQ_KV8_MAX_BATCH 1024
 #define HQ_KV8_MAX_HEADS 1024
 #define HQ_KV8_TAIL 128     /* positions of the 16-bit tail: the two newest blocks */
 #define HQ_KV8_K_INDEX(r, d) (((((r) / 8) * 2 + (d) / 64) * 8 + (r) % 8) * 64 + (d) % 64)
