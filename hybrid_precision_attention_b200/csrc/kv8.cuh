@@ -78,6 +78,21 @@ __device__ __forceinline__ bool kv8_seq(const hq_kv8_cache& c, const int32_t* cu
   return true;
 }
 
+// Arguments of the attention kernels (strides in elements).
+struct Kv8AttnArgs {
+  hq_kv8_cache c;
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t q_tok, q_head, o_tok, o_head;
+  int Hq, G, N, max_new, window;
+  const int32_t* cu;
+  const int32_t* kv_len;
+  float scale;             // sm_scale * log2 e
+  unsigned int* counters;  // of pieces delivered, one for each CTA
+  float* parts;            // pieces of tasks that CTAs share
+};
+
 // scale of a block from the bits of its largest magnitude (an infinity's or
 // NaN's bits are the largest of all); float32 division, as the format says
 __device__ __forceinline__ float kv8_scale(uint32_t amax_bits, int fmt) {

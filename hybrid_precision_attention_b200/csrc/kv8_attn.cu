@@ -37,12 +37,16 @@
 // reference.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <type_traits>
 
 #include "kv8.cuh"
 
 namespace hq {
+size_t kv8_attn_tc_parts(int64_t rows, int sms);
+hq_status launch_kv8_attn_tc(const Kv8AttnArgs& a, int dtype, int sms, cudaStream_t st);
+
 namespace {
 
 constexpr float P_BIAS = 6.0f;     // log2 of the fp16 weight at both references
@@ -74,20 +78,6 @@ struct Cfg {
   static constexpr int FIXED = OBUF + RED + RING + WARPS * (SLOTS * 8 + AHEAD) + 32 * 8 + 16;
 };
 
-struct AttnArgs {
-  hq_kv8_cache c;
-  const void* q;
-  void* out;
-  float* lse;
-  int64_t q_tok, q_head, o_tok, o_head;
-  int Hq, G, N, max_new, window, groups;  // groups: tasks of a (sequence, kv head)
-  const int32_t* cu;
-  const int32_t* kv_len;
-  float scale;  // sm_scale * log2 e
-  unsigned int* counters;
-  float* parts;
-};
-
 // blocks of sequence s that its queries see: [begin, end)
 __device__ __forceinline__ void seq_blocks(const Kv8Seq& s, int window, int& begin, int& end) {
   begin = window > 0 ? max(0, s.first + 1 - window) / KV8_BLOCK : 0;
@@ -111,7 +101,7 @@ __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, int32_
 }
 
 template <class E, int FMT, int NB, int W>
-__global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_attn_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   using C = Cfg<NB, W>;
   constexpr int R = C::R, NG = C::NG, SLOTS = C::SLOTS, MT = C::MT, SLICE = C::SLICE, SLOT = C::SLOT;
   extern __shared__ __align__(128) uint8_t sm[];
@@ -176,7 +166,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
   // what it costs besides them; or, where every task is short and none need share
   // a CTA with another, one unit, so that no task is cut (its pieces' way through
   // the workspace takes longer than 24 blocks).
-  const uint32_t per_seq = c.Hkv * a.groups;  // tasks of a sequence
+  const uint32_t per_seq = c.Hkv;  // tasks of a sequence: its kv heads
   const uint32_t tasks = static_cast<uint32_t>(carry >> 32) * per_seq;
   const bool uncut = longest <= 24 && tasks <= gridDim.x;
   const uint32_t total = uncut ? tasks : static_cast<uint32_t>(carry) * per_seq;
@@ -192,7 +182,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
   // A task of the CTA's run: [t0, t1) of its blocks are ours (none where the run
   // begins behind them), `units` of the run.
   struct Task {
-    int b, h, grp, begin, blocks, t0, t1;
+    int b, h, begin, blocks, t0, t1;
     uint32_t units;
     Kv8Seq s;
   };
@@ -217,22 +207,18 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
     seq_of(k);
     const uint32_t rel = u - before_of(lo) * per_seq;
     const uint32_t each = uncut ? 1u : k.blocks + TASK_UNITS, task = rel / each;
-    k.h = task / a.groups;
-    k.grp = task - k.h * a.groups;
+    k.h = task;
     k.t0 = rel - task * each;
     span_of(u, k);
   };
   auto next_task = [&](uint32_t u, Task& k) {  // the task after k, which begins with unit u < u1
     k.t0 = 0;
-    if (++k.grp == a.groups) {
-      k.grp = 0;
-      if (++k.h == c.Hkv) {
-        k.h = 0;
-        do {
-          ++k.b;
-          seq_of(k);
-        } while (k.blocks == 0);
-      }
+    if (++k.h == c.Hkv) {
+      k.h = 0;
+      do {
+        ++k.b;
+        seq_of(k);
+      } while (k.blocks == 0);
     }
     span_of(u, k);
   };
@@ -250,7 +236,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
 
   // raw query rows 8 nb + g of a task (elements 16 t4 .. and 64 + 16 t4 ..)
   auto load_q = [&](const Task& k, int nb, uint4 (&v)[4]) {
-    const int r = k.grp * R + 8 * nb + g;
+    const int r = 8 * nb + g;
     if (r < k.s.n * a.G) {
       const E* p = static_cast<const E*>(a.q) + static_cast<int64_t>(k.s.row0 + r / a.G) * a.q_tok +
                    static_cast<int64_t>(k.h * a.G + r % a.G) * a.q_head + 16 * t4;
@@ -345,7 +331,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
   int ordinal = 0;
   for (uint32_t u = u_first;;) {
     const size_t bh = static_cast<size_t>(k.b) * c.Hkv + k.h;
-    const int row0 = k.grp * R, rows = k.s.n * a.G;
+    const int rows = k.s.n * a.G;
 
     // query rows as B operands: lane (g, t4) holds row g (+ 8 nb), elements
     // 64 j + 16 t4 + 4 u + {0..3} at step 4 j + u, the elements that the K codes'
@@ -381,7 +367,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         qs[nb][i] = __shfl_sync(0xffffffffu, mul, (2 * t4 + i) * 4) * a.scale;
-        const int rr = row0 + 8 * nb + 2 * t4 + i;
+        const int rr = 8 * nb + 2 * t4 + i;
         // rows past the last have zero queries: their reference starts at their
         // score, 0, and no tile of theirs is ever masked or out of range
         qp[nb][i] = rr < rows ? k.s.first + rr / a.G : INT_MAX;
@@ -391,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
       }
     }
     // positions of the task's first and last real rows
-    const int q_lo = k.s.first + row0 / a.G, q_hi = k.s.first + (min(row0 + R, rows) - 1) / a.G;
+    const int q_lo = k.s.first, q_hi = k.s.len - 1;
 
     float o[NB][8][4];
 #pragma unroll
@@ -623,7 +609,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
     constexpr int PART = R * (D + 4);
     float* part = a.parts + static_cast<size_t>(2 * blockIdx.x + (k.t0 == 0)) * PART;
     auto finish = [&](int r, float m, float e, float l, float4 x) {
-      const int rr = row0 + r;
+      const int rr = r;
       if (rr >= rows) return;
       // accumulators are at 2^(P_BIAS - E), the sum at 2^-m: the quotient's exponent
       const float f = m == -INFINITY ? 0.f : ex2(e - m - P_BIAS) / l;
@@ -783,7 +769,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
 constexpr int SMEM_MAX = 224 * 1024;  // of an SM: 228 KB less 1 KB for each of up to four CTAs
 
 template <class E, int FMT, int NB, int W>
-hq_status launch(AttnArgs& a, int sms, cudaStream_t st) {
+hq_status launch(Kv8AttnArgs& a, int sms, cudaStream_t st) {
   using C = Cfg<NB, W>;
   static_assert(C::FIXED % 8 == 0 && C::FIXED + HQ_KV8_MAX_BATCH * 8 <= SMEM_MAX / C::CTAS, "shared memory of the largest batch");
   int dev = 0;
@@ -794,15 +780,15 @@ hq_status launch(AttnArgs& a, int sms, cudaStream_t st) {
     return cudaFuncSetAttribute(kv8_attn_kernel<E, FMT, NB, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX / C::CTAS);
   });
   if (e != cudaSuccess) return cuda_fail(e, "kv8 attention setup");
-  a.groups = (a.G * a.max_new + C::R - 1) / C::R;
   // units are counted in 32 bits
-  if (static_cast<double>(a.c.B) * a.c.Hkv * a.groups * (a.c.cap / KV8_BLOCK + TASK_UNITS) >= 4e9) return HQ_ERR_UNSUPPORTED;
+  if (static_cast<double>(a.c.B) * a.c.Hkv * (a.c.cap / KV8_BLOCK + TASK_UNITS) >= 4e9) return HQ_ERR_UNSUPPORTED;
   kv8_attn_kernel<E, FMT, NB, W><<<C::CTAS * sms, C::THREADS, C::FIXED + a.c.B * 8, st>>>(a);
   return cuda_status(cudaGetLastError(), "kv8 attention launch");
 }
 
-// Rows of a task, in eights: as many as there are, up to 4; beyond that tasks of 32 rows.
-int row_eights(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }
+// Rows of a kv head, in eights.
+constexpr int ROWS_MAX = 32;  // more go to the tcgen05 kernel
+int row_eights(int64_t rows) { return static_cast<int>((rows + 7) / 8); }
 
 // One CTA of 8 warps on an SM, or two of 4.  Where CTAs finish several tasks
 // each, one of two streams while the other joins its warps' results (64
@@ -810,14 +796,14 @@ int row_eights(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 
 // twice the pieces are to be joined and twice the plans made (one 32K sequence:
 // 24.8 us against 22.2 us).
 template <class E, int FMT, int NB>
-hq_status launch_w(AttnArgs& a, int sms, cudaStream_t st) {
-  if (static_cast<int64_t>(a.c.B) * a.c.Hkv * ((a.G * a.max_new + 8 * NB - 1) / (8 * NB)) >= 2 * sms)
+hq_status launch_w(Kv8AttnArgs& a, int sms, cudaStream_t st) {
+  if (static_cast<int64_t>(a.c.B) * a.c.Hkv >= 2 * sms)
     return launch<E, FMT, NB, 4>(a, sms, st);
   return launch<E, FMT, NB, 8>(a, sms, st);
 }
 
 template <class E, int FMT>
-hq_status launch_f(AttnArgs& a, int sms, cudaStream_t st) {
+hq_status launch_f(Kv8AttnArgs& a, int sms, cudaStream_t st) {
   switch (row_eights(a.G * a.max_new)) {
     case 1: return launch_w<E, FMT, 1>(a, sms, st);
     case 2: return launch_w<E, FMT, 2>(a, sms, st);
@@ -839,9 +825,10 @@ hq_status device_sms(int* sms) {
   return cuda_status(e, "device query");
 }
 
-size_t attn_workspace(int rows, int sms) {
-  const int R = 8 * row_eights(rows);
-  return counters_bytes(sms) + static_cast<size_t>(2) * CTAS * sms * R * (D + 4) * sizeof(float);
+size_t attn_workspace(int64_t rows, int sms) {
+  const size_t parts = rows > ROWS_MAX ? kv8_attn_tc_parts(rows, sms)
+                                       : static_cast<size_t>(2) * CTAS * sms * 8 * std::max(row_eights(rows), 1) * (D + 4);
+  return counters_bytes(sms) + parts * sizeof(float);
 }
 
 bool sizes_ok(const hq_kv8_cache* c, int Hq, int max_new) {
@@ -860,7 +847,7 @@ size_t hq_kv8_attn_workspace_bytes(const hq_kv8_cache* c, int32_t Hq, int32_t ma
   if (hq::kv8_validate(c) != HQ_OK || !hq::sizes_ok(c, Hq, max_new)) return 0;
   int sms = 148;  // without a device: the B200's
   if (hq::device_sms(&sms) != HQ_OK) sms = 148;
-  return hq::attn_workspace(Hq / c->Hkv * max_new, sms);
+  return hq::attn_workspace(static_cast<int64_t>(Hq / c->Hkv) * max_new, sms);
 }
 
 hq_status hq_kv8_attn(const hq_kv8_cache* c, int32_t dtype, const void* q, int64_t q_tok, int64_t q_head, int32_t Hq,
@@ -877,8 +864,8 @@ hq_status hq_kv8_attn(const hq_kv8_cache* c, int32_t dtype, const void* q, int64
   int sms = 0;
   const hq_status ds = hq::device_sms(&sms);
   if (ds != HQ_OK) return ds;
-  if (!hq::aligned16(ws) || ws_bytes < hq::attn_workspace(Hq / c->Hkv * max_new, sms)) return HQ_ERR_WORKSPACE;
-  hq::AttnArgs a = {};
+  if (!hq::aligned16(ws) || ws_bytes < hq::attn_workspace(static_cast<int64_t>(Hq / c->Hkv) * max_new, sms)) return HQ_ERR_WORKSPACE;
+  hq::Kv8AttnArgs a = {};
   a.c = *c;
   a.q = q;
   a.out = out;
@@ -898,6 +885,7 @@ hq_status hq_kv8_attn(const hq_kv8_cache* c, int32_t dtype, const void* q, int64
   a.counters = static_cast<unsigned int*>(ws);
   a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + hq::counters_bytes(sms));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (static_cast<int64_t>(a.G) * max_new > hq::ROWS_MAX) return hq::launch_kv8_attn_tc(a, dtype, sms, s);
   if (dtype == HQ_F16)
     return c->fmt == HQ_KV8_E4M3 ? hq::launch_f<__half, HQ_KV8_E4M3>(a, sms, s) : hq::launch_f<__half, HQ_KV8_INT8>(a, sms, s);
   return c->fmt == HQ_KV8_E4M3 ? hq::launch_f<__nv_bfloat16, HQ_KV8_E4M3>(a, sms, s)

@@ -1,0 +1,889 @@
+// kv8_attn_tc.cu — attention of many new tokens (prompt chunks, long drafts) over
+// the 8-bit block cache on tcgen05 tensor cores.
+//
+// The rows of a kv head (its G query heads x the sequence's n new tokens, row
+// r = i G + g, so that a page is read once for all of them) are taken NT x 128
+// at a time, one TMEM lane a row.  Keys go by tiles of two pages (128 positions):
+//   S = Q K^T    kind::f16, K the page's codes as fp16 (exact), 128 x 128
+//   P = 2^(S s_k - m) s_v 2^(m - E + 6) as fp16 (the block's scales in float32)
+//   O += P V     kind::f16, V the page's codes as fp16
+// with the two running references m, E of kv8_attn.cu: set to the exact maxima
+// only when a row's sum of weights in a tile passes 2^8, or a value scale passes
+// its reference by 2.
+//
+// Warps of a CTA (one CTA an SM, persistent):
+//   0-7    softmax: two streams of 128 threads, a row each.  NT = 2: the streams
+//          are two row tiles over the same key tiles; NT = 1 (up to 128 rows):
+//          the same rows, each stream taking every other key tile, joined at the end
+//   8-11   converters: codes of a page -> fp16 in the 128-byte-swizzled operand
+//          layouts, K as [key][d], V as [d][key], both K-major.  The page's V
+//          order gives a thread 4 keys of one d, which it stores as 8 bytes: the
+//          keys of 16 stand as t, t+1, t+8, t+9 for t = 0, 2, 4, 6, and P's
+//          columns follow the same order
+//   12     copies of the pages' codes, K and V apart (bulk copies, no multicast)
+//   13     TMEM allocation, tcgen05.mma issue (event-driven, one thread)
+// Bound: the tensor cores and the exponential unit alike (128 rows x 128 keys:
+// 1024 cycles of products, 1024 cycles of exponentials); the conversion of a
+// tile, about 700 cycles of four warps, runs beside them.
+//
+// Work: runs of equal units (key tiles) as in kv8_attn.cu; pieces of a task that
+// CTAs share are joined by the CTA that delivers the last one, in order.
+// All waits are bounded (about 1 s): a timeout sets the sequence's error bit and
+// the CTA drains its copies and products before it releases TMEM.
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "kv8.cuh"
+#include "tc.cuh"
+
+namespace hq {
+namespace {
+
+constexpr int TR = 128, TK = 128;          // rows of a tile, keys of a tile
+constexpr int W_CONV = 8, W_COPY = 12, W_MMA = 13;
+constexpr int THREADS = 14 * 32;
+constexpr float BIAS = 6.0f;               // log2 of the fp16 weight at both references
+constexpr float SUM_LIMIT = 256.0f;        // a tile's sum of weights (2^8): above it m is set anew
+constexpr float V_LIMIT = 128.0f;          // 2^(BIAS + 1); 2^8 * 2^7 < 65504
+constexpr int TASK_UNITS = 4;              // what a task costs besides its tiles, in tiles
+constexpr uint32_t TMEM_COLS = 512;        // S of the streams 0 .. 255, O 256 .. 511
+constexpr uint32_t TM_S = 0, TM_O = 256;
+constexpr uint32_t IDESC = idesc_make(0, 0, 0, TR, TK);  // fp16, K-major A and B, f32 accumulate
+constexpr int HALF = HQ_KV8_V;             // bytes of a page's K (or V) codes
+
+// shared memory (from a 1024-byte aligned base): operands as 128-byte-swizzled
+// regions of [128][128 B]
+template <int NT>
+struct Lay {
+  static constexpr int Q = 0;                    // NT x 2 regions (d halves)
+  static constexpr int K = Q + NT * 32768;       // 2 regions (d halves): [key][64 d]
+  static constexpr int V = K + 32768;            // 2 regions (pages): [d][64 keys]
+  static constexpr int P = V + 32768;            // 2 streams x 2 regions (pages): [row][64 keys]
+  static constexpr int RAW = P + 65536;          // codes: slots of a page's K or V
+  static constexpr int RK = NT == 2 ? 2 : 4;     // slots of K; as many of V
+  static constexpr int AUX = RAW + 2 * RK * HALF;  // scales: 8 tiles x 2 pages x (K, V); the tail's 64 K and 64 V scales
+  static constexpr int BARS = AUX + 8 * 16 + 512;
+  static constexpr int MISC = BARS + 32 * 8;     // TMEM base, flags, the plan's sums, 32 looked-up pages
+  static constexpr int JOIN = RAW;               // NT = 1: (m, E, l) of stream 1's rows, once the task's copies are done with
+  static constexpr int BYTES = MISC + 80 + 256 + 1024;  // with the alignment
+};
+
+// Key tiles of row group grp of a sequence: blocks [begin, end) and the positions
+// of its first and last row.
+struct Span {
+  int begin, end, q_lo, q_hi;
+};
+template <int NT>
+__device__ __forceinline__ Span span_of(const Kv8Seq& s, int G, int window, int grp) {
+  Span x;
+  const int rows = s.n * G, r0 = grp * NT * TR;
+  x.q_lo = s.first + r0 / G;
+  x.q_hi = s.first + (min(r0 + NT * TR, rows) - 1) / G;
+  x.begin = window > 0 ? max(0, x.q_lo + 1 - window) / KV8_BLOCK : 0;
+  x.end = x.q_hi / KV8_BLOCK + 1;
+  return x;
+}
+__device__ __forceinline__ int tiles_of(const Span& x) { return (x.end - x.begin + 1) / 2; }
+
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int32_t* err, volatile int* stop) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*stop) return false;
+    if (global_ns() - t0 > 1000000000ull) {
+      atomicOr(reinterpret_cast<unsigned int*>(err), HQ_DEVERR_TIMEOUT);
+      *stop = 1;
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
+template <class E, int FMT, int NT>
+__global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
+  using L = Lay<NT>;
+  constexpr int RK = L::RK, ROWS = NT * TR;
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BARS);
+  uint64_t *rk_full = bars, *rk_empty = bars + 4, *rv_full = bars + 8, *rv_empty = bars + 12, *s_full = bars + 16, *s_free = bars + 18,
+           *p_full = bars + 20, *o_done = bars + 22;
+  uint64_t &k_full = bars[24], &k_empty = bars[25], &v_full = bars[26], &v_empty = bars[27], &drain = bars[28];
+  uint32_t& tmem_sh = *reinterpret_cast<uint32_t*>(sm + L::MISC);
+  int* flags = reinterpret_cast<int*>(sm + L::MISC + 4);                  // stop, last
+  uint32_t* sums = reinterpret_cast<uint32_t*>(sm + L::MISC + 16);        // [warps]
+  uint64_t* looked = reinterpret_cast<uint64_t*>(sm + L::MISC + 80);      // [32] pages to copy
+  float* joined = reinterpret_cast<float*>(sm + L::JOIN);                 // [3][TR]
+  uint32_t* prefix = reinterpret_cast<uint32_t*>(sm + L::Q);  // units of the sequences before b, of one kv head: until the queries come
+  static_assert(HQ_KV8_MAX_BATCH * 4 <= 32768, "the plan fits where the queries go");
+  const hq_kv8_cache& c = a.c;
+  const int B = c.B;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---------------------------------------------------------------- plan
+  uint32_t carry = 0;
+  for (int b0 = 0; b0 < B; b0 += THREADS) {
+    const int b = b0 + threadIdx.x;
+    uint32_t n = 0;
+    if (b < B) {
+      Kv8Seq s;
+      kv8_seq(c, a.cu, a.kv_len, a.N, a.max_new, b, blockIdx.x == 0, s);
+      const int groups = (s.n * a.G + ROWS - 1) / ROWS;
+      for (int i = 0; i < groups; ++i) n += tiles_of(span_of<NT>(s, a.G, a.window, i)) + TASK_UNITS;
+    }
+    uint32_t x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    uint32_t before = carry;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) before += sums[w];
+      carry += sums[w];
+    }
+    if (b < B) prefix[b] = before + x - n;
+    __syncthreads();
+  }
+  const uint32_t total = carry * c.Hkv, parts = min(total, gridDim.x);
+  if (blockIdx.x >= parts) return;
+  const uint32_t run = total / parts, more = total - run * parts;
+  const uint32_t u0 = run * blockIdx.x + min(blockIdx.x, more), u1 = u0 + run + (blockIdx.x < more);
+  auto cta_of = [&](uint32_t u) { return u < more * (run + 1) ? u / (run + 1) : more + (u - more * (run + 1)) / run; };
+  struct Task {
+    int b, h, grp, tiles, t0, t1;  // key tiles [t0, t1) are ours (none where the run begins behind them)
+    uint32_t units;
+    Kv8Seq s;
+    Span sp;
+  };
+  auto enter = [&](uint32_t u, Task& k) {
+    k.sp = span_of<NT>(k.s, a.G, a.window, k.grp);
+    k.tiles = tiles_of(k.sp);
+    k.units = min(static_cast<uint32_t>(k.tiles + TASK_UNITS - k.t0), u1 - u);
+    k.t1 = min(k.tiles, k.t0 + static_cast<int>(k.units));
+  };
+  auto task_at = [&](uint32_t u, Task& k) {
+    const uint32_t want = u / c.Hkv;
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= want) lo = mid; else hi = mid;
+    }
+    k.b = lo;
+    kv8_seq(c, a.cu, a.kv_len, a.N, a.max_new, lo, false, k.s);
+    const uint32_t each = (lo + 1 < B ? prefix[lo + 1] : carry) - prefix[lo];  // units of a kv head
+    uint32_t rel = u - prefix[lo] * c.Hkv;
+    k.h = rel / each;
+    rel -= k.h * each;
+    for (k.grp = 0;; ++k.grp) {
+      const uint32_t n = tiles_of(span_of<NT>(k.s, a.G, a.window, k.grp)) + TASK_UNITS;
+      if (rel < n) break;
+      rel -= n;
+    }
+    k.t0 = rel;
+    enter(u, k);
+  };
+  auto next_task = [&](uint32_t u, Task& k) {
+    k.t0 = 0;
+    if (++k.grp * ROWS >= k.s.n * a.G) {
+      k.grp = 0;
+      if (++k.h == c.Hkv) {
+        k.h = 0;
+        do {
+          ++k.b;
+          kv8_seq(c, a.cu, a.kv_len, a.N, a.max_new, k.b, false, k.s);
+        } while (k.s.n == 0);
+      }
+    }
+    enter(u, k);
+  };
+  uint32_t u = u0;
+  Task k;
+  task_at(u, k);
+  if (k.t0 >= k.tiles) {  // the run begins behind a task's tiles
+    u += k.units;
+    if (u >= u1) return;
+    next_task(u, k);
+  }
+
+  // ---------------------------------------------------------------- setup
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < RK; ++i) {
+      mbar_init(rk_full + i, 1);
+      mbar_init(rk_empty + i, 128);
+      mbar_init(rv_full + i, 1);
+      mbar_init(rv_empty + i, 128);
+    }
+    mbar_init(&k_full, 128);
+    mbar_init(&k_empty, 1);
+    mbar_init(&v_full, 128);
+    mbar_init(&v_empty, 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(s_full + g, 1);
+      mbar_init(s_free + g, 128);
+      mbar_init(p_full + g, 128);
+      mbar_init(o_done + g, 1);
+    }
+    mbar_init(&drain, 1);
+    flags[0] = 0;
+    fence_mbar_init();
+  }
+  if (warp == W_MMA) {
+    tmem_alloc(&tmem_sh, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  const uint32_t base = smem_u32(sm);
+  volatile int* stop = flags;
+  float* aux = reinterpret_cast<float*>(sm + L::AUX);
+  float* tail_sc = aux + 8 * 4;  // [K, V][64]
+
+  // running uses of each barrier, kept by the roles that wait on it; a tile that
+  // stream g takes is its j-th: NT = 2 every tile, NT = 1 every other
+  int n_raw = 0, issued = 0;      // copied pages (copy warp, converters)
+  int n_tile = 0;                 // tiles (converters, MMA, aux slot of the softmax)
+  int n_str[2] = {0, 0};          // tiles of each stream (softmax, MMA)
+  bool ok = true;
+  auto takes = [&](int g, int t) { return NT == 2 || (t & 1) == g; };
+
+  while (true) {
+    const size_t bh = static_cast<size_t>(k.b) * c.Hkv + k.h;
+    const int row0 = k.grp * ROWS, rows = k.s.n * a.G;
+    const int nt = k.t1 - k.t0;
+    const int full_end = min(k.sp.end, k.s.len / KV8_BLOCK);  // complete blocks end here; the next one, if any, is the tail
+    int32_t* err = c.err + k.b;
+    auto pages_in = [&](int t) {  // complete pages of tile t: 0 .. 2
+      const int p = k.sp.begin + 2 * (k.t0 + t);
+      return max(0, min(2, full_end - p));
+    };
+
+    // ---------------------------------------------------------- queries -> shared memory
+    float qmul = a.scale;
+    if (warp < 8 && (NT == 2 || warp < 4)) {
+      const int r = threadIdx.x & 127, rr = row0 + (NT == 2 ? (warp >> 2) * TR : 0) + r;
+      const uint32_t dst = base + L::Q + (NT == 2 ? (warp >> 2) * 32768 : 0) + r * 128;
+      const E* p = static_cast<const E*>(a.q) + static_cast<int64_t>(k.s.row0 + rr / a.G) * a.q_tok +
+                   static_cast<int64_t>(k.h * a.G + rr % a.G) * a.q_head;
+      float inv = 1.0f;
+      if (IsBf16<E>::value && rr < rows) {
+        // bf16 rows become fp16 at a power of two that brings their largest value to [2^14, 2^15)
+        uint32_t m = 0;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+          E e[8];
+          *reinterpret_cast<uint4*>(e) = reinterpret_cast<const uint4*>(p)[i];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(to_float(e[j])) & 0x7fffffffu);
+        }
+        if (m != 0 && m < 0x7f800000u) {
+          const int ex = max(static_cast<int>(m >> 23) - 127 - 14, -126);
+          qmul *= __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+          inv = ex == -126 ? 0x1p126f : __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        }
+      }
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (rr < rows) {
+          E e[8];
+          *reinterpret_cast<uint4*>(e) = reinterpret_cast<const uint4*>(p)[i];
+          if (IsBf16<E>::value) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = pack_f16x2(to_float(e[2 * j]) * inv, to_float(e[2 * j + 1]) * inv);
+          } else {
+            *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(e);
+          }
+        }
+        sts128(dst + (i >> 3) * 16384 + (((i & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+      }
+      fence_proxy_async_smem();
+    }
+    if (NT == 1 && warp >= 4 && warp < 8) {
+      // stream 1 scores the same rows
+      const int rr = row0 + (threadIdx.x & 127);
+      if (IsBf16<E>::value && rr < rows) {
+        const E* p = static_cast<const E*>(a.q) + static_cast<int64_t>(k.s.row0 + rr / a.G) * a.q_tok +
+                     static_cast<int64_t>(k.h * a.G + rr % a.G) * a.q_head;
+        uint32_t m = 0;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+          E e[8];
+          *reinterpret_cast<uint4*>(e) = reinterpret_cast<const uint4*>(p)[i];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(to_float(e[j])) & 0x7fffffffu);
+        }
+        if (m != 0 && m < 0x7f800000u)
+          qmul *= __uint_as_float(static_cast<uint32_t>(max(static_cast<int>(m >> 23) - 127 - 14, -126) + 127) << 23);
+      }
+    }
+    __syncthreads();
+
+    if (warp == W_COPY) {
+      // -------------------------------------------------------- copies
+      // 32 pages looked up at a time; lane 0 copies the K codes, lane 1 the V codes,
+      // each as its slots come free
+      const int p_begin = k.sp.begin + 2 * k.t0, p_end = min(full_end, k.sp.begin + 2 * k.t1);
+      for (int p = p_begin; p < p_end; p += 32) {
+        const int m = min(32, p_end - p);
+        if (lane < m) looked[lane] = reinterpret_cast<uint64_t>(kv8_page(c, bh, p + lane));
+        __syncwarp();
+        if (lane < 2) {
+          uint64_t* e = lane ? rv_empty : rk_empty;
+          uint64_t* f = lane ? rv_full : rk_full;
+          for (int i = 0; ok && i < m; ++i) {
+            const int n = n_raw + i, st = n % RK;
+            if (n >= RK) ok = wait_for(e + st, (n / RK - 1) & 1, err, stop);
+            if (!ok) break;
+            mbar_arrive_expect_tx(f + st, HALF);
+            bulk_g2s(sm + L::RAW + (lane * RK + st) * HALF, reinterpret_cast<const uint8_t*>(looked[i]) + lane * HQ_KV8_V, HALF, f + st);
+            issued = n + 1;
+          }
+        }
+        __syncwarp();
+        n_raw += m;
+      }
+    } else if (warp >= W_CONV && warp < W_COPY) {
+      // -------------------------------------------------------- converters
+      const int ct = threadIdx.x - W_CONV * 32, cw = ct >> 5;  // thread of 128, warp of 4
+      const int g = lane >> 2, t4 = lane & 3;
+      // scale of (page ct / 2, K or V) of tile t: fetched a tile ahead
+      auto scale_of = [&](int t) {
+        if (t >= nt || ct >= 2 * pages_in(t)) return 1.0f;
+        const uint8_t* page = kv8_page(c, bh, k.sp.begin + 2 * (k.t0 + t) + (ct >> 1));
+        return *reinterpret_cast<const float*>(page + (ct & 1 ? HQ_KV8_VSCALE : HQ_KV8_KSCALE));
+      };
+      float scale = scale_of(0);
+      for (int t = 0; ok && t < nt; ++t, ++n_tile) {
+        const int np = pages_in(t), p0 = k.sp.begin + 2 * (k.t0 + t);
+        const bool tail = p0 + np < k.sp.end && np < 2;  // the tile's page np is the incomplete block
+        // ---- K: the operand is free once the tile before has been scored
+        if (n_tile > 0) ok = wait_for(&k_empty, (n_tile - 1) & 1, err, stop);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (ct < 4) aux[(n_tile & 7) * 4 + ct] = scale;
+        scale = scale_of(t + 1);
+        for (int pg = 0; pg < np; ++pg) {
+          const int st = (n_raw + pg) % RK;
+          ok = wait_for(rk_full + st, ((n_raw + pg) / RK) & 1, err, stop);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint4* src = reinterpret_cast<const uint4*>(sm + L::RAW + st * HALF);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int e = cw * 4 + i;  // 512-byte piece: 8 tokens x 64 d
+            const uint4 x = src[e * 32 + lane];
+            uint32_t y[8];
+            kv8_half4<FMT>(x.x, y[0], y[1]);
+            kv8_half4<FMT>(x.y, y[2], y[3]);
+            kv8_half4<FMT>(x.z, y[4], y[5]);
+            kv8_half4<FMT>(x.w, y[6], y[7]);
+            const uint32_t row = base + L::K + (e & 1) * 16384 + (pg * 64 + (e >> 1) * 8 + g) * 128;
+            sts128(row + (((2 * t4) ^ g) << 4), y[0], y[1], y[2], y[3]);
+            sts128(row + (((2 * t4 + 1) ^ g) << 4), y[4], y[5], y[6], y[7]);
+          }
+          mbar_arrive(rk_empty + st);
+        }
+        if (!ok) break;
+        const size_t half = bh * 2 + ((p0 + np) & 1);
+        if (tail) {
+          const uint4* src = reinterpret_cast<const uint4*>(c.tail_k + half * KV8_BLOCK * D);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int e = cw * 4 + i;
+            const uint4 x = src[(e * 32 + lane) * 2], y = src[(e * 32 + lane) * 2 + 1];
+            const uint32_t row = base + L::K + (e & 1) * 16384 + (np * 64 + (e >> 1) * 8 + g) * 128;
+            sts128(row + (((2 * t4) ^ g) << 4), x.x, x.y, x.z, x.w);
+            sts128(row + (((2 * t4 + 1) ^ g) << 4), y.x, y.y, y.z, y.w);
+          }
+          // the rows' scales; past the length 1: nothing there is seen
+          const int which = ct >> 6, r = ct & 63;
+          tail_sc[ct] = (p0 + np) * KV8_BLOCK + r < k.s.len
+                            ? c.tail_scale[(bh * 2 + which) * HQ_KV8_TAIL + ((p0 + np) & 1) * KV8_BLOCK + r]
+                            : 1.0f;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&k_full);
+        // ---- V: free once the tile before has been added
+        if (n_tile > 0) ok = wait_for(&v_empty, (n_tile - 1) & 1, err, stop);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        // 16-byte chunk (16 tokens tt, 32 d dq, d % 8 = g, token pair t4): 4 words of 4 tokens of one d
+        auto vrow = [&](int pg, int d) { return base + L::V + pg * 16384 + d * 128; };
+        for (int pg = 0; pg < np; ++pg) {
+          const int st = (n_raw + pg) % RK;
+          ok = wait_for(rv_full + st, ((n_raw + pg) / RK) & 1, err, stop);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint4* src = reinterpret_cast<const uint4*>(sm + L::RAW + (RK + st) * HALF);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int tt = cw, dq = i;
+            const uint4 x = src[(tt * 4 + dq) * 32 + lane];
+            const uint32_t col = (((tt * 2 + (t4 >> 1)) ^ g) << 4) + (t4 & 1) * 8;
+            uint32_t y[2];
+            kv8_half4<FMT>(x.x, y[0], y[1]);
+            sts64(vrow(pg, dq * 32 + g) + col, y[0], y[1]);
+            kv8_half4<FMT>(x.y, y[0], y[1]);
+            sts64(vrow(pg, dq * 32 + 8 + g) + col, y[0], y[1]);
+            kv8_half4<FMT>(x.z, y[0], y[1]);
+            sts64(vrow(pg, dq * 32 + 16 + g) + col, y[0], y[1]);
+            kv8_half4<FMT>(x.w, y[0], y[1]);
+            sts64(vrow(pg, dq * 32 + 24 + g) + col, y[0], y[1]);
+          }
+          mbar_arrive(rv_empty + st);
+        }
+        if (!ok) break;
+        for (int pg = np; pg < 2; ++pg) {
+          // the tail's values, or zeros where the tile ends: a weight of 0 must not meet what is left there
+          const bool have = tail && pg == np;
+          const uint4* src = reinterpret_cast<const uint4*>(c.tail_v + half * KV8_BLOCK * D);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t col = (((cw * 2 + (t4 >> 1)) ^ g) << 4) + (t4 & 1) * 8;
+            uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+            if (have) {
+              x = src[((cw * 4 + i) * 32 + lane) * 2];
+              y = src[((cw * 4 + i) * 32 + lane) * 2 + 1];
+            }
+            sts64(vrow(pg, i * 32 + g) + col, x.x, x.y);
+            sts64(vrow(pg, i * 32 + 8 + g) + col, x.z, x.w);
+            sts64(vrow(pg, i * 32 + 16 + g) + col, y.x, y.y);
+            sts64(vrow(pg, i * 32 + 24 + g) + col, y.z, y.w);
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&v_full);
+        n_raw += np;
+      }
+    } else if (warp == W_MMA) {
+      // -------------------------------------------------------- MMA issue
+      if (lane == 0 && ok) {
+        const uint32_t Ks = base + L::K, Vs = base + L::V;
+        auto issue_qk = [&](int g) {
+          tc_fence_after();
+          const uint32_t Qs = base + L::Q + (NT == 2 ? g * 32768 : 0);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * 16384 + 32 * (kk & 3);
+            umma_f16(tmem + TM_S + 128 * g, sdesc_sw128(Qs + off, 16, 1024), sdesc_sw128(Ks + off, 16, 1024), IDESC, kk > 0);
+          }
+          umma_commit(s_full + g);
+        };
+        auto issue_pv = [&](int g, bool first) {
+          tc_fence_after();
+          const uint32_t Ps = base + L::P + g * 32768;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * 16384 + 32 * (kk & 3);
+            umma_f16(tmem + TM_O + 128 * g, sdesc_sw128(Ps + off, 16, 1024), sdesc_sw128(Vs + off, 16, 1024), IDESC,
+                     !first || kk > 0 ? 1u : 0u);
+          }
+          umma_commit(o_done + g);
+        };
+        // whichever of the streams' QK and PV is ready goes next; a tile's operand is
+        // released when every stream that takes it has been issued
+        int tq[2], tp[2], jq[2], jp[2];  // next tile of each stream to score / to add, and its number in the stream
+        for (int g = 0; g < 2; ++g) {
+          tq[g] = tp[g] = NT == 2 ? 0 : g;
+          jq[g] = jp[g] = n_str[g];
+        }
+        const int step = NT == 2 ? 1 : 2;
+        uint64_t t_last = global_ns();
+        while (tp[0] < nt || tp[1] < nt) {
+          bool progress = false;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int t = tq[g];
+            if (t < nt && mbar_test_wait(&k_full, (n_tile + t) & 1) && (jq[g] == 0 || mbar_test_wait(s_free + g, (jq[g] - 1) & 1))) {
+              // NT = 1: the barrier's phase tells tile t from t - 2 only while t - 1 is scored
+              if (NT == 2 || tq[g ^ 1] == t + 1 || tq[g ^ 1] >= nt) {
+                issue_qk(g);
+                if (NT == 1 || tq[g ^ 1] > t) umma_commit(&k_empty);
+                tq[g] = t + step;
+                ++jq[g];
+                progress = true;
+              }
+            }
+            const int p = tp[g];
+            if (p < tq[g] && p < nt && mbar_test_wait(p_full + g, jp[g] & 1) && mbar_test_wait(&v_full, (n_tile + p) & 1)) {
+              if (NT == 2 || tp[g ^ 1] == p + 1 || tp[g ^ 1] >= nt) {
+                issue_pv(g, p < step);
+                if (NT == 1 || tp[g ^ 1] > p) umma_commit(&v_empty);
+                tp[g] = p + step;
+                ++jp[g];
+                progress = true;
+              }
+            }
+          }
+          if (progress) {
+            t_last = global_ns();
+          } else if (*stop) {
+            ok = false;
+            break;
+          } else if (global_ns() - t_last > 1000000000ull) {
+            atomicOr(reinterpret_cast<unsigned int*>(err), HQ_DEVERR_TIMEOUT);
+            *stop = 1;
+            ok = false;
+            break;
+          }
+        }
+        n_str[0] = jq[0];
+        n_str[1] = jq[1];
+      }
+      n_tile += nt;
+    } else {
+      // -------------------------------------------------------- softmax
+      const int g = warp >> 2, r = threadIdx.x & 127;
+      const int rr = row0 + (NT == 2 ? g * TR : 0) + r;  // row of the (sequence, kv head)
+      const bool real = rr < rows;
+      const int qpos = k.s.first + rr / a.G;
+      const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      const uint32_t srow = trow + TM_S + 128 * g, orow = trow + TM_O + 128 * g;
+      const uint32_t prow = base + L::P + g * 32768 + r * 128;
+      // rows past the last have zero queries and see every key
+      float m = real ? -INFINITY : 0.f, e = -INFINITY, l = 0.f, ef = 0.f;
+      bool any = false;  // a tile was taken
+      for (int t = 0; t < nt; ++t) {
+        if (!takes(g, t)) continue;
+        const int j = n_str[g];
+        ok = ok && wait_for(s_full + g, j & 1, err, stop);
+        if (any) ok = ok && wait_for(o_done + g, (j - 1) & 1, err, stop);  // P is free
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const int np = pages_in(t), p0 = k.sp.begin + 2 * (k.t0 + t);
+        const bool tail = np < 2 && p0 + np < k.sp.end;
+        const float4 sc = *reinterpret_cast<const float4*>(aux + ((n_tile + t) & 7) * 4);
+        // columns [lo, hi] of the tile are seen by this row
+        const int hi = real ? qpos - p0 * KV8_BLOCK : TK, lo = real && a.window > 0 ? hi - a.window + 1 : 0;
+        float vtop = fmaxf(np > 0 ? sc.y : 0.f, np > 1 ? sc.w : 0.f);  // ignores NaN
+        if (tail)
+          for (int i = 0; i < 64; ++i) vtop = fmaxf(vtop, tail_sc[64 + i]);
+        if (!(vtop > 0.f)) vtop = 1.f;
+
+        // scores of columns 32 c4 .. + 31 as exponents relative to mref: masked ones -inf.
+        // `seen`: all columns seen and no tail in the tile
+        const bool seen = __all_sync(0xffffffffu, !tail && np == 2 && hi >= TK - 1 && lo <= 0);
+        auto scores = [&](float (&x)[32], int c4, float mref) {
+          const float mul = qmul * (c4 < 2 ? sc.x : sc.z);
+          if (seen) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = fmaf(x[i], mul, -mref);
+          } else {
+            const bool tl = tail && (c4 >> 1) == np;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int col = 32 * c4 + i;
+              const float f = tl ? qmul * tail_sc[col & 63] : mul;
+              x[i] = col >= lo && col <= hi ? fmaf(x[i], f, -mref) : -INFINITY;
+            }
+          }
+        };
+        float sum = 0.f;
+        const int first = __any_sync(0xffffffffu, m == -INFINITY || ef * vtop > V_LIMIT) ? 1 : 0;
+        for (int pass = first; pass < 3; ++pass) {
+          if (pass == 1) {
+            // the references anew: the exact maximum of the tile
+            float mt = -INFINITY;
+#pragma unroll 1
+            for (int c4 = 0; c4 < 4; ++c4) {
+              float x[32];
+              tmem_ld32f(srow + 32 * c4, x);
+              tmem_wait_ld();
+              scores(x, c4, 0.f);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) mt = fmaxf(mt, x[i]);
+            }
+            const float m_new = fmaxf(m, mt), e_new = fmaxf(e, mt + log2f(vtop));
+            const float mb = m_new == -INFINITY ? 0.f : m_new, eb = e_new == -INFINITY ? 0.f : e_new;
+            l *= ex2(m - mb);
+            const float ao = ex2(e - eb);
+            m = m_new;
+            e = e_new;
+            // bounded, so that a weight that underflowed stays 0 beside a far larger earlier score
+            ef = e_new == -INFINITY ? 0.f : ex2(fminf(mb - eb + BIAS, 100.f));
+            if (any) {
+#pragma unroll 1
+              for (int c4 = 0; c4 < 4; ++c4) {
+                uint32_t y[32];
+                tmem_ld32(orow + 32 * c4, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * ao);
+                tmem_st32(orow + 32 * c4, y);
+              }
+              tmem_wait_st();
+            }
+            continue;
+          }
+          const float mref = m == -INFINITY ? 0.f : m;
+          // Weights of a page that is seen whole take its value scale w into the
+          // exponent, and their sum is divided by it: a product less per weight.
+          // Not where w is so small that weights would underflow.
+          const float w0 = ef * sc.y, w1 = ef * sc.w;
+          const bool plain = __all_sync(0xffffffffu, seen && w0 > 0x1p-60f && w1 > 0x1p-60f);
+          const float lw0 = plain ? log2f(w0) : 0.f, lw1 = plain ? log2f(w1) : 0.f;
+          sum = 0.f;
+          float s0 = 0.f, s1 = 0.f;
+          float x[32];
+          tmem_ld32f(srow, x);
+          tmem_wait_ld();
+#pragma unroll 1
+          for (int c4 = 0; c4 < 4; ++c4) {
+            uint32_t pk[16];
+            if (plain) {
+              scores(x, c4, mref - (c4 < 2 ? lw0 : lw1));
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float y0 = ex2(x[i]), y1 = ex2(x[i + 1]);
+                s0 += y0;
+                s1 += y1;
+                pk[i / 2] = pack_f16x2(y0, y1);
+              }
+              if (c4 & 1) {
+                sum += (s0 + s1) / (c4 < 2 ? w0 : w1);
+                s0 = s1 = 0.f;
+              }
+            } else {
+              scores(x, c4, mref);
+              const bool tl = tail && (c4 >> 1) == np;
+              const float w = c4 < 2 ? w0 : w1;
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                float y0 = ex2(x[i]), y1 = ex2(x[i + 1]);
+                sum += y0 + y1;
+                // a scale that is NaN stays behind the mask
+                const int col = (32 * c4 + i) & 63;
+                y0 = x[i] == -INFINITY ? 0.f : y0 * (tl ? ef * tail_sc[64 + col] : w);
+                y1 = x[i + 1] == -INFINITY ? 0.f : y1 * (tl ? ef * tail_sc[64 + col + 1] : w);
+                pk[i / 2] = pack_f16x2(y0, y1);
+              }
+            }
+            if (c4 < 3) tmem_ld32f(srow + 32 * (c4 + 1), x);  // the next columns, during the stores
+            // the keys of 16 in V's order: 0 1 8 9, 2 3 10 11, 4 5 12 13, 6 7 14 15
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const int chunk = (c4 & 1) * 4 + h * 2 + q;
+                sts128(prow + (c4 >> 1) * 16384 + ((chunk ^ (r & 7)) << 4), pk[h * 8 + 2 * q], pk[h * 8 + 2 * q + 4],
+                       pk[h * 8 + 2 * q + 1], pk[h * 8 + 2 * q + 5]);
+              }
+            if (c4 < 3) tmem_wait_ld();
+          }
+          if (pass == 2) break;
+          if (!__any_sync(0xffffffffu, !(sum <= SUM_LIMIT))) break;  // also an infinity or NaN
+        }
+        l += sum;
+        any = true;
+        ++n_str[g];
+        tc_fence_before();
+        mbar_arrive(s_free + g);
+        fence_proxy_async_smem();
+        mbar_arrive(p_full + g);
+      }
+      n_tile += nt;
+      if (any && ok) ok = wait_for(o_done + g, (n_str[g] - 1) & 1, err, stop);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+
+      // ------------------------------------------------------ the CTA's piece of the task
+      const bool whole = nt == k.tiles;
+      auto o_cols = [&](int c4, float (&x)[32]) {
+        tmem_ld32f(orow + 32 * c4, x);
+        tmem_wait_ld();
+      };
+      float* swap = reinterpret_cast<float*>(sm + L::P);  // [column][row]: the streams' weights are done with
+      if (NT == 1) {
+        // stream 1 hands its rows to stream 0, once both streams' products have read P
+        // and every code of the task has been converted
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+        if (g == 1) {
+          joined[r] = m;
+          joined[TR + r] = any ? e : -INFINITY;
+          joined[2 * TR + r] = l;
+        }
+        if (g == 1 && ok && any) {
+#pragma unroll 1
+          for (int c4 = 0; c4 < 4; ++c4) {
+            float x[32];
+            o_cols(c4, x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) swap[(32 * c4 + i) * TR + r] = x[i];
+          }
+        }
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+      }
+      // pieces: slot 2 cta (+ 1 for the task's first), [stream's rows][column][row] and (m, E, l)
+      constexpr int PIECE = TR * (D + 3);
+      const int q = NT == 2 ? g : 0;
+      float* part = a.parts + (static_cast<size_t>(2 * blockIdx.x + (k.t0 == 0)) * NT + q) * PIECE;
+      const uint32_t k0 = u - k.t0;
+      const int c0 = cta_of(k0), c1 = cta_of(k0 + k.tiles - 1);
+      const bool owner = NT == 2 || g == 0;  // threads that hold the piece's rows
+      float m2 = -INFINITY, e2 = -INFINITY, l2 = 0.f;
+      if (NT == 1 && owner && nt > 1) {
+        m2 = joined[r];
+        e2 = joined[TR + r];
+        l2 = joined[2 * TR + r];
+      }
+      const float mj = fmaxf(m, m2), ej = fmaxf(e, e2);
+      const float mb = mj == -INFINITY ? 0.f : mj, eb = ej == -INFINITY ? 0.f : ej;
+      const float lj = l * ex2(m - mb) + l2 * ex2(m2 - mb);
+      const float f1 = ej == -INFINITY ? 1.f : ex2(e - eb), f2 = ej == -INFINITY ? 1.f : ex2(e2 - eb);
+      auto write = [&](float m, float e, float l, auto cols) {  // the row's output from its accumulators
+        // accumulators are at 2^(BIAS - E), the sum at 2^-m
+        const float f = m == -INFINITY ? 0.f : ex2(e - m - BIAS) / l;
+        const int64_t tok = k.s.row0 + rr / a.G;
+        const int head = k.h * a.G + rr % a.G;
+        E* dst = static_cast<E*>(a.out) + tok * a.o_tok + head * a.o_head;
+#pragma unroll 1
+        for (int c4 = 0; c4 < 4; ++c4) {
+          float x[32];
+          cols(c4, x);
+          if (real) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              E y[8];
+#pragma unroll
+              for (int z = 0; z < 8; ++z) y[z] = from_float<E>(x[i + z] * f);
+              *reinterpret_cast<uint4*>(dst + 32 * c4 + i) = *reinterpret_cast<const uint4*>(y);
+            }
+          }
+        }
+        if (real && a.lse != nullptr) a.lse[tok * a.Hq + head] = m + log2f(l);
+      };
+      if (owner && ok) {
+        auto cols = [&](int c4, float (&x)[32]) {
+          o_cols(c4, x);
+          if (NT == 1) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = x[i] * f1 + (nt > 1 ? swap[(32 * c4 + i) * TR + r] * f2 : 0.f);
+          }
+        };
+        if (whole) {
+          write(mj, ej, lj, cols);
+        } else {
+#pragma unroll 1
+          for (int c4 = 0; c4 < 4; ++c4) {
+            float x[32];
+            cols(c4, x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) __stcg(part + (32 * c4 + i) * TR + r, x[i]);
+          }
+          __stcg(part + D * TR + r, mj);
+          __stcg(part + (D + 1) * TR + r, ej);
+          __stcg(part + (D + 2) * TR + r, lj);
+        }
+      }
+      if (!whole) {
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+        if (threadIdx.x == 0) {
+          // the barrier puts the CTA's writes before this release
+          const unsigned int before = atom_add_acq_rel_gpu(a.counters + c0, 1u);
+          const bool last = before == static_cast<unsigned int>(c1 - c0);
+          if (last) a.counters[c0] = 0u;
+          flags[1] = last;
+        }
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+        if (flags[1] && owner && ok) {
+          auto piece = [&](int p) { return a.parts + (static_cast<size_t>(2 * p + (p == c0)) * NT + q) * PIECE; };
+          float mm = -INFINITY, ee = -INFINITY, ll = 0.f;
+          for (int p = c0; p <= c1; ++p) {
+            mm = fmaxf(mm, __ldcg(piece(p) + D * TR + r));
+            ee = fmaxf(ee, __ldcg(piece(p) + (D + 1) * TR + r));
+          }
+          const float mmb = mm == -INFINITY ? 0.f : mm, eeb = ee == -INFINITY ? 0.f : ee;
+          for (int p = c0; p <= c1; ++p) ll += __ldcg(piece(p) + (D + 2) * TR + r) * ex2(__ldcg(piece(p) + D * TR + r) - mmb);
+          write(mm, ee, ll, [&](int c4, float (&x)[32]) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = 0.f;
+            for (int p = c0; p <= c1; ++p) {
+              const float* src = piece(p) + 32 * c4 * TR + r;
+              const float f = ex2(__ldcg(piece(p) + (D + 1) * TR + r) - eeb);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] += __ldcg(src + i * TR) * f;
+            }
+          });
+        }
+      }
+      tc_fence_before();
+    }
+    __syncwarp();
+    u += k.units;
+    const bool done = u >= u1 || *stop;
+    __syncthreads();  // the task's shared and tensor memory is free
+    tc_fence_after();
+    if (done || *stop) break;
+    next_task(u, k);
+  }
+
+  // Products and copies that were not waited for (only after a wait that gave up)
+  // end before TMEM and shared memory are given back.
+  if (warp == W_MMA) {
+    if (lane == 0) {
+      umma_commit(&drain);
+      int never = 0;
+      wait_for(&drain, 0, c.err, &never);
+    }
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+  if (warp == W_COPY && lane < 2 && *stop) {
+    int never = 0;
+    for (int i = max(0, issued - RK); i < issued; ++i) wait_for((lane ? rv_full : rk_full) + i % RK, (i / RK) & 1, c.err, &never);
+  }
+}
+
+template <class E, int FMT, int NT>
+hq_status launch(const Kv8AttnArgs& a, int sms, cudaStream_t st) {
+  using L = Lay<NT>;
+  static_assert(L::BYTES <= 227 * 1024, "shared memory of a CTA");
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "kv8 attention setup");
+  static DeviceOnce attrs;
+  e = attrs.run(dev, [] {
+    return cudaFuncSetAttribute(kv8_attn_tc_kernel<E, FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "kv8 attention setup");
+  // units are counted in 32 bits
+  const double groups = static_cast<double>(a.G) * a.max_new / (NT * TR) + 1;
+  if (groups * a.c.B * a.c.Hkv * (a.c.cap / TK + TASK_UNITS) >= 4e9) return HQ_ERR_UNSUPPORTED;
+  kv8_attn_tc_kernel<E, FMT, NT><<<sms, THREADS, L::BYTES, st>>>(a);
+  return cuda_status(cudaGetLastError(), "kv8 attention launch");
+}
+
+template <class E, int FMT>
+hq_status launch_f(const Kv8AttnArgs& a, int sms, cudaStream_t st) {
+  // one row tile with two streams over the keys, or two row tiles
+  return a.G * static_cast<int64_t>(a.max_new) <= TR ? launch<E, FMT, 1>(a, sms, st) : launch<E, FMT, 2>(a, sms, st);
+}
+
+}  // namespace
+
+// floats of the workspace's pieces for `rows` rows of a kv head
+size_t kv8_attn_tc_parts(int64_t rows, int sms) { return static_cast<size_t>(2) * sms * (rows <= TR ? 1 : 2) * TR * (D + 3); }
+
+hq_status launch_kv8_attn_tc(const Kv8AttnArgs& a, int dtype, int sms, cudaStream_t st) {
+  if (dtype == HQ_F16)
+    return a.c.fmt == HQ_KV8_E4M3 ? launch_f<__half, HQ_KV8_E4M3>(a, sms, st) : launch_f<__half, HQ_KV8_INT8>(a, sms, st);
+  return a.c.fmt == HQ_KV8_E4M3 ? launch_f<__nv_bfloat16, HQ_KV8_E4M3>(a, sms, st)
+                                : launch_f<__nv_bfloat16, HQ_KV8_INT8>(a, sms, st);
+}
+
+}  // namespace hq
