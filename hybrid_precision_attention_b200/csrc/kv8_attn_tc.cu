@@ -6,25 +6,27 @@
 // at a time, one TMEM lane a row.  Keys go by tiles of two pages (128 positions):
 //   S = Q K^T    kind::f16, K the page's codes as fp16 (exact), 128 x 128
 //   P = 2^(S s_k - m) s_v 2^(m - E + 6) as fp16 (the block's scales in float32)
-//   O += P V     kind::f16, V the page's codes as fp16
-// with the two running references m, E of kv8_attn.cu: set to the exact maxima
-// only when a row's sum of weights in a tile passes 2^8, or a value scale passes
-// its reference by 2.
+//   O += P V     kind::f16, P from TMEM (where it takes the place of S), V the
+//                page's codes as fp16
+// with the two running references m, E of kv8_attn.cu: they are set to the exact
+// maxima only when 32 of a row's weights sum to more than 2^15, whereupon what the
+// row has so far (sum, O, the tile's P) is rescaled.
 //
 // Warps of a CTA (one CTA an SM, persistent):
 //   0-7    softmax: two streams of 128 threads, a row each.  NT = 2: the streams
 //          are two row tiles over the same key tiles; NT = 1 (up to 128 rows):
 //          the same rows, each stream taking every other key tile, joined at the end
 //   8-11   converters: codes of a page -> fp16 in the 128-byte-swizzled operand
-//          layouts, K as [key][d], V as [d][key], both K-major.  The page's V
-//          order gives a thread 4 keys of one d, which it stores as 8 bytes: the
-//          keys of 16 stand as t, t+1, t+8, t+9 for t = 0, 2, 4, 6, and P's
-//          columns follow the same order
+//          layouts, K as [key][d], V as [d][key], both K-major, two stages of each.
+//          The page's V order gives a thread 4 keys of one d, which it stores as 8
+//          bytes: the keys of 16 stand as t, t+1, t+8, t+9 for t = 0, 2, 4, 6, and
+//          P's columns follow the same order
 //   12     copies of the pages' codes, K and V apart (bulk copies, no multicast)
 //   13     TMEM allocation, tcgen05.mma issue (event-driven, one thread)
-// Bound: the tensor cores and the exponential unit alike (128 rows x 128 keys:
-// 1024 cycles of products, 1024 cycles of exponentials); the conversion of a
-// tile, about 700 cycles of four warps, runs beside them.
+// Bound: shared-memory bandwidth first (per two row tiles and 128 keys 192 KB of
+// operands, 64 KB converted, 64 KB of codes in and out: 2500 cycles at 128
+// bytes), then the tensor cores and the exponential unit (2048 cycles each).
+// With P through shared memory and one stage of K and V it took 8000.
 //
 // Work: runs of equal units (key tiles) as in kv8_attn.cu; pieces of a task that
 // CTAs share are joined by the CTA that delivers the last one, in order.
@@ -44,8 +46,7 @@ constexpr int TR = 128, TK = 128;          // rows of a tile, keys of a tile
 constexpr int W_CONV = 8, W_COPY = 12, W_MMA = 13;
 constexpr int THREADS = 14 * 32;
 constexpr float BIAS = 6.0f;               // log2 of the fp16 weight at both references
-constexpr float SUM_LIMIT = 256.0f;        // a tile's sum of weights (2^8): above it m is set anew
-constexpr float V_LIMIT = 128.0f;          // 2^(BIAS + 1); 2^8 * 2^7 < 65504
+constexpr float W_LIMIT = 32768.0f;        // sum of 32 fp16 weights above which the references are set anew
 constexpr int TASK_UNITS = 4;              // what a task costs besides its tiles, in tiles
 constexpr uint32_t TMEM_COLS = 512;        // S of the streams 0 .. 255, O 256 .. 511
 constexpr uint32_t TM_S = 0, TM_O = 256;
@@ -57,13 +58,12 @@ constexpr int HALF = HQ_KV8_V;             // bytes of a page's K (or V) codes
 template <int NT>
 struct Lay {
   static constexpr int Q = 0;                    // NT x 2 regions (d halves)
-  static constexpr int K = Q + NT * 32768;       // 2 regions (d halves): [key][64 d]
-  static constexpr int V = K + 32768;            // 2 regions (pages): [d][64 keys]
-  static constexpr int P = V + 32768;            // 2 streams x 2 regions (pages): [row][64 keys]
-  static constexpr int RAW = P + 65536;          // codes: slots of a page's K or V
+  static constexpr int K = Q + NT * 32768;       // 2 stages x 2 regions (d halves): [key][64 d]
+  static constexpr int V = K + 65536;            // 2 stages x 2 regions (pages): [d][64 keys]
+  static constexpr int RAW = V + 65536;          // codes: slots of a page's K or V
   static constexpr int RK = NT == 2 ? 2 : 4;     // slots of K; as many of V
-  static constexpr int AUX = RAW + 2 * RK * HALF;  // scales: 8 tiles x 2 pages x (K, V); the tail's 64 K and 64 V scales
-  static constexpr int BARS = AUX + 8 * 16 + 512;
+  static constexpr int AUX = RAW + 2 * RK * HALF;  // 8 tiles x 2 pages x (s_k, s_v, log2 s_v, 1 / s_v); the tail's 64 K and 64 V scales
+  static constexpr int BARS = AUX + 8 * 32 + 512;
   static constexpr int MISC = BARS + 32 * 8;     // TMEM base, flags, the plan's sums, 32 looked-up pages
   static constexpr int JOIN = RAW;               // NT = 1: (m, E, l) of stream 1's rows, once the task's copies are done with
   static constexpr int BYTES = MISC + 80 + 256 + 1024;  // with the alignment
@@ -114,9 +114,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BARS);
-  uint64_t *rk_full = bars, *rk_empty = bars + 4, *rv_full = bars + 8, *rv_empty = bars + 12, *s_full = bars + 16, *s_free = bars + 18,
-           *p_full = bars + 20, *o_done = bars + 22;
-  uint64_t &k_full = bars[24], &k_empty = bars[25], &v_full = bars[26], &v_empty = bars[27], &drain = bars[28];
+  uint64_t *rk_full = bars, *rk_empty = bars + 4, *rv_full = bars + 8, *rv_empty = bars + 12, *s_full = bars + 16, *p_full = bars + 18,
+           *o_done = bars + 20, *k_full = bars + 22, *k_empty = bars + 24, *v_full = bars + 26, *v_empty = bars + 28;
+  uint64_t& drain = bars[30];
   uint32_t& tmem_sh = *reinterpret_cast<uint32_t*>(sm + L::MISC);
   int* flags = reinterpret_cast<int*>(sm + L::MISC + 4);                  // stop, last
   uint32_t* sums = reinterpret_cast<uint32_t*>(sm + L::MISC + 16);        // [warps]
@@ -224,13 +224,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       mbar_init(rv_full + i, 1);
       mbar_init(rv_empty + i, 128);
     }
-    mbar_init(&k_full, 128);
-    mbar_init(&k_empty, 1);
-    mbar_init(&v_full, 128);
-    mbar_init(&v_empty, 1);
     for (int g = 0; g < 2; ++g) {
+      mbar_init(k_full + g, 128);
+      mbar_init(k_empty + g, 1);
+      mbar_init(v_full + g, 128);
+      mbar_init(v_empty + g, 1);
       mbar_init(s_full + g, 1);
-      mbar_init(s_free + g, 128);
       mbar_init(p_full + g, 128);
       mbar_init(o_done + g, 1);
     }
@@ -249,11 +248,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   const uint32_t base = smem_u32(sm);
   volatile int* stop = flags;
   float* aux = reinterpret_cast<float*>(sm + L::AUX);
-  float* tail_sc = aux + 8 * 4;  // [K, V][64]
+  float* tail_sc = aux + 8 * 8;  // [K, V][64]
 
   // running uses of each barrier, kept by the roles that wait on it; a tile that
   // stream g takes is its j-th: NT = 2 every tile, NT = 1 every other
-  int n_raw = 0, issued = 0;      // copied pages (copy warp, converters)
+  int n_raw = 0, issued = 0;      // pages to copy, copied (copy warp)
+  int raw_k = 0, raw_v = 0;       // converted (converters)
   int n_tile = 0;                 // tiles (converters, MMA, aux slot of the softmax)
   int n_str[2] = {0, 0};          // tiles of each stream (softmax, MMA)
   bool ok = true;
@@ -366,45 +366,60 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
         return *reinterpret_cast<const float*>(page + (ct & 1 ? HQ_KV8_VSCALE : HQ_KV8_KSCALE));
       };
       float scale = scale_of(0);
-      for (int t = 0; ok && t < nt; ++t, ++n_tile) {
-        const int np = pages_in(t), p0 = k.sp.begin + 2 * (k.t0 + t);
-        const bool tail = p0 + np < k.sp.end && np < 2;  // the tile's page np is the incomplete block
-        // ---- K: the operand is free once the tile before has been scored
-        if (n_tile > 0) ok = wait_for(&k_empty, (n_tile - 1) & 1, err, stop);
+      auto page_tail = [&](int t, int& np) {  // the tile's page np is the incomplete block
+        np = pages_in(t);
+        return np < 2 && k.sp.begin + 2 * (k.t0 + t) + np < k.sp.end;
+      };
+      // K of tile t: free once the tile two before has been scored
+      auto convert_k = [&](int t) {
+        int np;
+        const bool tail = page_tail(t, np);
+        const int T = n_tile + t, st = T & 1, p0 = k.sp.begin + 2 * (k.t0 + t);
+        if (T >= 2) ok = wait_for(k_empty + st, ((T >> 1) - 1) & 1, err, stop);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (ct < 4) aux[(n_tile & 7) * 4 + ct] = scale;
+        if (!ok) return;
+        if (ct < 4) {
+          float* x = aux + (T & 7) * 8 + (ct >> 1) * 4;
+          x[ct & 1] = scale;
+          if (ct & 1) {
+            x[2] = log2f(scale);
+            x[3] = 1.0f / scale;
+          }
+        }
         scale = scale_of(t + 1);
+        const uint32_t dst = base + L::K + st * 32768;
         for (int pg = 0; pg < np; ++pg) {
-          const int st = (n_raw + pg) % RK;
-          ok = wait_for(rk_full + st, ((n_raw + pg) / RK) & 1, err, stop);
+          const int n = raw_k + pg, sl = n % RK;
+          ok = wait_for(rk_full + sl, (n / RK) & 1, err, stop);
           ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const uint4* src = reinterpret_cast<const uint4*>(sm + L::RAW + st * HALF);
+          if (!ok) return;
+          const uint4* src = reinterpret_cast<const uint4*>(sm + L::RAW + sl * HALF);
+          uint4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = src[(cw * 4 + i) * 32 + lane];
+          mbar_arrive(rk_empty + sl);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int e = cw * 4 + i;  // 512-byte piece: 8 tokens x 64 d
-            const uint4 x = src[e * 32 + lane];
             uint32_t y[8];
-            kv8_half4<FMT>(x.x, y[0], y[1]);
-            kv8_half4<FMT>(x.y, y[2], y[3]);
-            kv8_half4<FMT>(x.z, y[4], y[5]);
-            kv8_half4<FMT>(x.w, y[6], y[7]);
-            const uint32_t row = base + L::K + (e & 1) * 16384 + (pg * 64 + (e >> 1) * 8 + g) * 128;
+            kv8_half4<FMT>(x[i].x, y[0], y[1]);
+            kv8_half4<FMT>(x[i].y, y[2], y[3]);
+            kv8_half4<FMT>(x[i].z, y[4], y[5]);
+            kv8_half4<FMT>(x[i].w, y[6], y[7]);
+            const uint32_t row = dst + (e & 1) * 16384 + (pg * 64 + (e >> 1) * 8 + g) * 128;
             sts128(row + (((2 * t4) ^ g) << 4), y[0], y[1], y[2], y[3]);
             sts128(row + (((2 * t4 + 1) ^ g) << 4), y[4], y[5], y[6], y[7]);
           }
-          mbar_arrive(rk_empty + st);
         }
-        if (!ok) break;
-        const size_t half = bh * 2 + ((p0 + np) & 1);
+        raw_k += np;
         if (tail) {
+          const size_t half = bh * 2 + ((p0 + np) & 1);
           const uint4* src = reinterpret_cast<const uint4*>(c.tail_k + half * KV8_BLOCK * D);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int e = cw * 4 + i;
             const uint4 x = src[(e * 32 + lane) * 2], y = src[(e * 32 + lane) * 2 + 1];
-            const uint32_t row = base + L::K + (e & 1) * 16384 + (np * 64 + (e >> 1) * 8 + g) * 128;
+            const uint32_t row = dst + (e & 1) * 16384 + (np * 64 + (e >> 1) * 8 + g) * 128;
             sts128(row + (((2 * t4) ^ g) << 4), x.x, x.y, x.z, x.w);
             sts128(row + (((2 * t4 + 1) ^ g) << 4), y.x, y.y, y.z, y.w);
           }
@@ -415,66 +430,76 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
                             : 1.0f;
         }
         fence_proxy_async_smem();
-        mbar_arrive(&k_full);
-        // ---- V: free once the tile before has been added
-        if (n_tile > 0) ok = wait_for(&v_empty, (n_tile - 1) & 1, err, stop);
+        mbar_arrive(k_full + st);
+      };
+      // V of tile t: free once the tile two before has been added
+      auto convert_v = [&](int t) {
+        int np;
+        const bool tail = page_tail(t, np);
+        const int T = n_tile + t, st = T & 1, p0 = k.sp.begin + 2 * (k.t0 + t);
+        if (T >= 2) ok = wait_for(v_empty + st, ((T >> 1) - 1) & 1, err, stop);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        // 16-byte chunk (16 tokens tt, 32 d dq, d % 8 = g, token pair t4): 4 words of 4 tokens of one d
-        auto vrow = [&](int pg, int d) { return base + L::V + pg * 16384 + d * 128; };
+        if (!ok) return;
+        // 16-byte chunk (16 tokens cw, 32 d i, d % 8 = g, token pair t4): 4 words of 4 tokens of one d
+        const uint32_t col = (((cw * 2 + (t4 >> 1)) ^ g) << 4) + (t4 & 1) * 8;
+        auto vrow = [&](int pg, int d) { return base + L::V + st * 32768 + pg * 16384 + d * 128 + col; };
         for (int pg = 0; pg < np; ++pg) {
-          const int st = (n_raw + pg) % RK;
-          ok = wait_for(rv_full + st, ((n_raw + pg) / RK) & 1, err, stop);
+          const int n = raw_v + pg, sl = n % RK;
+          ok = wait_for(rv_full + sl, (n / RK) & 1, err, stop);
           ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const uint4* src = reinterpret_cast<const uint4*>(sm + L::RAW + (RK + st) * HALF);
+          if (!ok) return;
+          const uint4* src = reinterpret_cast<const uint4*>(sm + L::RAW + (RK + sl) * HALF);
+          uint4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = src[(cw * 4 + i) * 32 + lane];
+          mbar_arrive(rv_empty + sl);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int tt = cw, dq = i;
-            const uint4 x = src[(tt * 4 + dq) * 32 + lane];
-            const uint32_t col = (((tt * 2 + (t4 >> 1)) ^ g) << 4) + (t4 & 1) * 8;
             uint32_t y[2];
-            kv8_half4<FMT>(x.x, y[0], y[1]);
-            sts64(vrow(pg, dq * 32 + g) + col, y[0], y[1]);
-            kv8_half4<FMT>(x.y, y[0], y[1]);
-            sts64(vrow(pg, dq * 32 + 8 + g) + col, y[0], y[1]);
-            kv8_half4<FMT>(x.z, y[0], y[1]);
-            sts64(vrow(pg, dq * 32 + 16 + g) + col, y[0], y[1]);
-            kv8_half4<FMT>(x.w, y[0], y[1]);
-            sts64(vrow(pg, dq * 32 + 24 + g) + col, y[0], y[1]);
+            kv8_half4<FMT>(x[i].x, y[0], y[1]);
+            sts64(vrow(pg, i * 32 + g), y[0], y[1]);
+            kv8_half4<FMT>(x[i].y, y[0], y[1]);
+            sts64(vrow(pg, i * 32 + 8 + g), y[0], y[1]);
+            kv8_half4<FMT>(x[i].z, y[0], y[1]);
+            sts64(vrow(pg, i * 32 + 16 + g), y[0], y[1]);
+            kv8_half4<FMT>(x[i].w, y[0], y[1]);
+            sts64(vrow(pg, i * 32 + 24 + g), y[0], y[1]);
           }
-          mbar_arrive(rv_empty + st);
         }
-        if (!ok) break;
+        raw_v += np;
         for (int pg = np; pg < 2; ++pg) {
           // the tail's values, or zeros where the tile ends: a weight of 0 must not meet what is left there
           const bool have = tail && pg == np;
-          const uint4* src = reinterpret_cast<const uint4*>(c.tail_v + half * KV8_BLOCK * D);
+          const uint4* src = reinterpret_cast<const uint4*>(c.tail_v + (bh * 2 + ((p0 + np) & 1)) * KV8_BLOCK * D);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t col = (((cw * 2 + (t4 >> 1)) ^ g) << 4) + (t4 & 1) * 8;
             uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
             if (have) {
               x = src[((cw * 4 + i) * 32 + lane) * 2];
               y = src[((cw * 4 + i) * 32 + lane) * 2 + 1];
             }
-            sts64(vrow(pg, i * 32 + g) + col, x.x, x.y);
-            sts64(vrow(pg, i * 32 + 8 + g) + col, x.z, x.w);
-            sts64(vrow(pg, i * 32 + 16 + g) + col, y.x, y.y);
-            sts64(vrow(pg, i * 32 + 24 + g) + col, y.z, y.w);
+            sts64(vrow(pg, i * 32 + g), x.x, x.y);
+            sts64(vrow(pg, i * 32 + 8 + g), x.z, x.w);
+            sts64(vrow(pg, i * 32 + 16 + g), y.x, y.y);
+            sts64(vrow(pg, i * 32 + 24 + g), y.z, y.w);
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(&v_full);
-        n_raw += np;
+        mbar_arrive(v_full + st);
+      };
+      // K runs a tile ahead of V: a tile is scored before its values are needed
+      convert_k(0);
+      for (int t = 0; ok && t < nt; ++t) {
+        if (t + 1 < nt) convert_k(t + 1);
+        if (ok) convert_v(t);
       }
+      n_tile += nt;
     } else if (warp == W_MMA) {
       // -------------------------------------------------------- MMA issue
       if (lane == 0 && ok) {
-        const uint32_t Ks = base + L::K, Vs = base + L::V;
-        auto issue_qk = [&](int g) {
+        auto issue_qk = [&](int g, int st) {
           tc_fence_after();
-          const uint32_t Qs = base + L::Q + (NT == 2 ? g * 32768 : 0);
+          const uint32_t Qs = base + L::Q + (NT == 2 ? g * 32768 : 0), Ks = base + L::K + st * 32768;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t off = (kk >> 2) * 16384 + 32 * (kk & 3);
@@ -482,23 +507,24 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           }
           umma_commit(s_full + g);
         };
-        auto issue_pv = [&](int g, bool first) {
+        auto issue_pv = [&](int g, int st, bool first) {
           tc_fence_after();
-          const uint32_t Ps = base + L::P + g * 32768;
+          const uint32_t Vs = base + L::V + st * 32768;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t off = (kk >> 2) * 16384 + 32 * (kk & 3);
-            umma_f16(tmem + TM_O + 128 * g, sdesc_sw128(Ps + off, 16, 1024), sdesc_sw128(Vs + off, 16, 1024), IDESC,
-                     !first || kk > 0 ? 1u : 0u);
+            umma_f16_ta(tmem + TM_O + 128 * g, tmem + TM_S + 128 * g + 8 * kk, sdesc_sw128(Vs + off, 16, 1024), IDESC,
+                        !first || kk > 0 ? 1u : 0u);
           }
           umma_commit(o_done + g);
         };
-        // whichever of the streams' QK and PV is ready goes next; a tile's operand is
-        // released when every stream that takes it has been issued
-        int tq[2], tp[2], jq[2], jp[2];  // next tile of each stream to score / to add, and its number in the stream
+        // A stream goes QK, PV, QK, .. (its P lies where its S does); whichever
+        // stream is ready goes next.  A tile's operand is released when every
+        // stream that takes it has been issued.
+        int tq[2], tp[2], jq[2];  // next tile of each stream to score / to add, and the former's number in the stream
         for (int g = 0; g < 2; ++g) {
           tq[g] = tp[g] = NT == 2 ? 0 : g;
-          jq[g] = jp[g] = n_str[g];
+          jq[g] = n_str[g];
         }
         const int step = NT == 2 ? 1 : 2;
         uint64_t t_last = global_ns();
@@ -506,24 +532,21 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           bool progress = false;
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const int t = tq[g];
-            if (t < nt && mbar_test_wait(&k_full, (n_tile + t) & 1) && (jq[g] == 0 || mbar_test_wait(s_free + g, (jq[g] - 1) & 1))) {
-              // NT = 1: the barrier's phase tells tile t from t - 2 only while t - 1 is scored
-              if (NT == 2 || tq[g ^ 1] == t + 1 || tq[g ^ 1] >= nt) {
-                issue_qk(g);
-                if (NT == 1 || tq[g ^ 1] > t) umma_commit(&k_empty);
+            if (tp[g] == tq[g]) {
+              const int t = tq[g], T = n_tile + t;
+              if (t < nt && (t < step || mbar_test_wait(o_done + g, (jq[g] - 1) & 1)) && mbar_test_wait(k_full + (T & 1), (T >> 1) & 1)) {
+                issue_qk(g, T & 1);
+                if (NT == 1 || tq[g ^ 1] > t) umma_commit(k_empty + (T & 1));
                 tq[g] = t + step;
                 ++jq[g];
                 progress = true;
               }
-            }
-            const int p = tp[g];
-            if (p < tq[g] && p < nt && mbar_test_wait(p_full + g, jp[g] & 1) && mbar_test_wait(&v_full, (n_tile + p) & 1)) {
-              if (NT == 2 || tp[g ^ 1] == p + 1 || tp[g ^ 1] >= nt) {
-                issue_pv(g, p < step);
-                if (NT == 1 || tp[g ^ 1] > p) umma_commit(&v_empty);
-                tp[g] = p + step;
-                ++jp[g];
+            } else {
+              const int t = tp[g], T = n_tile + t;
+              if (mbar_test_wait(p_full + g, (jq[g] - 1) & 1) && mbar_test_wait(v_full + (T & 1), (T >> 1) & 1)) {
+                issue_pv(g, T & 1, t < step);
+                if (NT == 1 || tp[g ^ 1] > t) umma_commit(v_empty + (T & 1));
+                tp[g] = t + step;
                 progress = true;
               }
             }
@@ -552,33 +575,35 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       const int qpos = k.s.first + rr / a.G;
       const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       const uint32_t srow = trow + TM_S + 128 * g, orow = trow + TM_O + 128 * g;
-      const uint32_t prow = base + L::P + g * 32768 + r * 128;
-      // rows past the last have zero queries and see every key
-      float m = real ? -INFINITY : 0.f, e = -INFINITY, l = 0.f, ef = 0.f;
+      // rows past the last have zero queries and see every key; their references
+      // stay at 1.  A warp without a row only keeps the barriers going.
+      float m = real ? -INFINITY : 0.f, e = real ? -INFINITY : 0.f, l = 0.f;
+      float lef = real ? -INFINITY : 0.f, ref = real ? 0.f : 1.f;  // log2 of 2^(m - E + BIAS), and its inverse
+      const bool idle = !__any_sync(0xffffffffu, real);
       bool any = false;  // a tile was taken
       for (int t = 0; t < nt; ++t) {
         if (!takes(g, t)) continue;
-        const int j = n_str[g];
-        ok = ok && wait_for(s_full + g, j & 1, err, stop);
-        if (any) ok = ok && wait_for(o_done + g, (j - 1) & 1, err, stop);  // P is free
+        ok = ok && wait_for(s_full + g, n_str[g] & 1, err, stop);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
+        if (idle) {
+          any = true;
+          ++n_str[g];
+          mbar_arrive(p_full + g);
+          continue;
+        }
         const int np = pages_in(t), p0 = k.sp.begin + 2 * (k.t0 + t);
         const bool tail = np < 2 && p0 + np < k.sp.end;
-        const float4 sc = *reinterpret_cast<const float4*>(aux + ((n_tile + t) & 7) * 4);
+        const float4 sc0 = *reinterpret_cast<const float4*>(aux + ((n_tile + t) & 7) * 8);  // s_k, s_v, log2 s_v, 1 / s_v
+        const float4 sc1 = *reinterpret_cast<const float4*>(aux + ((n_tile + t) & 7) * 8 + 4);
         // columns [lo, hi] of the tile are seen by this row
         const int hi = real ? qpos - p0 * KV8_BLOCK : TK, lo = real && a.window > 0 ? hi - a.window + 1 : 0;
-        float vtop = fmaxf(np > 0 ? sc.y : 0.f, np > 1 ? sc.w : 0.f);  // ignores NaN
-        if (tail)
-          for (int i = 0; i < 64; ++i) vtop = fmaxf(vtop, tail_sc[64 + i]);
-        if (!(vtop > 0.f)) vtop = 1.f;
-
-        // scores of columns 32 c4 .. + 31 as exponents relative to mref: masked ones -inf.
-        // `seen`: all columns seen and no tail in the tile
+        // all columns seen and no tail in the tile
         const bool seen = __all_sync(0xffffffffu, !tail && np == 2 && hi >= TK - 1 && lo <= 0);
+        // scores of columns 32 c4 .. + 31 less mref: masked ones -inf
         auto scores = [&](float (&x)[32], int c4, float mref) {
-          const float mul = qmul * (c4 < 2 ? sc.x : sc.z);
+          const float mul = qmul * (c4 < 2 ? sc0.x : sc1.x);
           if (seen) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = fmaf(x[i], mul, -mref);
@@ -592,107 +617,130 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
             }
           }
         };
+        // The references anew at columns 32 c4: the exact maximum of the columns
+        // from there on; sums, O and the tile's weights so far are rescaled.
         float sum = 0.f;
-        const int first = __any_sync(0xffffffffu, m == -INFINITY || ef * vtop > V_LIMIT) ? 1 : 0;
-        for (int pass = first; pass < 3; ++pass) {
-          if (pass == 1) {
-            // the references anew: the exact maximum of the tile
-            float mt = -INFINITY;
+        auto renew = [&](int c4) {
+          float vtop = fmaxf(np > 0 ? sc0.y : 0.f, np > 1 ? sc1.y : 0.f);  // ignores NaN
+          if (tail)
+            for (int i = 0; i < 64; ++i) vtop = fmaxf(vtop, tail_sc[64 + i]);
+          if (!(vtop > 0.f)) vtop = 1.f;
+          float mt = -INFINITY;
 #pragma unroll 1
-            for (int c4 = 0; c4 < 4; ++c4) {
-              float x[32];
-              tmem_ld32f(srow + 32 * c4, x);
+          for (int q4 = c4; q4 < 4; ++q4) {
+            float x[32];
+            tmem_ld32f(srow + 32 * q4, x);
+            tmem_wait_ld();
+            scores(x, q4, 0.f);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mt = fmaxf(mt, x[i]);
+          }
+          const float m_new = fmaxf(m, mt), e_new = fmaxf(e, mt + log2f(vtop));
+          const float mb = m_new == -INFINITY ? 0.f : m_new, eb = e_new == -INFINITY ? 0.f : e_new;
+          const float al = ex2(m - mb), ao = ex2(e - eb);
+          l *= al;
+          sum *= al;
+          m = m_new;
+          e = e_new;
+          // bounded, so that a weight that underflowed stays 0 beside a far larger earlier score
+          lef = e_new == -INFINITY ? -INFINITY : fminf(mb - eb + BIAS, 100.f);
+          ref = e_new == -INFINITY ? 0.f : ex2(-lef);
+          if (any) {
+#pragma unroll 1
+            for (int q4 = 0; q4 < 4; ++q4) {
+              uint32_t y[32];
+              tmem_ld32(orow + 32 * q4, y);
               tmem_wait_ld();
-              scores(x, c4, 0.f);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) mt = fmaxf(mt, x[i]);
+              for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * ao);
+              tmem_st32(orow + 32 * q4, y);
             }
-            const float m_new = fmaxf(m, mt), e_new = fmaxf(e, mt + log2f(vtop));
-            const float mb = m_new == -INFINITY ? 0.f : m_new, eb = e_new == -INFINITY ? 0.f : e_new;
-            l *= ex2(m - mb);
-            const float ao = ex2(e - eb);
-            m = m_new;
-            e = e_new;
-            // bounded, so that a weight that underflowed stays 0 beside a far larger earlier score
-            ef = e_new == -INFINITY ? 0.f : ex2(fminf(mb - eb + BIAS, 100.f));
-            if (any) {
+          }
+          tmem_wait_st();
 #pragma unroll 1
-              for (int c4 = 0; c4 < 4; ++c4) {
-                uint32_t y[32];
-                tmem_ld32(orow + 32 * c4, y);
-                tmem_wait_ld();
+          for (int q4 = 0; q4 < c4; ++q4) {
+            uint32_t y[16];
+            tmem_ld16(srow + 16 * q4, y);
+            tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * ao);
-                tmem_st32(orow + 32 * c4, y);
-              }
-              tmem_wait_st();
+            for (int i = 0; i < 16; ++i) {
+              const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
+              y[i] = pack_f16x2(w.x * ao, w.y * ao);
             }
+            tmem_st16(srow + 16 * q4, y);
+          }
+          tmem_wait_st();
+        };
+        int fresh = -1;  // columns at which the references were set
+        if (__any_sync(0xffffffffu, m == -INFINITY)) {
+          renew(0);
+          fresh = 0;
+        }
+        float x[32];
+        tmem_ld32f(srow, x);
+        tmem_wait_ld();
+#pragma unroll 1
+        for (int c4 = 0; c4 < 4; ++c4) {
+          const float mref = m == -INFINITY ? 0.f : m;
+          const float4 sc = c4 < 2 ? sc0 : sc1;
+          // Weights of a page that is seen whole take the value scale into the
+          // exponent, and their sum is divided by it: a product less per weight.
+          // Not where it is so small that weights would underflow.
+          const float lw = lef + sc.z;
+          float s0 = 0.f, s1 = 0.f;
+          uint32_t pk[16];
+          if (__all_sync(0xffffffffu, seen && lw > -60.f)) {
+            scores(x, c4, mref - lw);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float y0 = ex2(x[i]), y1 = ex2(x[i + 1]);
+              s0 += y0;
+              s1 += y1;
+              pk[i / 2] = pack_f16x2(y0, y1);
+            }
+            s0 += s1;
+            s1 = s0 * (ref * sc.w);
+          } else {
+            scores(x, c4, mref);
+            const bool tl = tail && (c4 >> 1) == np;
+            const float ef = ex2(lef), w = ef * sc.y;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float y0 = ex2(x[i]), y1 = ex2(x[i + 1]);
+              s1 += y0 + y1;
+              // a scale that is NaN stays behind the mask
+              const int col = (32 * c4 + i) & 63;
+              y0 = x[i] == -INFINITY ? 0.f : y0 * (tl ? ef * tail_sc[64 + col] : w);
+              y1 = x[i + 1] == -INFINITY ? 0.f : y1 * (tl ? ef * tail_sc[64 + col + 1] : w);
+              s0 += y0 + y1;
+              pk[i / 2] = pack_f16x2(y0, y1);
+            }
+          }
+          // s0: the fp16 weights' sum, s1: the softmax's
+          if (__any_sync(0xffffffffu, !(s0 <= W_LIMIT)) && fresh != c4) {  // also an infinity or NaN
+            renew(c4);
+            fresh = c4;
+            tmem_ld32f(srow + 32 * c4, x);
+            tmem_wait_ld();
+            --c4;
             continue;
           }
-          const float mref = m == -INFINITY ? 0.f : m;
-          // Weights of a page that is seen whole take its value scale w into the
-          // exponent, and their sum is divided by it: a product less per weight.
-          // Not where w is so small that weights would underflow.
-          const float w0 = ef * sc.y, w1 = ef * sc.w;
-          const bool plain = __all_sync(0xffffffffu, seen && w0 > 0x1p-60f && w1 > 0x1p-60f);
-          const float lw0 = plain ? log2f(w0) : 0.f, lw1 = plain ? log2f(w1) : 0.f;
-          sum = 0.f;
-          float s0 = 0.f, s1 = 0.f;
-          float x[32];
-          tmem_ld32f(srow, x);
-          tmem_wait_ld();
-#pragma unroll 1
-          for (int c4 = 0; c4 < 4; ++c4) {
-            uint32_t pk[16];
-            if (plain) {
-              scores(x, c4, mref - (c4 < 2 ? lw0 : lw1));
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float y0 = ex2(x[i]), y1 = ex2(x[i + 1]);
-                s0 += y0;
-                s1 += y1;
-                pk[i / 2] = pack_f16x2(y0, y1);
-              }
-              if (c4 & 1) {
-                sum += (s0 + s1) / (c4 < 2 ? w0 : w1);
-                s0 = s1 = 0.f;
-              }
-            } else {
-              scores(x, c4, mref);
-              const bool tl = tail && (c4 >> 1) == np;
-              const float w = c4 < 2 ? w0 : w1;
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                float y0 = ex2(x[i]), y1 = ex2(x[i + 1]);
-                sum += y0 + y1;
-                // a scale that is NaN stays behind the mask
-                const int col = (32 * c4 + i) & 63;
-                y0 = x[i] == -INFINITY ? 0.f : y0 * (tl ? ef * tail_sc[64 + col] : w);
-                y1 = x[i + 1] == -INFINITY ? 0.f : y1 * (tl ? ef * tail_sc[64 + col + 1] : w);
-                pk[i / 2] = pack_f16x2(y0, y1);
-              }
-            }
-            if (c4 < 3) tmem_ld32f(srow + 32 * (c4 + 1), x);  // the next columns, during the stores
-            // the keys of 16 in V's order: 0 1 8 9, 2 3 10 11, 4 5 12 13, 6 7 14 15
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const int chunk = (c4 & 1) * 4 + h * 2 + q;
-                sts128(prow + (c4 >> 1) * 16384 + ((chunk ^ (r & 7)) << 4), pk[h * 8 + 2 * q], pk[h * 8 + 2 * q + 4],
-                       pk[h * 8 + 2 * q + 1], pk[h * 8 + 2 * q + 5]);
-              }
-            if (c4 < 3) tmem_wait_ld();
+          sum += s1;
+          // P's columns 16 c4 .. take the place of scores that have been read: pairs of
+          // keys, those of 16 in V's order 0 1 8 9, 2 3 10 11, 4 5 12 13, 6 7 14 15
+          const uint32_t w[16] = {pk[0], pk[4], pk[1], pk[5], pk[2], pk[6], pk[3], pk[7],
+                                  pk[8], pk[12], pk[9], pk[13], pk[10], pk[14], pk[11], pk[15]};
+          tmem_st16(srow + 16 * c4, w);
+          if (c4 < 3) {
+            tmem_ld32f(srow + 32 * (c4 + 1), x);
+            tmem_wait_ld();
           }
-          if (pass == 2) break;
-          if (!__any_sync(0xffffffffu, !(sum <= SUM_LIMIT))) break;  // also an infinity or NaN
         }
+        tmem_wait_st();
         l += sum;
         any = true;
         ++n_str[g];
         tc_fence_before();
-        mbar_arrive(s_free + g);
-        fence_proxy_async_smem();
         mbar_arrive(p_full + g);
       }
       n_tile += nt;
@@ -706,10 +754,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
         tmem_ld32f(orow + 32 * c4, x);
         tmem_wait_ld();
       };
-      float* swap = reinterpret_cast<float*>(sm + L::P);  // [column][row]: the streams' weights are done with
+      float* swap = reinterpret_cast<float*>(sm + L::K);  // [column][row]: the keys are done with
       if (NT == 1) {
-        // stream 1 hands its rows to stream 0, once both streams' products have read P
-        // and every code of the task has been converted
+        // stream 1 hands its rows to stream 0, once both streams are through with the
+        // keys and every code of the task has been converted
         asm volatile("bar.sync 2, 256;" ::: "memory");
         if (g == 1) {
           joined[r] = m;
