@@ -21,8 +21,8 @@
 //          The page's V order gives a thread 4 keys of one d, which it stores as 8
 //          bytes: the keys of 16 stand as t, t+1, t+8, t+9 for t = 0, 2, 4, 6, and
 //          P's columns follow the same order
-//   12     copies of the pages' codes, K and V apart (bulk copies, no multicast)
-//   13     TMEM allocation, tcgen05.mma issue (event-driven, one thread)
+//   12, 13 copies of the pages' codes, K and V (bulk copies, no multicast)
+//   14     TMEM allocation, tcgen05.mma issue (event-driven, one thread)
 // Bound: shared-memory bandwidth first (per two row tiles and 128 keys 192 KB of
 // operands, 64 KB converted, 64 KB of codes in and out: 2500 cycles at 128
 // bytes), then the tensor cores and the exponential unit (2048 cycles each).
@@ -43,8 +43,8 @@ namespace hq {
 namespace {
 
 constexpr int TR = 128, TK = 128;          // rows of a tile, keys of a tile
-constexpr int W_CONV = 8, W_COPY = 12, W_MMA = 13;
-constexpr int THREADS = 14 * 32;
+constexpr int W_CONV = 8, W_COPY = 12, W_MMA = 14;  // W_COPY: K, W_COPY + 1: V
+constexpr int THREADS = 15 * 32;
 constexpr float BIAS = 6.0f;               // log2 of the fp16 weight at both references
 constexpr float W_LIMIT = 32768.0f;        // sum of 32 fp16 weights above which the references are set anew
 constexpr int TASK_UNITS = 4;              // what a task costs besides its tiles, in tiles
@@ -64,9 +64,9 @@ struct Lay {
   static constexpr int RK = NT == 2 ? 2 : 4;     // slots of K; as many of V
   static constexpr int AUX = RAW + 2 * RK * HALF;  // 8 tiles x 2 pages x (s_k, s_v, log2 s_v, 1 / s_v); the tail's 64 K and 64 V scales
   static constexpr int BARS = AUX + 8 * 32 + 512;
-  static constexpr int MISC = BARS + 32 * 8;     // TMEM base, flags, the plan's sums, 32 looked-up pages
+  static constexpr int MISC = BARS + 32 * 8;     // TMEM base, flags, the plan's sums
   static constexpr int JOIN = RAW;               // NT = 1: (m, E, l) of stream 1's rows, once the task's copies are done with
-  static constexpr int BYTES = MISC + 80 + 256 + 1024;  // with the alignment
+  static constexpr int BYTES = MISC + 80 + 1024;  // with the alignment
 };
 
 // Key tiles of row group grp of a sequence: blocks [begin, end) and the positions
@@ -120,7 +120,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   uint32_t& tmem_sh = *reinterpret_cast<uint32_t*>(sm + L::MISC);
   int* flags = reinterpret_cast<int*>(sm + L::MISC + 4);                  // stop, last
   uint32_t* sums = reinterpret_cast<uint32_t*>(sm + L::MISC + 16);        // [warps]
-  uint64_t* looked = reinterpret_cast<uint64_t*>(sm + L::MISC + 80);      // [32] pages to copy
   float* joined = reinterpret_cast<float*>(sm + L::JOIN);                 // [3][TR]
   uint32_t* prefix = reinterpret_cast<uint32_t*>(sm + L::Q);  // units of the sequences before b, of one kv head: until the queries come
   static_assert(HQ_KV8_MAX_BATCH * 4 <= 32768, "the plan fits where the queries go");
@@ -252,7 +251,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
 
   // running uses of each barrier, kept by the roles that wait on it; a tile that
   // stream g takes is its j-th: NT = 2 every tile, NT = 1 every other
-  int n_raw = 0, issued = 0;      // pages to copy, copied (copy warp)
+  int n_raw = 0;                  // copied (copy warps)
   int raw_k = 0, raw_v = 0;       // converted (converters)
   int n_tile = 0;                 // tiles (converters, MMA, aux slot of the softmax)
   int n_str[2] = {0, 0};          // tiles of each stream (softmax, MMA)
@@ -331,29 +330,30 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
     }
     __syncthreads();
 
-    if (warp == W_COPY) {
+    if (warp == W_COPY || warp == W_COPY + 1) {
       // -------------------------------------------------------- copies
-      // 32 pages looked up at a time; lane 0 copies the K codes, lane 1 the V codes,
-      // each as its slots come free
+      // 32 pages looked up at a time, and the next 32 while these are copied
+      const int which = warp - W_COPY;
+      uint64_t* empty = which ? rv_empty : rk_empty;
+      uint64_t* full = which ? rv_full : rk_full;
       const int p_begin = k.sp.begin + 2 * k.t0, p_end = min(full_end, k.sp.begin + 2 * k.t1);
-      for (int p = p_begin; p < p_end; p += 32) {
+      auto look_up = [&](int p) { return p + lane < p_end ? reinterpret_cast<uint64_t>(kv8_page(c, bh, p + lane)) : 0ull; };
+      uint64_t next = look_up(p_begin);
+      for (int p = p_begin; ok && p < p_end; p += 32) {
+        const uint64_t now = next;
+        next = look_up(p + 32);
         const int m = min(32, p_end - p);
-        if (lane < m) looked[lane] = reinterpret_cast<uint64_t>(kv8_page(c, bh, p + lane));
-        __syncwarp();
-        if (lane < 2) {
-          uint64_t* e = lane ? rv_empty : rk_empty;
-          uint64_t* f = lane ? rv_full : rk_full;
-          for (int i = 0; ok && i < m; ++i) {
-            const int n = n_raw + i, st = n % RK;
-            if (n >= RK) ok = wait_for(e + st, (n / RK - 1) & 1, err, stop);
-            if (!ok) break;
-            mbar_arrive_expect_tx(f + st, HALF);
-            bulk_g2s(sm + L::RAW + (lane * RK + st) * HALF, reinterpret_cast<const uint8_t*>(looked[i]) + lane * HQ_KV8_V, HALF, f + st);
-            issued = n + 1;
+        for (int i = 0; ok && i < m; ++i, ++n_raw) {
+          const int sl = n_raw % RK;
+          const uint8_t* page = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, now, i));
+          if (n_raw >= RK) ok = wait_for(empty + sl, (n_raw / RK - 1) & 1, err, stop);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(full + sl, HALF);
+            bulk_g2s(sm + L::RAW + (which * RK + sl) * HALF, page + which * HQ_KV8_V, HALF, full + sl);
           }
         }
-        __syncwarp();
-        n_raw += m;
       }
     } else if (warp >= W_CONV && warp < W_COPY) {
       // -------------------------------------------------------- converters
@@ -527,7 +527,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           jq[g] = n_str[g];
         }
         const int step = NT == 2 ? 1 : 2;
-        uint64_t t_last = global_ns();
+        uint64_t t_last = 0;
+        uint32_t idle = 0;
         while (tp[0] < nt || tp[1] < nt) {
           bool progress = false;
 #pragma unroll
@@ -552,10 +553,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
             }
           }
           if (progress) {
-            t_last = global_ns();
+            idle = 0;
+          } else if (++idle < 1024) {
           } else if (*stop) {
             ok = false;
             break;
+          } else if (idle == 1024) {
+            t_last = global_ns();  // the clock is read only once nothing has been ready for a while
           } else if (global_ns() - t_last > 1000000000ull) {
             atomicOr(reinterpret_cast<unsigned int*>(err), HQ_DEVERR_TIMEOUT);
             *stop = 1;
@@ -891,9 +895,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
   }
-  if (warp == W_COPY && lane < 2 && *stop) {
+  if ((warp == W_COPY || warp == W_COPY + 1) && lane == 0 && *stop) {
     int never = 0;
-    for (int i = max(0, issued - RK); i < issued; ++i) wait_for((lane ? rv_full : rk_full) + i % RK, (i / RK) & 1, c.err, &never);
+    for (int i = max(0, n_raw - RK); i < n_raw; ++i) wait_for((warp == W_COPY ? rk_full : rv_full) + i % RK, (i / RK) & 1, c.err, &never);
   }
 }
 
