@@ -64,9 +64,9 @@ struct Lay {
   static constexpr int RK = NT == 2 ? 2 : 4;     // slots of K; as many of V
   static constexpr int AUX = RAW + 2 * RK * HALF;  // 8 tiles x 2 pages x (s_k, s_v, log2 s_v, 1 / s_v); the tail's 64 K and 64 V scales
   static constexpr int BARS = AUX + 8 * 32 + 512;
-  static constexpr int MISC = BARS + 32 * 8;     // TMEM base, flags, the plan's sums
+  static constexpr int MISC = BARS + 32 * 8;     // TMEM base, flags, the plan's sums, walk and job
   static constexpr int JOIN = RAW;               // NT = 1: (m, E, l) of stream 1's rows, once the task's copies are done with
-  static constexpr int BYTES = MISC + 80 + 1024;  // with the alignment
+  static constexpr int BYTES = MISC + 80 + 144 + 1024;  // with the alignment
 };
 
 // Key tiles of row group grp of a sequence: blocks [begin, end) and the positions
@@ -85,6 +85,25 @@ __device__ __forceinline__ Span span_of(const Kv8Seq& s, int G, int window, int 
   return x;
 }
 __device__ __forceinline__ int tiles_of(const Span& x) { return (x.end - x.begin + 1) / 2; }
+
+// A task (sequence, kv head, row group) of a CTA's run, [t0, t1) of its key tiles
+// ours, and what the roles need of it.  One thread walks the run; both lie in
+// shared memory, for want of registers.
+struct Walk {
+  int b, h, grp, tiles, t0, t1;  // no tiles are ours where the run begins behind them
+  uint32_t u, u1;                // the task's first unit of ours, the run's end
+  uint32_t units;                // ours of the task
+  Kv8Seq s;
+  Span sp;
+};
+struct Job {
+  int b, h, row0, rows, tok0;    // rows row0 .. of the kv head's `rows`; the sequence's first row of q
+  int first, len;                // position of its first new token, its length
+  int page, full_end, end;       // first page of our tiles; complete pages end; the task's pages end
+  int nt;                        // our tiles: 0, the run has no more
+  int head, whole;               // the task's first tile is ours; all are
+  int c0, c1;                    // the CTAs that share the task
+};
 
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int32_t* err, volatile int* stop) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -107,6 +126,52 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
+// The run's task at k.u (k.t0 of its tiles belong to the CTAs before).
+template <int NT>
+__device__ __noinline__ void enter(const Kv8AttnArgs& a, Walk& k, uint32_t total, Job& j) {
+  k.sp = span_of<NT>(k.s, a.G, a.window, k.grp);
+  k.tiles = tiles_of(k.sp);
+  k.units = min(static_cast<uint32_t>(k.tiles + TASK_UNITS - k.t0), k.u1 - k.u);
+  k.t1 = min(k.tiles, k.t0 + static_cast<int>(k.units));
+  const uint32_t parts = min(total, gridDim.x), run = total / parts, more = total - run * parts;
+  // the first `more` runs have a unit more than the others
+  auto cta_of = [&](uint32_t u) { return u < more * (run + 1) ? u / (run + 1) : more + (u - more * (run + 1)) / run; };
+  j.b = k.b;
+  j.h = k.h;
+  j.row0 = k.grp * NT * TR;
+  j.rows = k.s.n * a.G;
+  j.tok0 = k.s.row0;
+  j.first = k.s.first;
+  j.len = k.s.len;
+  j.page = k.sp.begin + 2 * k.t0;
+  j.full_end = min(k.sp.end, k.s.len / KV8_BLOCK);
+  j.end = k.sp.end;
+  j.nt = max(0, k.t1 - k.t0);
+  j.head = k.t0 == 0;
+  j.whole = j.nt == k.tiles;
+  j.c0 = cta_of(k.u - k.t0);
+  j.c1 = cta_of(k.u - k.t0 + k.tiles - 1);
+}
+// The run's next task, or none (j.nt = 0).
+template <int NT>
+__device__ __noinline__ void next_task(const Kv8AttnArgs& a, Walk& k, uint32_t total, Job& j) {
+  j.nt = 0;
+  k.u += k.units;
+  if (k.u >= k.u1) return;
+  k.t0 = 0;
+  if (++k.grp * NT * TR >= k.s.n * a.G) {
+    k.grp = 0;
+    if (++k.h == a.c.Hkv) {
+      k.h = 0;
+      do {
+        ++k.b;
+        kv8_seq(a.c, a.cu, a.kv_len, a.N, a.max_new, k.b, false, k.s);
+      } while (k.s.n == 0);
+    }
+  }
+  enter<NT>(a, k, total, j);
+}
+
 template <class E, int FMT, int NT>
 __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
   using L = Lay<NT>;
@@ -120,6 +185,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   uint32_t& tmem_sh = *reinterpret_cast<uint32_t*>(sm + L::MISC);
   int* flags = reinterpret_cast<int*>(sm + L::MISC + 4);                  // stop, last
   uint32_t* sums = reinterpret_cast<uint32_t*>(sm + L::MISC + 16);        // [warps]
+  Walk& walk = *reinterpret_cast<Walk*>(sm + L::MISC + 80);
+  Job& job = *reinterpret_cast<Job*>(sm + L::MISC + 80 + sizeof(Walk));
+  static_assert(sizeof(Walk) + sizeof(Job) <= 144, "their place");
   float* joined = reinterpret_cast<float*>(sm + L::JOIN);                 // [3][TR]
   uint32_t* prefix = reinterpret_cast<uint32_t*>(sm + L::Q);  // units of the sequences before b, of one kv head: until the queries come
   static_assert(HQ_KV8_MAX_BATCH * 4 <= 32768, "the plan fits where the queries go");
@@ -154,66 +222,40 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
     if (b < B) prefix[b] = before + x - n;
     __syncthreads();
   }
-  const uint32_t total = carry * c.Hkv, parts = min(total, gridDim.x);
-  if (blockIdx.x >= parts) return;
-  const uint32_t run = total / parts, more = total - run * parts;
-  const uint32_t u0 = run * blockIdx.x + min(blockIdx.x, more), u1 = u0 + run + (blockIdx.x < more);
-  auto cta_of = [&](uint32_t u) { return u < more * (run + 1) ? u / (run + 1) : more + (u - more * (run + 1)) / run; };
-  struct Task {
-    int b, h, grp, tiles, t0, t1;  // key tiles [t0, t1) are ours (none where the run begins behind them)
-    uint32_t units;
-    Kv8Seq s;
-    Span sp;
-  };
-  auto enter = [&](uint32_t u, Task& k) {
-    k.sp = span_of<NT>(k.s, a.G, a.window, k.grp);
-    k.tiles = tiles_of(k.sp);
-    k.units = min(static_cast<uint32_t>(k.tiles + TASK_UNITS - k.t0), u1 - u);
-    k.t1 = min(k.tiles, k.t0 + static_cast<int>(k.units));
-  };
-  auto task_at = [&](uint32_t u, Task& k) {
-    const uint32_t want = u / c.Hkv;
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= want) lo = mid; else hi = mid;
-    }
-    k.b = lo;
-    kv8_seq(c, a.cu, a.kv_len, a.N, a.max_new, lo, false, k.s);
-    const uint32_t each = (lo + 1 < B ? prefix[lo + 1] : carry) - prefix[lo];  // units of a kv head
-    uint32_t rel = u - prefix[lo] * c.Hkv;
-    k.h = rel / each;
-    rel -= k.h * each;
-    for (k.grp = 0;; ++k.grp) {
-      const uint32_t n = tiles_of(span_of<NT>(k.s, a.G, a.window, k.grp)) + TASK_UNITS;
-      if (rel < n) break;
-      rel -= n;
-    }
-    k.t0 = rel;
-    enter(u, k);
-  };
-  auto next_task = [&](uint32_t u, Task& k) {
-    k.t0 = 0;
-    if (++k.grp * ROWS >= k.s.n * a.G) {
-      k.grp = 0;
-      if (++k.h == c.Hkv) {
-        k.h = 0;
-        do {
-          ++k.b;
-          kv8_seq(c, a.cu, a.kv_len, a.N, a.max_new, k.b, false, k.s);
-        } while (k.s.n == 0);
+  if (threadIdx.x == 0) {
+    const uint32_t total = carry * c.Hkv, parts = min(total, gridDim.x);
+    job.nt = 0;
+    if (blockIdx.x < parts) {
+      const uint32_t run = total / parts, more = total - run * parts;
+      Walk k;
+      k.u = run * blockIdx.x + min(blockIdx.x, more);
+      k.u1 = k.u + run + (blockIdx.x < more);
+      const uint32_t want = k.u / c.Hkv;
+      int lo = 0, hi = B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= want) lo = mid; else hi = mid;
       }
+      k.b = lo;
+      kv8_seq(c, a.cu, a.kv_len, a.N, a.max_new, lo, false, k.s);
+      const uint32_t each = (lo + 1 < B ? prefix[lo + 1] : carry) - prefix[lo];  // units of a kv head
+      uint32_t rel = k.u - prefix[lo] * c.Hkv;
+      k.h = rel / each;
+      rel -= k.h * each;
+      for (k.grp = 0;; ++k.grp) {
+        const uint32_t n = tiles_of(span_of<NT>(k.s, a.G, a.window, k.grp)) + TASK_UNITS;
+        if (rel < n) break;
+        rel -= n;
+      }
+      k.t0 = rel;
+      enter<NT>(a, k, total, job);
+      if (job.nt == 0) next_task<NT>(a, k, total, job);  // the run begins behind a task's tiles
+      walk = k;
+      sums[0] = total;
     }
-    enter(u, k);
-  };
-  uint32_t u = u0;
-  Task k;
-  task_at(u, k);
-  if (k.t0 >= k.tiles) {  // the run begins behind a task's tiles
-    u += k.units;
-    if (u >= u1) return;
-    next_task(u, k);
   }
+  __syncthreads();
+  if (job.nt == 0) return;
 
   // ---------------------------------------------------------------- setup
   if (threadIdx.x == 0) {
@@ -259,23 +301,18 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   auto takes = [&](int g, int t) { return NT == 2 || (t & 1) == g; };
 
   while (true) {
-    const size_t bh = static_cast<size_t>(k.b) * c.Hkv + k.h;
-    const int row0 = k.grp * ROWS, rows = k.s.n * a.G;
-    const int nt = k.t1 - k.t0;
-    const int full_end = min(k.sp.end, k.s.len / KV8_BLOCK);  // complete blocks end here; the next one, if any, is the tail
-    int32_t* err = c.err + k.b;
-    auto pages_in = [&](int t) {  // complete pages of tile t: 0 .. 2
-      const int p = k.sp.begin + 2 * (k.t0 + t);
-      return max(0, min(2, full_end - p));
-    };
+    const size_t bh = static_cast<size_t>(job.b) * c.Hkv + job.h;
+    const int rows = job.rows, nt = job.nt, page0 = job.page, full_end = job.full_end;  // complete pages end there
+    int32_t* err = c.err + job.b;
+    auto pages_in = [&](int t) { return max(0, min(2, full_end - (page0 + 2 * t))); };  // complete pages of tile t
 
     // ---------------------------------------------------------- queries -> shared memory
     float qmul = a.scale;
     if (warp < 8 && (NT == 2 || warp < 4)) {
-      const int r = threadIdx.x & 127, rr = row0 + (NT == 2 ? (warp >> 2) * TR : 0) + r;
+      const int r = threadIdx.x & 127, rr = job.row0 + (NT == 2 ? (warp >> 2) * TR : 0) + r;
       const uint32_t dst = base + L::Q + (NT == 2 ? (warp >> 2) * 32768 : 0) + r * 128;
-      const E* p = static_cast<const E*>(a.q) + static_cast<int64_t>(k.s.row0 + rr / a.G) * a.q_tok +
-                   static_cast<int64_t>(k.h * a.G + rr % a.G) * a.q_head;
+      const E* p = static_cast<const E*>(a.q) + static_cast<int64_t>(job.tok0 + rr / a.G) * a.q_tok +
+                   static_cast<int64_t>(job.h * a.G + rr % a.G) * a.q_head;
       float inv = 1.0f;
       if (IsBf16<E>::value && rr < rows) {
         // bf16 rows become fp16 at a power of two that brings their largest value to [2^14, 2^15)
@@ -312,10 +349,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
     }
     if (NT == 1 && warp >= 4 && warp < 8) {
       // stream 1 scores the same rows
-      const int rr = row0 + (threadIdx.x & 127);
+      const int rr = job.row0 + (threadIdx.x & 127);
       if (IsBf16<E>::value && rr < rows) {
-        const E* p = static_cast<const E*>(a.q) + static_cast<int64_t>(k.s.row0 + rr / a.G) * a.q_tok +
-                     static_cast<int64_t>(k.h * a.G + rr % a.G) * a.q_head;
+        const E* p = static_cast<const E*>(a.q) + static_cast<int64_t>(job.tok0 + rr / a.G) * a.q_tok +
+                     static_cast<int64_t>(job.h * a.G + rr % a.G) * a.q_head;
         uint32_t m = 0;
 #pragma unroll 4
         for (int i = 0; i < 16; ++i) {
@@ -336,7 +373,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       const int which = warp - W_COPY;
       uint64_t* empty = which ? rv_empty : rk_empty;
       uint64_t* full = which ? rv_full : rk_full;
-      const int p_begin = k.sp.begin + 2 * k.t0, p_end = min(full_end, k.sp.begin + 2 * k.t1);
+      const int p_begin = page0, p_end = min(full_end, page0 + 2 * nt);
       auto look_up = [&](int p) { return p + lane < p_end ? reinterpret_cast<uint64_t>(kv8_page(c, bh, p + lane)) : 0ull; };
       uint64_t next = look_up(p_begin);
       for (int p = p_begin; ok && p < p_end; p += 32) {
@@ -362,19 +399,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       // scale of (page ct / 2, K or V) of tile t: fetched a tile ahead
       auto scale_of = [&](int t) {
         if (t >= nt || ct >= 2 * pages_in(t)) return 1.0f;
-        const uint8_t* page = kv8_page(c, bh, k.sp.begin + 2 * (k.t0 + t) + (ct >> 1));
+        const uint8_t* page = kv8_page(c, bh, page0 + 2 * t + (ct >> 1));
         return *reinterpret_cast<const float*>(page + (ct & 1 ? HQ_KV8_VSCALE : HQ_KV8_KSCALE));
       };
       float scale = scale_of(0);
       auto page_tail = [&](int t, int& np) {  // the tile's page np is the incomplete block
         np = pages_in(t);
-        return np < 2 && k.sp.begin + 2 * (k.t0 + t) + np < k.sp.end;
+        return np < 2 && page0 + 2 * t + np < job.end;
       };
       // K of tile t: free once the tile two before has been scored
       auto convert_k = [&](int t) {
         int np;
         const bool tail = page_tail(t, np);
-        const int T = n_tile + t, st = T & 1, p0 = k.sp.begin + 2 * (k.t0 + t);
+        const int T = n_tile + t, st = T & 1, p0 = page0 + 2 * t;
         if (T >= 2) ok = wait_for(k_empty + st, ((T >> 1) - 1) & 1, err, stop);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
@@ -425,7 +462,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           }
           // the rows' scales; past the length 1: nothing there is seen
           const int which = ct >> 6, r = ct & 63;
-          tail_sc[ct] = (p0 + np) * KV8_BLOCK + r < k.s.len
+          tail_sc[ct] = (p0 + np) * KV8_BLOCK + r < job.len
                             ? c.tail_scale[(bh * 2 + which) * HQ_KV8_TAIL + ((p0 + np) & 1) * KV8_BLOCK + r]
                             : 1.0f;
         }
@@ -436,7 +473,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       auto convert_v = [&](int t) {
         int np;
         const bool tail = page_tail(t, np);
-        const int T = n_tile + t, st = T & 1, p0 = k.sp.begin + 2 * (k.t0 + t);
+        const int T = n_tile + t, st = T & 1, p0 = page0 + 2 * t;
         if (T >= 2) ok = wait_for(v_empty + st, ((T >> 1) - 1) & 1, err, stop);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
@@ -574,9 +611,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
     } else {
       // -------------------------------------------------------- softmax
       const int g = warp >> 2, r = threadIdx.x & 127;
-      const int rr = row0 + (NT == 2 ? g * TR : 0) + r;  // row of the (sequence, kv head)
+      const int rr = job.row0 + (NT == 2 ? g * TR : 0) + r;  // row of the (sequence, kv head)
       const bool real = rr < rows;
-      const int qpos = k.s.first + rr / a.G;
+      const int qpos = job.first + rr / a.G;
       const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       const uint32_t srow = trow + TM_S + 128 * g, orow = trow + TM_O + 128 * g;
       // rows past the last have zero queries and see every key; their references
@@ -597,8 +634,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           mbar_arrive(p_full + g);
           continue;
         }
-        const int np = pages_in(t), p0 = k.sp.begin + 2 * (k.t0 + t);
-        const bool tail = np < 2 && p0 + np < k.sp.end;
+        const int np = pages_in(t), p0 = page0 + 2 * t;
+        const bool tail = np < 2 && p0 + np < job.end;
         const float4 sc0 = *reinterpret_cast<const float4*>(aux + ((n_tile + t) & 7) * 8);  // s_k, s_v, log2 s_v, 1 / s_v
         const float4 sc1 = *reinterpret_cast<const float4*>(aux + ((n_tile + t) & 7) * 8 + 4);
         // columns [lo, hi] of the tile are seen by this row
@@ -685,14 +722,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
         tmem_wait_ld();
 #pragma unroll 1
         for (int c4 = 0; c4 < 4; ++c4) {
-          const float mref = m == -INFINITY ? 0.f : m;
           const float4 sc = c4 < 2 ? sc0 : sc1;
+          const float mref = m == -INFINITY ? 0.f : m;
+          uint32_t pk[16];
+          float s0 = 0.f, s1 = 0.f;  // sums of the fp16 weights and of the softmax's
           // Weights of a page that is seen whole take the value scale into the
           // exponent, and their sum is divided by it: a product less per weight.
           // Not where it is so small that weights would underflow.
           const float lw = lef + sc.z;
-          float s0 = 0.f, s1 = 0.f;
-          uint32_t pk[16];
           if (__all_sync(0xffffffffu, seen && lw > -60.f)) {
             scores(x, c4, mref - lw);
 #pragma unroll
@@ -720,8 +757,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
               pk[i / 2] = pack_f16x2(y0, y1);
             }
           }
-          // s0: the fp16 weights' sum, s1: the softmax's
+          if (c4 < 3) tmem_ld32f(srow + 32 * (c4 + 1), x);  // the next columns, while these are checked and stored
           if (__any_sync(0xffffffffu, !(s0 <= W_LIMIT)) && fresh != c4) {  // also an infinity or NaN
+            tmem_wait_ld();
             renew(c4);
             fresh = c4;
             tmem_ld32f(srow + 32 * c4, x);
@@ -735,10 +773,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           const uint32_t w[16] = {pk[0], pk[4], pk[1], pk[5], pk[2], pk[6], pk[3], pk[7],
                                   pk[8], pk[12], pk[9], pk[13], pk[10], pk[14], pk[11], pk[15]};
           tmem_st16(srow + 16 * c4, w);
-          if (c4 < 3) {
-            tmem_ld32f(srow + 32 * (c4 + 1), x);
-            tmem_wait_ld();
-          }
+          if (c4 < 3) tmem_wait_ld();
         }
         tmem_wait_st();
         l += sum;
@@ -753,7 +788,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       tc_fence_after();
 
       // ------------------------------------------------------ the CTA's piece of the task
-      const bool whole = nt == k.tiles;
+      const bool whole = job.whole;
       auto o_cols = [&](int c4, float (&x)[32]) {
         tmem_ld32f(orow + 32 * c4, x);
         tmem_wait_ld();
@@ -782,9 +817,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       // pieces: slot 2 cta (+ 1 for the task's first), [stream's rows][column][row] and (m, E, l)
       constexpr int PIECE = TR * (D + 3);
       const int q = NT == 2 ? g : 0;
-      float* part = a.parts + (static_cast<size_t>(2 * blockIdx.x + (k.t0 == 0)) * NT + q) * PIECE;
-      const uint32_t k0 = u - k.t0;
-      const int c0 = cta_of(k0), c1 = cta_of(k0 + k.tiles - 1);
+      float* part = a.parts + (static_cast<size_t>(2 * blockIdx.x + job.head) * NT + q) * PIECE;
+      const int c0 = job.c0, c1 = job.c1;
       const bool owner = NT == 2 || g == 0;  // threads that hold the piece's rows
       float m2 = -INFINITY, e2 = -INFINITY, l2 = 0.f;
       if (NT == 1 && owner && nt > 1) {
@@ -799,8 +833,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       auto write = [&](float m, float e, float l, auto cols) {  // the row's output from its accumulators
         // accumulators are at 2^(BIAS - E), the sum at 2^-m
         const float f = m == -INFINITY ? 0.f : ex2(e - m - BIAS) / l;
-        const int64_t tok = k.s.row0 + rr / a.G;
-        const int head = k.h * a.G + rr % a.G;
+        const int64_t tok = job.tok0 + rr / a.G;
+        const int head = job.h * a.G + rr % a.G;
         E* dst = static_cast<E*>(a.out) + tok * a.o_tok + head * a.o_head;
 #pragma unroll 1
         for (int c4 = 0; c4 < 4; ++c4) {
@@ -875,12 +909,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       tc_fence_before();
     }
     __syncwarp();
-    u += k.units;
-    const bool done = u >= u1 || *stop;
     __syncthreads();  // the task's shared and tensor memory is free
     tc_fence_after();
-    if (done || *stop) break;
-    next_task(u, k);
+    if (threadIdx.x == 0) {
+      next_task<NT>(a, walk, sums[0], job);
+      if (*stop) job.nt = 0;
+    }
+    __syncthreads();
+    if (job.nt == 0) break;
   }
 
   // Products and copies that were not waited for (only after a wait that gave up)
