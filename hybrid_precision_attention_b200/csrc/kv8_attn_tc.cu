@@ -3,32 +3,33 @@
 //
 // The rows of a kv head (its G query heads x the sequence's n new tokens, row
 // r = i G + g, so that a page is read once for all of them) are taken NT x 128
-// at a time, one TMEM lane a row.  Keys go by tiles of two pages (128 positions):
-//   S = Q K^T    kind::f16, K the page's codes as fp16 (exact), 128 x 128
-//   P = 2^(S s_k - m) s_v 2^(m - E + 6) as fp16 (the block's scales in float32)
+// at a time, one TMEM lane a row.  Keys go a page (64 positions) at a time:
+//   S = Q K^T    kind::f16, K the page's codes as fp16 (exact), 128 x 64
+//   P = 2^(S s_k - m) s_v 2^(m - E + 6) as fp16 (the page's scales in float32)
 //   O += P V     kind::f16, P from TMEM (where it takes the place of S), V the
 //                page's codes as fp16
 // with the two running references m, E of kv8_attn.cu: they are set to the exact
 // maxima only when 32 of a row's weights sum to more than 2^15, whereupon what the
-// row has so far (sum, O, the tile's P) is rescaled.
+// row has so far (sum, O, the page's P) is rescaled.
 //
 // Warps of a CTA (one CTA an SM, persistent):
-//   0-7    softmax: two streams of 128 threads, a row each.  NT = 2: the streams
-//          are two row tiles over the same key tiles; NT = 1 (up to 128 rows):
-//          the same rows, each stream taking every other key tile, joined at the end
+//   0-7    softmax: two streams of 128 threads, a row each, with two pages of
+//          scores each, so that one page's products run while the other's weights
+//          are made.  NT = 2: the streams are two row tiles over the same pages;
+//          NT = 1 (up to 128 rows): the same rows, each stream taking every other
+//          page, joined at the end
 //   8-11   converters: codes of a page -> fp16 in the 128-byte-swizzled operand
-//          layouts, K as [key][d], V as [d][key], both K-major, two stages of each.
+//          layouts, K as [key][d], V as [d][key], both K-major, four stages of each.
 //          The page's V order gives a thread 4 keys of one d, which it stores as 8
 //          bytes: the keys of 16 stand as t, t+1, t+8, t+9 for t = 0, 2, 4, 6, and
 //          P's columns follow the same order
 //   12, 13 copies of the pages' codes, K and V (bulk copies, no multicast)
 //   14     TMEM allocation, tcgen05.mma issue (event-driven, one thread)
-// Bound: shared-memory bandwidth first (per two row tiles and 128 keys 192 KB of
-// operands, 64 KB converted, 64 KB of codes in and out: 2500 cycles at 128
-// bytes), then the tensor cores and the exponential unit (2048 cycles each).
-// With P through shared memory and one stage of K and V it took 8000.
+// Bound: two row tiles and 128 keys take 2048 cycles of products, 2048 of
+// exponentials and, at 128 bytes a cycle, 3000 of shared memory (256 KB of
+// operands, 64 KB converted, 64 KB of codes in and out).
 //
-// Work: runs of equal units (key tiles) as in kv8_attn.cu; pieces of a task that
+// Work: runs of equal units (pages) as in kv8_attn.cu; pieces of a task that
 // CTAs share are joined by the CTA that delivers the last one, in order.
 // All waits are bounded (about 1 s): a timeout sets the sequence's error bit and
 // the CTA drains its copies and products before it releases TMEM.
@@ -42,15 +43,17 @@
 namespace hq {
 namespace {
 
-constexpr int TR = 128, TK = 128;          // rows of a tile, keys of a tile
+constexpr int TR = 128;                    // rows of a tile
+constexpr int STAGES = 4;                  // pages of K, and of V, as operands
 constexpr int W_CONV = 8, W_COPY = 12, W_MMA = 14;  // W_COPY: K, W_COPY + 1: V
 constexpr int THREADS = 15 * 32;
 constexpr float BIAS = 6.0f;               // log2 of the fp16 weight at both references
 constexpr float W_LIMIT = 32768.0f;        // sum of 32 fp16 weights above which the references are set anew
-constexpr int TASK_UNITS = 4;              // what a task costs besides its tiles, in tiles
+constexpr int TASK_UNITS = 8;              // what a task costs besides its pages, in pages
 constexpr uint32_t TMEM_COLS = 512;        // S of the streams 0 .. 255, O 256 .. 511
 constexpr uint32_t TM_S = 0, TM_O = 256;
-constexpr uint32_t IDESC = idesc_make(0, 0, 0, TR, TK);  // fp16, K-major A and B, f32 accumulate
+// fp16, K-major A and B, f32 accumulate
+constexpr uint32_t IDESC_QK = idesc_make(0, 0, 0, TR, KV8_BLOCK), IDESC_PV = idesc_make(0, 0, 0, TR, D);
 constexpr int HALF = HQ_KV8_V;             // bytes of a page's K (or V) codes
 
 // shared memory (from a 1024-byte aligned base): operands as 128-byte-swizzled
@@ -58,19 +61,19 @@ constexpr int HALF = HQ_KV8_V;             // bytes of a page's K (or V) codes
 template <int NT>
 struct Lay {
   static constexpr int Q = 0;                    // NT x 2 regions (d halves)
-  static constexpr int K = Q + NT * 32768;       // 2 stages x 2 regions (d halves): [key][64 d]
-  static constexpr int V = K + 65536;            // 2 stages x 2 regions (pages): [d][64 keys]
-  static constexpr int RAW = V + 65536;          // codes: slots of a page's K or V
+  static constexpr int K = Q + NT * 32768;       // stages x 2 regions (d halves): [64 keys][64 d]
+  static constexpr int V = K + STAGES * 16384;   // stages: [d][64 keys]
+  static constexpr int RAW = V + STAGES * 16384; // codes: slots of a page's K or V
   static constexpr int RK = NT == 2 ? 2 : 4;     // slots of K; as many of V
-  static constexpr int AUX = RAW + 2 * RK * HALF;  // 8 tiles x 2 pages x (s_k, s_v, log2 s_v, 1 / s_v); the tail's 64 K and 64 V scales
-  static constexpr int BARS = AUX + 8 * 32 + 512;
-  static constexpr int MISC = BARS + 32 * 8;     // TMEM base, flags, the plan's sums, walk and job
+  static constexpr int AUX = RAW + 2 * RK * HALF;  // 8 pages x (s_k, s_v, log2 s_v, 1 / s_v); the tail's 64 K and 64 V scales
+  static constexpr int BARS = AUX + 8 * 16 + 512;
+  static constexpr int MISC = BARS + 48 * 8;     // TMEM base, flags, the plan's sums, walk and job
   static constexpr int JOIN = RAW;               // NT = 1: (m, E, l) of stream 1's rows, once the task's copies are done with
   static constexpr int BYTES = MISC + 80 + 144 + 1024;  // with the alignment
 };
 
-// Key tiles of row group grp of a sequence: blocks [begin, end) and the positions
-// of its first and last row.
+// Pages [begin, end) that row group grp of a sequence sees, and the positions of its
+// first and last row.
 struct Span {
   int begin, end, q_lo, q_hi;
 };
@@ -84,13 +87,13 @@ __device__ __forceinline__ Span span_of(const Kv8Seq& s, int G, int window, int 
   x.end = x.q_hi / KV8_BLOCK + 1;
   return x;
 }
-__device__ __forceinline__ int tiles_of(const Span& x) { return (x.end - x.begin + 1) / 2; }
+__device__ __forceinline__ int pages_of(const Span& x) { return x.end - x.begin; }
 
-// A task (sequence, kv head, row group) of a CTA's run, [t0, t1) of its key tiles
+// A task (sequence, kv head, row group) of a CTA's run, [t0, t1) of its pages
 // ours, and what the roles need of it.  One thread walks the run; both lie in
 // shared memory, for want of registers.
 struct Walk {
-  int b, h, grp, tiles, t0, t1;  // no tiles are ours where the run begins behind them
+  int b, h, grp, pages, t0, t1;  // no pages are ours where the run begins behind them
   uint32_t u, u1;                // the task's first unit of ours, the run's end
   uint32_t units;                // ours of the task
   Kv8Seq s;
@@ -99,9 +102,9 @@ struct Walk {
 struct Job {
   int b, h, row0, rows, tok0;    // rows row0 .. of the kv head's `rows`; the sequence's first row of q
   int first, len;                // position of its first new token, its length
-  int page, full_end, end;       // first page of our tiles; complete pages end; the task's pages end
-  int nt;                        // our tiles: 0, the run has no more
-  int head, whole;               // the task's first tile is ours; all are
+  int page, full_end;            // our first page; complete pages end there, the next one is the tail
+  int nt;                        // our pages: 0, the run has no more
+  int head, whole;               // the task's first page is ours; all are
   int c0, c1;                    // the CTAs that share the task
 };
 
@@ -126,13 +129,13 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
-// The run's task at k.u (k.t0 of its tiles belong to the CTAs before).
+// The run's task at k.u (k.t0 of its pages belong to the CTAs before).
 template <int NT>
 __device__ __noinline__ void enter(const Kv8AttnArgs& a, Walk& k, uint32_t total, Job& j) {
   k.sp = span_of<NT>(k.s, a.G, a.window, k.grp);
-  k.tiles = tiles_of(k.sp);
-  k.units = min(static_cast<uint32_t>(k.tiles + TASK_UNITS - k.t0), k.u1 - k.u);
-  k.t1 = min(k.tiles, k.t0 + static_cast<int>(k.units));
+  k.pages = pages_of(k.sp);
+  k.units = min(static_cast<uint32_t>(k.pages + TASK_UNITS - k.t0), k.u1 - k.u);
+  k.t1 = min(k.pages, k.t0 + static_cast<int>(k.units));
   const uint32_t parts = min(total, gridDim.x), run = total / parts, more = total - run * parts;
   // the first `more` runs have a unit more than the others
   auto cta_of = [&](uint32_t u) { return u < more * (run + 1) ? u / (run + 1) : more + (u - more * (run + 1)) / run; };
@@ -143,14 +146,13 @@ __device__ __noinline__ void enter(const Kv8AttnArgs& a, Walk& k, uint32_t total
   j.tok0 = k.s.row0;
   j.first = k.s.first;
   j.len = k.s.len;
-  j.page = k.sp.begin + 2 * k.t0;
+  j.page = k.sp.begin + k.t0;
   j.full_end = min(k.sp.end, k.s.len / KV8_BLOCK);
-  j.end = k.sp.end;
   j.nt = max(0, k.t1 - k.t0);
   j.head = k.t0 == 0;
-  j.whole = j.nt == k.tiles;
+  j.whole = j.nt == k.pages;
   j.c0 = cta_of(k.u - k.t0);
-  j.c1 = cta_of(k.u - k.t0 + k.tiles - 1);
+  j.c1 = cta_of(k.u - k.t0 + k.pages - 1);
 }
 // The run's next task, or none (j.nt = 0).
 template <int NT>
@@ -179,9 +181,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BARS);
-  uint64_t *rk_full = bars, *rk_empty = bars + 4, *rv_full = bars + 8, *rv_empty = bars + 12, *s_full = bars + 16, *p_full = bars + 18,
-           *o_done = bars + 20, *k_full = bars + 22, *k_empty = bars + 24, *v_full = bars + 26, *v_empty = bars + 28;
-  uint64_t& drain = bars[30];
+  // of the slots of codes, of the stages of operands, and [stream * 2 + page % 2]
+  uint64_t *rk_full = bars, *rk_empty = bars + 4, *rv_full = bars + 8, *rv_empty = bars + 12, *k_full = bars + 16, *k_empty = bars + 20,
+           *v_full = bars + 24, *v_empty = bars + 28, *s_full = bars + 32, *p_full = bars + 36, *o_done = bars + 40;
+  uint64_t& drain = bars[44];
   uint32_t& tmem_sh = *reinterpret_cast<uint32_t*>(sm + L::MISC);
   int* flags = reinterpret_cast<int*>(sm + L::MISC + 4);                  // stop, last
   uint32_t* sums = reinterpret_cast<uint32_t*>(sm + L::MISC + 16);        // [warps]
@@ -193,7 +196,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   static_assert(HQ_KV8_MAX_BATCH * 4 <= 32768, "the plan fits where the queries go");
   const hq_kv8_cache& c = a.c;
   const int B = c.B;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // the roles' branches are uniform
 
   // ---------------------------------------------------------------- plan
   uint32_t carry = 0;
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       Kv8Seq s;
       kv8_seq(c, a.cu, a.kv_len, a.N, a.max_new, b, blockIdx.x == 0, s);
       const int groups = (s.n * a.G + ROWS - 1) / ROWS;
-      for (int i = 0; i < groups; ++i) n += tiles_of(span_of<NT>(s, a.G, a.window, i)) + TASK_UNITS;
+      for (int i = 0; i < groups; ++i) n += pages_of(span_of<NT>(s, a.G, a.window, i)) + TASK_UNITS;
     }
     uint32_t x = n;
 #pragma unroll
@@ -243,13 +246,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       k.h = rel / each;
       rel -= k.h * each;
       for (k.grp = 0;; ++k.grp) {
-        const uint32_t n = tiles_of(span_of<NT>(k.s, a.G, a.window, k.grp)) + TASK_UNITS;
+        const uint32_t n = pages_of(span_of<NT>(k.s, a.G, a.window, k.grp)) + TASK_UNITS;
         if (rel < n) break;
         rel -= n;
       }
       k.t0 = rel;
       enter<NT>(a, k, total, job);
-      if (job.nt == 0) next_task<NT>(a, k, total, job);  // the run begins behind a task's tiles
+      if (job.nt == 0) next_task<NT>(a, k, total, job);  // the run begins behind a task's pages
       walk = k;
       sums[0] = total;
     }
@@ -265,14 +268,16 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       mbar_init(rv_full + i, 1);
       mbar_init(rv_empty + i, 128);
     }
-    for (int g = 0; g < 2; ++g) {
-      mbar_init(k_full + g, 128);
-      mbar_init(k_empty + g, 1);
-      mbar_init(v_full + g, 128);
-      mbar_init(v_empty + g, 1);
-      mbar_init(s_full + g, 1);
-      mbar_init(p_full + g, 128);
-      mbar_init(o_done + g, 1);
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(k_full + i, 128);
+      mbar_init(k_empty + i, 1);
+      mbar_init(v_full + i, 128);
+      mbar_init(v_empty + i, 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 128);
+      mbar_init(o_done + i, 1);
     }
     mbar_init(&drain, 1);
     flags[0] = 0;
@@ -289,22 +294,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   const uint32_t base = smem_u32(sm);
   volatile int* stop = flags;
   float* aux = reinterpret_cast<float*>(sm + L::AUX);
-  float* tail_sc = aux + 8 * 8;  // [K, V][64]
+  float* tail_sc = aux + 8 * 4;  // [K, V][64]
 
-  // running uses of each barrier, kept by the roles that wait on it; a tile that
-  // stream g takes is its j-th: NT = 2 every tile, NT = 1 every other
-  int n_raw = 0;                  // copied (copy warps)
-  int raw_k = 0, raw_v = 0;       // converted (converters)
-  int n_tile = 0;                 // tiles (converters, MMA, aux slot of the softmax)
-  int n_str[2] = {0, 0};          // tiles of each stream (softmax, MMA)
+  // running uses of each barrier, kept by the roles that wait on it
+  int n_raw = 0;                  // copied pages (copy warps), those before the task's (converters)
+  int n_page = 0;                 // pages before the task's (converters, MMA, the softmax's scales)
+  int n_str[2] = {0, 0};          // pages of each stream (softmax, MMA)
   bool ok = true;
   auto takes = [&](int g, int t) { return NT == 2 || (t & 1) == g; };
 
   while (true) {
     const size_t bh = static_cast<size_t>(job.b) * c.Hkv + job.h;
-    const int rows = job.rows, nt = job.nt, page0 = job.page, full_end = job.full_end;  // complete pages end there
+    const int rows = job.rows, nt = job.nt, page0 = job.page;
+    const int full = min(nt, job.full_end - page0);  // our complete pages; the tail may follow
     int32_t* err = c.err + job.b;
-    auto pages_in = [&](int t) { return max(0, min(2, full_end - (page0 + 2 * t))); };  // complete pages of tile t
 
     // ---------------------------------------------------------- queries -> shared memory
     float qmul = a.scale;
@@ -371,9 +374,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       // -------------------------------------------------------- copies
       // 32 pages looked up at a time, and the next 32 while these are copied
       const int which = warp - W_COPY;
-      uint64_t* empty = which ? rv_empty : rk_empty;
-      uint64_t* full = which ? rv_full : rk_full;
-      const int p_begin = page0, p_end = min(full_end, page0 + 2 * nt);
+      uint64_t* slot_empty = which ? rv_empty : rk_empty;
+      uint64_t* slot_full = which ? rv_full : rk_full;
+      const int p_begin = page0, p_end = page0 + full;
       auto look_up = [&](int p) { return p + lane < p_end ? reinterpret_cast<uint64_t>(kv8_page(c, bh, p + lane)) : 0ull; };
       uint64_t next = look_up(p_begin);
       for (int p = p_begin; ok && p < p_end; p += 32) {
@@ -383,12 +386,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
         for (int i = 0; ok && i < m; ++i, ++n_raw) {
           const int sl = n_raw % RK;
           const uint8_t* page = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, now, i));
-          if (n_raw >= RK) ok = wait_for(empty + sl, (n_raw / RK - 1) & 1, err, stop);
+          if (n_raw >= RK) ok = wait_for(slot_empty + sl, (n_raw / RK - 1) & 1, err, stop);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane == 0) {
-            mbar_arrive_expect_tx(full + sl, HALF);
-            bulk_g2s(sm + L::RAW + (which * RK + sl) * HALF, page + which * HQ_KV8_V, HALF, full + sl);
+            mbar_arrive_expect_tx(slot_full + sl, HALF);
+            bulk_g2s(sm + L::RAW + (which * RK + sl) * HALF, page + which * HQ_KV8_V, HALF, slot_full + sl);
           }
         }
       }
@@ -396,37 +399,37 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       // -------------------------------------------------------- converters
       const int ct = threadIdx.x - W_CONV * 32, cw = ct >> 5;  // thread of 128, warp of 4
       const int g = lane >> 2, t4 = lane & 3;
-      // scale of (page ct / 2, K or V) of tile t: fetched a tile ahead
+      // K and V scale of page t (threads 0 and 1): fetched two pages ahead
       auto scale_of = [&](int t) {
-        if (t >= nt || ct >= 2 * pages_in(t)) return 1.0f;
-        const uint8_t* page = kv8_page(c, bh, page0 + 2 * t + (ct >> 1));
-        return *reinterpret_cast<const float*>(page + (ct & 1 ? HQ_KV8_VSCALE : HQ_KV8_KSCALE));
+        if (t >= full || ct >= 2) return 1.0f;
+        return *reinterpret_cast<const float*>(kv8_page(c, bh, page0 + t) + (ct ? HQ_KV8_VSCALE : HQ_KV8_KSCALE));
       };
-      float scale = scale_of(0);
-      auto page_tail = [&](int t, int& np) {  // the tile's page np is the incomplete block
-        np = pages_in(t);
-        return np < 2 && page0 + 2 * t + np < job.end;
-      };
-      // K of tile t: free once the tile two before has been scored
+      float scale = scale_of(0), scale_next = scale_of(1);
+      // K of page t: free once the page four before has been scored
       auto convert_k = [&](int t) {
-        int np;
-        const bool tail = page_tail(t, np);
-        const int T = n_tile + t, st = T & 1, p0 = page0 + 2 * t;
-        if (T >= 2) ok = wait_for(k_empty + st, ((T >> 1) - 1) & 1, err, stop);
+        const int T = n_page + t, st = T % STAGES;
+        if (T >= STAGES) ok = wait_for(k_empty + st, (T / STAGES - 1) & 1, err, stop);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
-        if (ct < 4) {
-          float* x = aux + (T & 7) * 8 + (ct >> 1) * 4;
-          x[ct & 1] = scale;
-          if (ct & 1) {
+        if (ct < 2) {
+          float* x = aux + (T & 7) * 4;
+          x[ct] = scale;
+          if (ct) {
             x[2] = log2f(scale);
             x[3] = 1.0f / scale;
           }
         }
-        scale = scale_of(t + 1);
-        const uint32_t dst = base + L::K + st * 32768;
-        for (int pg = 0; pg < np; ++pg) {
-          const int n = raw_k + pg, sl = n % RK;
+        scale = scale_next;
+        scale_next = scale_of(t + 2);
+        const uint32_t dst = base + L::K + st * 16384;
+        uint32_t y[8] = {};
+        auto put = [&](int e) {  // 512-byte piece of codes: 8 keys x 64 d
+          const uint32_t row = dst + (e & 1) * 8192 + ((e >> 1) * 8 + g) * 128;
+          sts128(row + (((2 * t4) ^ g) << 4), y[0], y[1], y[2], y[3]);
+          sts128(row + (((2 * t4 + 1) ^ g) << 4), y[4], y[5], y[6], y[7]);
+        };
+        if (t < full) {
+          const int n = n_raw + t, sl = n % RK;
           ok = wait_for(rk_full + sl, (n / RK) & 1, err, stop);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) return;
@@ -437,51 +440,39 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           mbar_arrive(rk_empty + sl);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int e = cw * 4 + i;  // 512-byte piece: 8 tokens x 64 d
-            uint32_t y[8];
             kv8_half4<FMT>(x[i].x, y[0], y[1]);
             kv8_half4<FMT>(x[i].y, y[2], y[3]);
             kv8_half4<FMT>(x[i].z, y[4], y[5]);
             kv8_half4<FMT>(x[i].w, y[6], y[7]);
-            const uint32_t row = dst + (e & 1) * 16384 + (pg * 64 + (e >> 1) * 8 + g) * 128;
-            sts128(row + (((2 * t4) ^ g) << 4), y[0], y[1], y[2], y[3]);
-            sts128(row + (((2 * t4 + 1) ^ g) << 4), y[4], y[5], y[6], y[7]);
+            put(cw * 4 + i);
           }
-        }
-        raw_k += np;
-        if (tail) {
-          const size_t half = bh * 2 + ((p0 + np) & 1);
-          const uint4* src = reinterpret_cast<const uint4*>(c.tail_k + half * KV8_BLOCK * D);
+        } else {
+          const uint4* src = reinterpret_cast<const uint4*>(c.tail_k + (bh * 2 + ((page0 + t) & 1)) * KV8_BLOCK * D);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int e = cw * 4 + i;
-            const uint4 x = src[(e * 32 + lane) * 2], y = src[(e * 32 + lane) * 2 + 1];
-            const uint32_t row = dst + (e & 1) * 16384 + (np * 64 + (e >> 1) * 8 + g) * 128;
-            sts128(row + (((2 * t4) ^ g) << 4), x.x, x.y, x.z, x.w);
-            sts128(row + (((2 * t4 + 1) ^ g) << 4), y.x, y.y, y.z, y.w);
+            *reinterpret_cast<uint4*>(y) = src[((cw * 4 + i) * 32 + lane) * 2];
+            *reinterpret_cast<uint4*>(y + 4) = src[((cw * 4 + i) * 32 + lane) * 2 + 1];
+            put(cw * 4 + i);
           }
           // the rows' scales; past the length 1: nothing there is seen
           const int which = ct >> 6, r = ct & 63;
-          tail_sc[ct] = (p0 + np) * KV8_BLOCK + r < job.len
-                            ? c.tail_scale[(bh * 2 + which) * HQ_KV8_TAIL + ((p0 + np) & 1) * KV8_BLOCK + r]
+          tail_sc[ct] = (page0 + t) * KV8_BLOCK + r < job.len
+                            ? c.tail_scale[(bh * 2 + which) * HQ_KV8_TAIL + ((page0 + t) & 1) * KV8_BLOCK + r]
                             : 1.0f;
         }
         fence_proxy_async_smem();
         mbar_arrive(k_full + st);
       };
-      // V of tile t: free once the tile two before has been added
+      // V of page t: free once the page four before has been added
       auto convert_v = [&](int t) {
-        int np;
-        const bool tail = page_tail(t, np);
-        const int T = n_tile + t, st = T & 1, p0 = page0 + 2 * t;
-        if (T >= 2) ok = wait_for(v_empty + st, ((T >> 1) - 1) & 1, err, stop);
+        const int T = n_page + t, st = T % STAGES;
+        if (T >= STAGES) ok = wait_for(v_empty + st, (T / STAGES - 1) & 1, err, stop);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         // 16-byte chunk (16 tokens cw, 32 d i, d % 8 = g, token pair t4): 4 words of 4 tokens of one d
-        const uint32_t col = (((cw * 2 + (t4 >> 1)) ^ g) << 4) + (t4 & 1) * 8;
-        auto vrow = [&](int pg, int d) { return base + L::V + st * 32768 + pg * 16384 + d * 128 + col; };
-        for (int pg = 0; pg < np; ++pg) {
-          const int n = raw_v + pg, sl = n % RK;
+        const uint32_t dst = base + L::V + st * 16384 + g * 128 + (((cw * 2 + (t4 >> 1)) ^ g) << 4) + (t4 & 1) * 8;
+        if (t < full) {
+          const int n = n_raw + t, sl = n % RK;
           ok = wait_for(rv_full + sl, (n / RK) & 1, err, stop);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) return;
@@ -494,74 +485,66 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           for (int i = 0; i < 4; ++i) {
             uint32_t y[2];
             kv8_half4<FMT>(x[i].x, y[0], y[1]);
-            sts64(vrow(pg, i * 32 + g), y[0], y[1]);
+            sts64(dst + (i * 32) * 128, y[0], y[1]);
             kv8_half4<FMT>(x[i].y, y[0], y[1]);
-            sts64(vrow(pg, i * 32 + 8 + g), y[0], y[1]);
+            sts64(dst + (i * 32 + 8) * 128, y[0], y[1]);
             kv8_half4<FMT>(x[i].z, y[0], y[1]);
-            sts64(vrow(pg, i * 32 + 16 + g), y[0], y[1]);
+            sts64(dst + (i * 32 + 16) * 128, y[0], y[1]);
             kv8_half4<FMT>(x[i].w, y[0], y[1]);
-            sts64(vrow(pg, i * 32 + 24 + g), y[0], y[1]);
+            sts64(dst + (i * 32 + 24) * 128, y[0], y[1]);
           }
-        }
-        raw_v += np;
-        for (int pg = np; pg < 2; ++pg) {
-          // the tail's values, or zeros where the tile ends: a weight of 0 must not meet what is left there
-          const bool have = tail && pg == np;
-          const uint4* src = reinterpret_cast<const uint4*>(c.tail_v + (bh * 2 + ((p0 + np) & 1)) * KV8_BLOCK * D);
+        } else {
+          const uint4* src = reinterpret_cast<const uint4*>(c.tail_v + (bh * 2 + ((page0 + t) & 1)) * KV8_BLOCK * D);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-            if (have) {
-              x = src[((cw * 4 + i) * 32 + lane) * 2];
-              y = src[((cw * 4 + i) * 32 + lane) * 2 + 1];
-            }
-            sts64(vrow(pg, i * 32 + g), x.x, x.y);
-            sts64(vrow(pg, i * 32 + 8 + g), x.z, x.w);
-            sts64(vrow(pg, i * 32 + 16 + g), y.x, y.y);
-            sts64(vrow(pg, i * 32 + 24 + g), y.z, y.w);
+            const uint4 x = src[((cw * 4 + i) * 32 + lane) * 2], y = src[((cw * 4 + i) * 32 + lane) * 2 + 1];
+            sts64(dst + (i * 32) * 128, x.x, x.y);
+            sts64(dst + (i * 32 + 8) * 128, x.z, x.w);
+            sts64(dst + (i * 32 + 16) * 128, y.x, y.y);
+            sts64(dst + (i * 32 + 24) * 128, y.z, y.w);
           }
         }
         fence_proxy_async_smem();
         mbar_arrive(v_full + st);
       };
-      // K runs a tile ahead of V: a tile is scored before its values are needed
-      convert_k(0);
-      for (int t = 0; ok && t < nt; ++t) {
-        if (t + 1 < nt) convert_k(t + 1);
-        if (ok) convert_v(t);
+      // K runs two pages ahead of V: a page is scored before its values are needed
+      for (int t = 0; ok && t < nt + 2; ++t) {
+        if (t < nt) convert_k(t);
+        if (ok && t >= 2) convert_v(t - 2);
       }
-      n_tile += nt;
+      n_raw += full;
+      n_page += nt;
     } else if (warp == W_MMA) {
       // -------------------------------------------------------- MMA issue
-      if (lane == 0 && ok) {
-        auto issue_qk = [&](int g, int st) {
+      // the whole warp, in uniform control flow; its leader issues
+      if (ok) {
+        const uint32_t leader = elect_leader();
+        auto ready = [](uint64_t* bar, int parity) { return __any_sync(0xffffffffu, mbar_test_wait(bar, parity)); };
+        auto issue_qk = [&](int g, int j, int st) {
           tc_fence_after();
-          const uint32_t Qs = base + L::Q + (NT == 2 ? g * 32768 : 0), Ks = base + L::K + st * 32768;
+          const uint32_t Qs = base + L::Q + (NT == 2 ? g * 32768 : 0), Ks = base + L::K + st * 16384;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + 32 * (kk & 3);
-            umma_f16(tmem + TM_S + 128 * g, sdesc_sw128(Qs + off, 16, 1024), sdesc_sw128(Ks + off, 16, 1024), IDESC, kk > 0);
-          }
-          umma_commit(s_full + g);
+          for (int kk = 0; kk < 8; ++kk)
+            umma_f16_warp(leader, tmem + TM_S + 128 * g + 64 * (j & 1), sdesc_sw128(Qs + (kk >> 2) * 16384 + 32 * (kk & 3), 16, 1024),
+                     sdesc_sw128(Ks + (kk >> 2) * 8192 + 32 * (kk & 3), 16, 1024), IDESC_QK, kk > 0);
+          umma_commit_warp(leader, s_full + 2 * g + (j & 1));
         };
-        auto issue_pv = [&](int g, int st, bool first) {
+        auto issue_pv = [&](int g, int j, int st, bool first) {
           tc_fence_after();
-          const uint32_t Vs = base + L::V + st * 32768;
+          const uint32_t Vs = base + L::V + st * 16384;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + 32 * (kk & 3);
-            umma_f16_ta(tmem + TM_O + 128 * g, tmem + TM_S + 128 * g + 8 * kk, sdesc_sw128(Vs + off, 16, 1024), IDESC,
-                        !first || kk > 0 ? 1u : 0u);
-          }
-          umma_commit(o_done + g);
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f16_ta_warp(leader, tmem + TM_O + 128 * g, tmem + TM_S + 128 * g + 64 * (j & 1) + 8 * kk, sdesc_sw128(Vs + 32 * kk, 16, 1024),
+                        IDESC_PV, !first || kk > 0 ? 1u : 0u);
+          umma_commit_warp(leader, o_done + 2 * g + (j & 1));
         };
-        // A stream goes QK, PV, QK, .. (its P lies where its S does); whichever
-        // stream is ready goes next.  A tile's operand is released when every
-        // stream that takes it has been issued.
-        int tq[2], tp[2], jq[2];  // next tile of each stream to score / to add, and the former's number in the stream
+        // A stream's j-th page goes QK, weights, PV; its scores take the place of the
+        // (j - 2)-th page's weights.  Whichever stream is ready goes next.  A page's
+        // operand is released when every stream that takes it has been issued.
+        int tq[2], tp[2], jq[2], jp[2];  // next page of each stream to score / to add, and its number in the stream
         for (int g = 0; g < 2; ++g) {
           tq[g] = tp[g] = NT == 2 ? 0 : g;
-          jq[g] = n_str[g];
+          jq[g] = jp[g] = n_str[g];
         }
         const int step = NT == 2 ? 1 : 2;
         uint64_t t_last = 0;
@@ -570,21 +553,24 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           bool progress = false;
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            if (tp[g] == tq[g]) {
-              const int t = tq[g], T = n_tile + t;
-              if (t < nt && (t < step || mbar_test_wait(o_done + g, (jq[g] - 1) & 1)) && mbar_test_wait(k_full + (T & 1), (T >> 1) & 1)) {
-                issue_qk(g, T & 1);
-                if (NT == 1 || tq[g ^ 1] > t) umma_commit(k_empty + (T & 1));
-                tq[g] = t + step;
-                ++jq[g];
+            {
+              const int t = tp[g], j = jp[g], T = n_page + t, st = T % STAGES;
+              if (t < tq[g] && ready(p_full + 2 * g + (j & 1), (j >> 1) & 1) && ready(v_full + st, (T / STAGES) & 1)) {
+                issue_pv(g, j, st, t < step);
+                if (NT == 1 || tp[g ^ 1] > t) umma_commit_warp(leader, v_empty + st);
+                tp[g] = t + step;
+                ++jp[g];
                 progress = true;
               }
-            } else {
-              const int t = tp[g], T = n_tile + t;
-              if (mbar_test_wait(p_full + g, (jq[g] - 1) & 1) && mbar_test_wait(v_full + (T & 1), (T >> 1) & 1)) {
-                issue_pv(g, T & 1, t < step);
-                if (NT == 1 || tp[g ^ 1] > t) umma_commit(v_empty + (T & 1));
-                tp[g] = t + step;
+            }
+            {
+              const int t = tq[g], j = jq[g], T = n_page + t, st = T % STAGES;
+              if (t < nt && j - jp[g] < 2 && (t < 2 * step || ready(o_done + 2 * g + (j & 1), ((j >> 1) - 1) & 1)) &&
+                  ready(k_full + st, (T / STAGES) & 1)) {
+                issue_qk(g, j, st);
+                if (NT == 1 || tq[g ^ 1] > t) umma_commit_warp(leader, k_empty + st);
+                tq[g] = t + step;
+                ++jq[g];
                 progress = true;
               }
             }
@@ -592,13 +578,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           if (progress) {
             idle = 0;
           } else if (++idle < 1024) {
-          } else if (*stop) {
+          } else if (__any_sync(0xffffffffu, *stop)) {
             ok = false;
             break;
           } else if (idle == 1024) {
             t_last = global_ns();  // the clock is read only once nothing has been ready for a while
-          } else if (global_ns() - t_last > 1000000000ull) {
-            atomicOr(reinterpret_cast<unsigned int*>(err), HQ_DEVERR_TIMEOUT);
+          } else if (__any_sync(0xffffffffu, global_ns() - t_last > 1000000000ull)) {
+            if (lane == 0) atomicOr(reinterpret_cast<unsigned int*>(err), HQ_DEVERR_TIMEOUT);
             *stop = 1;
             ok = false;
             break;
@@ -607,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
         n_str[0] = jq[0];
         n_str[1] = jq[1];
       }
-      n_tile += nt;
+      n_page += nt;
     } else {
       // -------------------------------------------------------- softmax
       const int g = warp >> 2, r = threadIdx.x & 127;
@@ -615,60 +601,60 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       const bool real = rr < rows;
       const int qpos = job.first + rr / a.G;
       const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-      const uint32_t srow = trow + TM_S + 128 * g, orow = trow + TM_O + 128 * g;
+      const uint32_t orow = trow + TM_O + 128 * g;
       // rows past the last have zero queries and see every key; their references
       // stay at 1.  A warp without a row only keeps the barriers going.
       float m = real ? -INFINITY : 0.f, e = real ? -INFINITY : 0.f, l = 0.f;
       float lef = real ? -INFINITY : 0.f, ref = real ? 0.f : 1.f;  // log2 of 2^(m - E + BIAS), and its inverse
       const bool idle = !__any_sync(0xffffffffu, real);
-      bool any = false;  // a tile was taken
+      bool any = false;  // a page was taken
       for (int t = 0; t < nt; ++t) {
         if (!takes(g, t)) continue;
-        ok = ok && wait_for(s_full + g, n_str[g] & 1, err, stop);
+        const int j = n_str[g], sb = 2 * g + (j & 1);
+        const uint32_t srow = trow + TM_S + 128 * g + 64 * (j & 1);
+        ok = ok && wait_for(s_full + sb, (j >> 1) & 1, err, stop);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         if (idle) {
           any = true;
           ++n_str[g];
-          mbar_arrive(p_full + g);
+          mbar_arrive(p_full + sb);
           continue;
         }
-        const int np = pages_in(t), p0 = page0 + 2 * t;
-        const bool tail = np < 2 && p0 + np < job.end;
-        const float4 sc0 = *reinterpret_cast<const float4*>(aux + ((n_tile + t) & 7) * 8);  // s_k, s_v, log2 s_v, 1 / s_v
-        const float4 sc1 = *reinterpret_cast<const float4*>(aux + ((n_tile + t) & 7) * 8 + 4);
-        // columns [lo, hi] of the tile are seen by this row
-        const int hi = real ? qpos - p0 * KV8_BLOCK : TK, lo = real && a.window > 0 ? hi - a.window + 1 : 0;
-        // all columns seen and no tail in the tile
-        const bool seen = __all_sync(0xffffffffu, !tail && np == 2 && hi >= TK - 1 && lo <= 0);
-        // scores of columns 32 c4 .. + 31 less mref: masked ones -inf
+        float x[32];
+        tmem_ld32f(srow, x);
+        const bool tail = t >= full;
+        const float4 sc = *reinterpret_cast<const float4*>(aux + ((n_page + t) & 7) * 4);  // s_k, s_v, log2 s_v, 1 / s_v
+        // columns [lo, hi] of the page are seen by this row
+        const int hi = real ? qpos - (page0 + t) * KV8_BLOCK : KV8_BLOCK, lo = real && a.window > 0 ? hi - a.window + 1 : 0;
+        const bool seen = __all_sync(0xffffffffu, !tail && hi >= KV8_BLOCK - 1 && lo <= 0);  // all columns, by 16-bit rows none
+        // scores of columns 32 c .. + 31 less mref: masked ones -inf
         auto scores = [&](float (&x)[32], int c4, float mref) {
-          const float mul = qmul * (c4 < 2 ? sc0.x : sc1.x);
+          const float mul = qmul * sc.x;
           if (seen) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = fmaf(x[i], mul, -mref);
           } else {
-            const bool tl = tail && (c4 >> 1) == np;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const int col = 32 * c4 + i;
-              const float f = tl ? qmul * tail_sc[col & 63] : mul;
+              const float f = tail ? qmul * tail_sc[col] : mul;
               x[i] = col >= lo && col <= hi ? fmaf(x[i], f, -mref) : -INFINITY;
             }
           }
         };
         // The references anew at columns 32 c4: the exact maximum of the columns
-        // from there on; sums, O and the tile's weights so far are rescaled.
+        // from there on; sums, O and the page's weights so far are rescaled.
         float sum = 0.f;
         auto renew = [&](int c4) {
-          float vtop = fmaxf(np > 0 ? sc0.y : 0.f, np > 1 ? sc1.y : 0.f);  // ignores NaN
+          float vtop = tail ? 0.f : fmaxf(sc.y, 0.f);  // ignores NaN
           if (tail)
             for (int i = 0; i < 64; ++i) vtop = fmaxf(vtop, tail_sc[64 + i]);
           if (!(vtop > 0.f)) vtop = 1.f;
           float mt = -INFINITY;
 #pragma unroll 1
-          for (int q4 = c4; q4 < 4; ++q4) {
+          for (int q4 = c4; q4 < 2; ++q4) {
             float x[32];
             tmem_ld32f(srow + 32 * q4, x);
             tmem_wait_ld();
@@ -687,6 +673,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           lef = e_new == -INFINITY ? -INFINITY : fminf(mb - eb + BIAS, 100.f);
           ref = e_new == -INFINITY ? 0.f : ex2(-lef);
           if (any) {
+            // the page before may still be being added
+            ok = wait_for(o_done + 2 * g + ((j - 1) & 1), ((j - 1) >> 1) & 1, err, stop);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
 #pragma unroll 1
             for (int q4 = 0; q4 < 4; ++q4) {
               uint32_t y[32];
@@ -713,16 +703,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           tmem_wait_st();
         };
         int fresh = -1;  // columns at which the references were set
+        tmem_wait_ld();
         if (__any_sync(0xffffffffu, m == -INFINITY)) {
           renew(0);
           fresh = 0;
         }
-        float x[32];
-        tmem_ld32f(srow, x);
-        tmem_wait_ld();
 #pragma unroll 1
-        for (int c4 = 0; c4 < 4; ++c4) {
-          const float4 sc = c4 < 2 ? sc0 : sc1;
+        for (int c4 = 0; c4 < 2; ++c4) {
           const float mref = m == -INFINITY ? 0.f : m;
           uint32_t pk[16];
           float s0 = 0.f, s1 = 0.f;  // sums of the fp16 weights and of the softmax's
@@ -743,21 +730,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
             s1 = s0 * (ref * sc.w);
           } else {
             scores(x, c4, mref);
-            const bool tl = tail && (c4 >> 1) == np;
             const float ef = ex2(lef), w = ef * sc.y;
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               float y0 = ex2(x[i]), y1 = ex2(x[i + 1]);
               s1 += y0 + y1;
               // a scale that is NaN stays behind the mask
-              const int col = (32 * c4 + i) & 63;
-              y0 = x[i] == -INFINITY ? 0.f : y0 * (tl ? ef * tail_sc[64 + col] : w);
-              y1 = x[i + 1] == -INFINITY ? 0.f : y1 * (tl ? ef * tail_sc[64 + col + 1] : w);
+              const int col = 32 * c4 + i;
+              y0 = x[i] == -INFINITY ? 0.f : y0 * (tail ? ef * tail_sc[64 + col] : w);
+              y1 = x[i + 1] == -INFINITY ? 0.f : y1 * (tail ? ef * tail_sc[64 + col + 1] : w);
               s0 += y0 + y1;
               pk[i / 2] = pack_f16x2(y0, y1);
             }
           }
-          if (c4 < 3) tmem_ld32f(srow + 32 * (c4 + 1), x);  // the next columns, while these are checked and stored
+          if (c4 < 1) tmem_ld32f(srow + 32, x);  // the next columns, while these are checked and stored
           if (__any_sync(0xffffffffu, !(s0 <= W_LIMIT)) && fresh != c4) {  // also an infinity or NaN
             tmem_wait_ld();
             renew(c4);
@@ -773,17 +759,17 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           const uint32_t w[16] = {pk[0], pk[4], pk[1], pk[5], pk[2], pk[6], pk[3], pk[7],
                                   pk[8], pk[12], pk[9], pk[13], pk[10], pk[14], pk[11], pk[15]};
           tmem_st16(srow + 16 * c4, w);
-          if (c4 < 3) tmem_wait_ld();
+          if (c4 < 1) tmem_wait_ld();
         }
         tmem_wait_st();
         l += sum;
         any = true;
         ++n_str[g];
         tc_fence_before();
-        mbar_arrive(p_full + g);
+        mbar_arrive(p_full + sb);
       }
-      n_tile += nt;
-      if (any && ok) ok = wait_for(o_done + g, (n_str[g] - 1) & 1, err, stop);
+      n_page += nt;
+      if (any && ok) ok = wait_for(o_done + 2 * g + ((n_str[g] - 1) & 1), ((n_str[g] - 1) >> 1) & 1, err, stop);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
 
@@ -922,11 +908,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   // Products and copies that were not waited for (only after a wait that gave up)
   // end before TMEM and shared memory are given back.
   if (warp == W_MMA) {
-    if (lane == 0) {
-      umma_commit(&drain);
-      int never = 0;
-      wait_for(&drain, 0, c.err, &never);
-    }
+    umma_commit_warp(elect_leader(), &drain);
+    int never = 0;
+    wait_for(&drain, 0, c.err, &never);
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
@@ -951,7 +935,7 @@ hq_status launch(const Kv8AttnArgs& a, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return cuda_fail(e, "kv8 attention setup");
   // units are counted in 32 bits
   const double groups = static_cast<double>(a.G) * a.max_new / (NT * TR) + 1;
-  if (groups * a.c.B * a.c.Hkv * (a.c.cap / TK + TASK_UNITS) >= 4e9) return HQ_ERR_UNSUPPORTED;
+  if (groups * a.c.B * a.c.Hkv * (a.c.cap / KV8_BLOCK + TASK_UNITS) >= 4e9) return HQ_ERR_UNSUPPORTED;
   kv8_attn_tc_kernel<E, FMT, NT><<<sms, THREADS, L::BYTES, st>>>(a);
   return cuda_status(cudaGetLastError(), "kv8 attention launch");
 }
