@@ -6,18 +6,18 @@
 // at a time, one TMEM lane a row.  Keys go a page (64 positions) at a time:
 //   S = Q K^T    kind::f16, K the page's codes as fp16 (exact), 128 x 64
 //   P = 2^(S s_k - m) s_v 2^(m - E + 6) as fp16 (the page's scales in float32)
-//   O += P V     kind::f16, P from TMEM (where it takes the place of S), V the
-//                page's codes as fp16
+//   O += P V     kind::f16, P from TMEM, V the page's codes as fp16
 // with the two running references m, E of kv8_attn.cu: they are set to the exact
 // maxima only when 32 of a row's weights sum to more than 2^15, whereupon what the
 // row has so far (sum, O, the page's P) is rescaled.
 //
 // Warps of a CTA (one CTA an SM, persistent):
-//   0-7    softmax: two streams of 128 threads, a row each, with two pages of
-//          scores each, so that one page's products run while the other's weights
-//          are made.  NT = 2: the streams are two row tiles over the same pages;
-//          NT = 1 (up to 128 rows): the same rows, each stream taking every other
-//          page, joined at the end
+//   0-7    softmax: two streams of 128 threads, a row each.  A page's scores are
+//          given back once they are in registers, and its weights go to one of two
+//          places, so that the next page is scored and the last one added while a
+//          page's weights are made.  NT = 2: the streams are two row tiles over the
+//          same pages; NT = 1 (up to 128 rows): the same rows, each stream taking
+//          every other page, joined at the end
 //   8-11   converters: codes of a page -> fp16 in the 128-byte-swizzled operand
 //          layouts, K as [key][d], V as [d][key], both K-major, four stages of each.
 //          The page's V order gives a thread 4 keys of one d, which it stores as 8
@@ -50,8 +50,8 @@ constexpr int THREADS = 15 * 32;
 constexpr float BIAS = 6.0f;               // log2 of the fp16 weight at both references
 constexpr float W_LIMIT = 32768.0f;        // sum of 32 fp16 weights above which the references are set anew
 constexpr int TASK_UNITS = 8;              // what a task costs besides its pages, in pages
-constexpr uint32_t TMEM_COLS = 512;        // S of the streams 0 .. 255, O 256 .. 511
-constexpr uint32_t TM_S = 0, TM_O = 256;
+constexpr uint32_t TMEM_COLS = 512;        // each stream: S 64 columns, P 2 x 32, O 128
+constexpr uint32_t TM_S = 0, TM_P = 128, TM_O = 256;
 // fp16, K-major A and B, f32 accumulate
 constexpr uint32_t IDESC_QK = idesc_make(0, 0, 0, TR, KV8_BLOCK), IDESC_PV = idesc_make(0, 0, 0, TR, D);
 constexpr int HALF = HQ_KV8_V;             // bytes of a page's K (or V) codes
@@ -65,7 +65,8 @@ struct Lay {
   static constexpr int V = K + STAGES * 16384;   // stages: [d][64 keys]
   static constexpr int RAW = V + STAGES * 16384; // codes: slots of a page's K or V
   static constexpr int RK = NT == 2 ? 2 : 4;     // slots of K; as many of V
-  static constexpr int AUX = RAW + 2 * RK * HALF;  // 8 pages x (s_k, s_v, log2 s_v, 1 / s_v); the tail's 64 K and 64 V scales
+  static constexpr int RAWS = RAW + 2 * RK * HALF; // the two scales (16 bytes) of each K slot's page
+  static constexpr int AUX = RAWS + RK * 16;     // 8 pages x (s_k, s_v, log2 s_v, 1 / s_v); the tail's 64 K and 64 V scales
   static constexpr int BARS = AUX + 8 * 16 + 512;
   static constexpr int MISC = BARS + 48 * 8;     // TMEM base, flags, the plan's sums, walk and job
   static constexpr int JOIN = RAW;               // NT = 1: (m, E, l) of stream 1's rows, once the task's copies are done with
@@ -181,9 +182,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BARS);
-  // of the slots of codes, of the stages of operands, and [stream * 2 + page % 2]
+  // of the slots of codes, of the stages of operands, of the streams, and [stream * 2 + page % 2]
   uint64_t *rk_full = bars, *rk_empty = bars + 4, *rv_full = bars + 8, *rv_empty = bars + 12, *k_full = bars + 16, *k_empty = bars + 20,
-           *v_full = bars + 24, *v_empty = bars + 28, *s_full = bars + 32, *p_full = bars + 36, *o_done = bars + 40;
+           *v_full = bars + 24, *v_empty = bars + 28, *s_full = bars + 32, *s_free = bars + 34, *p_full = bars + 36, *o_done = bars + 40;
   uint64_t& drain = bars[44];
   uint32_t& tmem_sh = *reinterpret_cast<uint32_t*>(sm + L::MISC);
   int* flags = reinterpret_cast<int*>(sm + L::MISC + 4);                  // stop, last
@@ -274,8 +275,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       mbar_init(v_full + i, 128);
       mbar_init(v_empty + i, 1);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
+      mbar_init(s_free + i, 128);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(p_full + i, 128);
       mbar_init(o_done + i, 1);
     }
@@ -390,8 +394,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane == 0) {
-            mbar_arrive_expect_tx(slot_full + sl, HALF);
+            mbar_arrive_expect_tx(slot_full + sl, which ? HALF : HALF + 16);
             bulk_g2s(sm + L::RAW + (which * RK + sl) * HALF, page + which * HQ_KV8_V, HALF, slot_full + sl);
+            if (!which) bulk_g2s(sm + L::RAWS + sl * 16, page + HQ_KV8_KSCALE, 16, slot_full + sl);
           }
         }
       }
@@ -399,28 +404,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       // -------------------------------------------------------- converters
       const int ct = threadIdx.x - W_CONV * 32, cw = ct >> 5;  // thread of 128, warp of 4
       const int g = lane >> 2, t4 = lane & 3;
-      // K and V scale of page t (threads 0 and 1): fetched two pages ahead
-      auto scale_of = [&](int t) {
-        if (t >= full || ct >= 2) return 1.0f;
-        return *reinterpret_cast<const float*>(kv8_page(c, bh, page0 + t) + (ct ? HQ_KV8_VSCALE : HQ_KV8_KSCALE));
-      };
-      float scale = scale_of(0), scale_next = scale_of(1);
       // K of page t: free once the page four before has been scored
       auto convert_k = [&](int t) {
         const int T = n_page + t, st = T % STAGES;
         if (T >= STAGES) ok = wait_for(k_empty + st, (T / STAGES - 1) & 1, err, stop);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
-        if (ct < 2) {
-          float* x = aux + (T & 7) * 4;
-          x[ct] = scale;
-          if (ct) {
-            x[2] = log2f(scale);
-            x[3] = 1.0f / scale;
-          }
-        }
-        scale = scale_next;
-        scale_next = scale_of(t + 2);
         const uint32_t dst = base + L::K + st * 16384;
         uint32_t y[8] = {};
         auto put = [&](int e) {  // 512-byte piece of codes: 8 keys x 64 d
@@ -437,6 +426,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           uint4 x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[i] = src[(cw * 4 + i) * 32 + lane];
+          if (ct == 0) {
+            const float2 sc = *reinterpret_cast<const float2*>(sm + L::RAWS + sl * 16);
+            *reinterpret_cast<float4*>(aux + (T & 7) * 4) = make_float4(sc.x, sc.y, log2f(sc.y), 1.0f / sc.y);
+          }
           mbar_arrive(rk_empty + sl);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -454,6 +447,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
             *reinterpret_cast<uint4*>(y + 4) = src[((cw * 4 + i) * 32 + lane) * 2 + 1];
             put(cw * 4 + i);
           }
+          if (ct == 0) *reinterpret_cast<float4*>(aux + (T & 7) * 4) = make_float4(1.f, 1.f, 0.f, 1.f);
           // the rows' scales; past the length 1: nothing there is seen
           const int which = ct >> 6, r = ct & 63;
           tail_sc[ct] = (page0 + t) * KV8_BLOCK + r < job.len
@@ -520,26 +514,26 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       if (ok) {
         const uint32_t leader = elect_leader();
         auto ready = [](uint64_t* bar, int parity) { return __any_sync(0xffffffffu, mbar_test_wait(bar, parity)); };
-        auto issue_qk = [&](int g, int j, int st) {
+        auto issue_qk = [&](int g, int st) {
           tc_fence_after();
           const uint32_t Qs = base + L::Q + (NT == 2 ? g * 32768 : 0), Ks = base + L::K + st * 16384;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_f16_warp(leader, tmem + TM_S + 128 * g + 64 * (j & 1), sdesc_sw128(Qs + (kk >> 2) * 16384 + 32 * (kk & 3), 16, 1024),
+            umma_f16_warp(leader, tmem + TM_S + 64 * g, sdesc_sw128(Qs + (kk >> 2) * 16384 + 32 * (kk & 3), 16, 1024),
                      sdesc_sw128(Ks + (kk >> 2) * 8192 + 32 * (kk & 3), 16, 1024), IDESC_QK, kk > 0);
-          umma_commit_warp(leader, s_full + 2 * g + (j & 1));
+          umma_commit_warp(leader, s_full + g);
         };
         auto issue_pv = [&](int g, int j, int st, bool first) {
           tc_fence_after();
           const uint32_t Vs = base + L::V + st * 16384;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_f16_ta_warp(leader, tmem + TM_O + 128 * g, tmem + TM_S + 128 * g + 64 * (j & 1) + 8 * kk, sdesc_sw128(Vs + 32 * kk, 16, 1024),
-                        IDESC_PV, !first || kk > 0 ? 1u : 0u);
+            umma_f16_ta_warp(leader, tmem + TM_O + 128 * g, tmem + TM_P + 64 * g + 32 * (j & 1) + 8 * kk,
+                             sdesc_sw128(Vs + 32 * kk, 16, 1024), IDESC_PV, !first || kk > 0 ? 1u : 0u);
           umma_commit_warp(leader, o_done + 2 * g + (j & 1));
         };
-        // A stream's j-th page goes QK, weights, PV; its scores take the place of the
-        // (j - 2)-th page's weights.  Whichever stream is ready goes next.  A page's
+        // A stream's page goes QK, weights, PV; the next one is scored as soon as its
+        // scores have been read.  Whichever stream is ready goes next.  A page's
         // operand is released when every stream that takes it has been issued.
         int tq[2], tp[2], jq[2], jp[2];  // next page of each stream to score / to add, and its number in the stream
         for (int g = 0; g < 2; ++g) {
@@ -565,9 +559,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
             }
             {
               const int t = tq[g], j = jq[g], T = n_page + t, st = T % STAGES;
-              if (t < nt && j - jp[g] < 2 && (t < 2 * step || ready(o_done + 2 * g + (j & 1), ((j >> 1) - 1) & 1)) &&
-                  ready(k_full + st, (T / STAGES) & 1)) {
-                issue_qk(g, j, st);
+              if (t < nt && (j == 0 || ready(s_free + g, (j - 1) & 1)) && ready(k_full + st, (T / STAGES) & 1)) {
+                issue_qk(g, st);
                 if (NT == 1 || tq[g ^ 1] > t) umma_commit_warp(leader, k_empty + st);
                 tq[g] = t + step;
                 ++jq[g];
@@ -607,18 +600,21 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       float m = real ? -INFINITY : 0.f, e = real ? -INFINITY : 0.f, l = 0.f;
       float lef = real ? -INFINITY : 0.f, ref = real ? 0.f : 1.f;  // log2 of 2^(m - E + BIAS), and its inverse
       const bool idle = !__any_sync(0xffffffffu, real);
-      bool any = false;  // a page was taken
+      int taken = 0;  // pages of the task
       for (int t = 0; t < nt; ++t) {
         if (!takes(g, t)) continue;
         const int j = n_str[g], sb = 2 * g + (j & 1);
-        const uint32_t srow = trow + TM_S + 128 * g + 64 * (j & 1);
-        ok = ok && wait_for(s_full + sb, (j >> 1) & 1, err, stop);
+        const uint32_t srow = trow + TM_S + 64 * g, prow = trow + TM_P + 64 * g + 32 * (j & 1);
+        ok = ok && wait_for(s_full + g, j & 1, err, stop);
+        // the weights' place: free once the page two before has been added
+        if (taken >= 2) ok = ok && wait_for(o_done + sb, ((j >> 1) - 1) & 1, err, stop);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
+        ++n_str[g];
+        ++taken;
         if (idle) {
-          any = true;
-          ++n_str[g];
+          mbar_arrive(s_free + g);
           mbar_arrive(p_full + sb);
           continue;
         }
@@ -647,20 +643,28 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
         // The references anew at columns 32 c4: the exact maximum of the columns
         // from there on; sums, O and the page's weights so far are rescaled.
         float sum = 0.f;
+        float off = 0.f;  // what the scores in x are less
         auto renew = [&](int c4) {
           float vtop = tail ? 0.f : fmaxf(sc.y, 0.f);  // ignores NaN
           if (tail)
             for (int i = 0; i < 64; ++i) vtop = fmaxf(vtop, tail_sc[64 + i]);
           if (!(vtop > 0.f)) vtop = 1.f;
           float mt = -INFINITY;
+          if (c4 == 0) {
 #pragma unroll 1
-          for (int q4 = c4; q4 < 2; ++q4) {
-            float x[32];
-            tmem_ld32f(srow + 32 * q4, x);
-            tmem_wait_ld();
-            scores(x, q4, 0.f);
+            for (int q4 = 0; q4 < 2; ++q4) {
+              float y[32];
+              tmem_ld32f(srow + 32 * q4, y);
+              tmem_wait_ld();
+              scores(y, q4, 0.f);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) mt = fmaxf(mt, y[i]);
+            }
+          } else {
+            // the second half's scores are in registers, less `off`: their place may be taken
 #pragma unroll
             for (int i = 0; i < 32; ++i) mt = fmaxf(mt, x[i]);
+            mt += off;
           }
           const float m_new = fmaxf(m, mt), e_new = fmaxf(e, mt + log2f(vtop));
           const float mb = m_new == -INFINITY ? 0.f : m_new, eb = e_new == -INFINITY ? 0.f : e_new;
@@ -672,7 +676,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           // bounded, so that a weight that underflowed stays 0 beside a far larger earlier score
           lef = e_new == -INFINITY ? -INFINITY : fminf(mb - eb + BIAS, 100.f);
           ref = e_new == -INFINITY ? 0.f : ex2(-lef);
-          if (any) {
+          if (taken > 1) {
             // the page before may still be being added
             ok = wait_for(o_done + 2 * g + ((j - 1) & 1), ((j - 1) >> 1) & 1, err, stop);
             ok = __all_sync(0xffffffffu, ok);
@@ -688,20 +692,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
             }
           }
           tmem_wait_st();
-#pragma unroll 1
-          for (int q4 = 0; q4 < c4; ++q4) {
+          if (c4 == 1) {
             uint32_t y[16];
-            tmem_ld16(srow + 16 * q4, y);
+            tmem_ld16(prow, y);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
               y[i] = pack_f16x2(w.x * ao, w.y * ao);
             }
-            tmem_st16(srow + 16 * q4, y);
+            tmem_st16(prow, y);
+            tmem_wait_st();
           }
-          tmem_wait_st();
         };
+        bool scored = false;  // x holds scores (in exponents of 2), not products
         int fresh = -1;  // columns at which the references were set
         tmem_wait_ld();
         if (__any_sync(0xffffffffu, m == -INFINITY)) {
@@ -710,66 +714,78 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
         }
 #pragma unroll 1
         for (int c4 = 0; c4 < 2; ++c4) {
-          const float mref = m == -INFINITY ? 0.f : m;
           uint32_t pk[16];
-          float s0 = 0.f, s1 = 0.f;  // sums of the fp16 weights and of the softmax's
-          // Weights of a page that is seen whole take the value scale into the
-          // exponent, and their sum is divided by it: a product less per weight.
-          // Not where it is so small that weights would underflow.
-          const float lw = lef + sc.z;
-          if (__all_sync(0xffffffffu, seen && lw > -60.f)) {
-            scores(x, c4, mref - lw);
+          float s0, s1;  // sums of the fp16 weights and of the softmax's
+          while (true) {
+            const float mref = m == -INFINITY ? 0.f : m;
+            s0 = s1 = 0.f;
+            // Weights of a page that is seen whole take the value scale into the
+            // exponent, and their sum is divided by it: a product less per weight.
+            // Not where it is so small that weights would underflow.
+            const float lw = lef + sc.z;
+            const bool plain = __all_sync(0xffffffffu, seen && lw > -60.f);
+            off = plain ? mref - lw : mref;
+            if (scored) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float y0 = ex2(x[i]), y1 = ex2(x[i + 1]);
-              s0 += y0;
-              s1 += y1;
-              pk[i / 2] = pack_f16x2(y0, y1);
+              for (int i = 0; i < 32; ++i) x[i] -= off;
+            } else {
+              scores(x, c4, off);
             }
-            s0 += s1;
-            s1 = s0 * (ref * sc.w);
-          } else {
-            scores(x, c4, mref);
-            const float ef = ex2(lef), w = ef * sc.y;
+            if (plain) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float y0 = ex2(x[i]), y1 = ex2(x[i + 1]);
-              s1 += y0 + y1;
-              // a scale that is NaN stays behind the mask
-              const int col = 32 * c4 + i;
-              y0 = x[i] == -INFINITY ? 0.f : y0 * (tail ? ef * tail_sc[64 + col] : w);
-              y1 = x[i + 1] == -INFINITY ? 0.f : y1 * (tail ? ef * tail_sc[64 + col + 1] : w);
-              s0 += y0 + y1;
-              pk[i / 2] = pack_f16x2(y0, y1);
+              for (int i = 0; i < 32; i += 2) {
+                const float y0 = ex2(x[i]), y1 = ex2(x[i + 1]);
+                s0 += y0;
+                s1 += y1;
+                pk[i / 2] = pack_f16x2(y0, y1);
+              }
+              s0 += s1;
+              s1 = s0 * (ref * sc.w);
+            } else {
+              const float ef = ex2(lef), w = ef * sc.y;
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                float y0 = ex2(x[i]), y1 = ex2(x[i + 1]);
+                s1 += y0 + y1;
+                // a scale that is NaN stays behind the mask
+                const int col = 32 * c4 + i;
+                y0 = x[i] == -INFINITY ? 0.f : y0 * (tail ? ef * tail_sc[64 + col] : w);
+                y1 = x[i + 1] == -INFINITY ? 0.f : y1 * (tail ? ef * tail_sc[64 + col + 1] : w);
+                s0 += y0 + y1;
+                pk[i / 2] = pack_f16x2(y0, y1);
+              }
             }
-          }
-          if (c4 < 1) tmem_ld32f(srow + 32, x);  // the next columns, while these are checked and stored
-          if (__any_sync(0xffffffffu, !(s0 <= W_LIMIT)) && fresh != c4) {  // also an infinity or NaN
-            tmem_wait_ld();
+            if (!__any_sync(0xffffffffu, !(s0 <= W_LIMIT)) || fresh == c4) break;  // also an infinity or NaN
             renew(c4);
             fresh = c4;
-            tmem_ld32f(srow + 32 * c4, x);
-            tmem_wait_ld();
-            --c4;
-            continue;
+            if (c4 == 0) {
+              tmem_ld32f(srow, x);
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] += off;  // the scores themselves: -inf stays
+              scored = true;
+            }
           }
+          if (c4 == 0) tmem_ld32f(srow + 32, x);  // the other half, while these weights are stored
           sum += s1;
-          // P's columns 16 c4 .. take the place of scores that have been read: pairs of
-          // keys, those of 16 in V's order 0 1 8 9, 2 3 10 11, 4 5 12 13, 6 7 14 15
+          // P's columns: pairs of keys, those of 16 in V's order 0 1 8 9, 2 3 10 11, 4 5 12 13, 6 7 14 15
           const uint32_t w[16] = {pk[0], pk[4], pk[1], pk[5], pk[2], pk[6], pk[3], pk[7],
                                   pk[8], pk[12], pk[9], pk[13], pk[10], pk[14], pk[11], pk[15]};
-          tmem_st16(srow + 16 * c4, w);
-          if (c4 < 1) tmem_wait_ld();
+          tmem_st16(prow + 16 * c4, w);
+          if (c4 == 0) {
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive(s_free + g);  // all scores are in registers
+          }
         }
         tmem_wait_st();
         l += sum;
-        any = true;
-        ++n_str[g];
         tc_fence_before();
         mbar_arrive(p_full + sb);
       }
       n_page += nt;
-      if (any && ok) ok = wait_for(o_done + 2 * g + ((n_str[g] - 1) & 1), ((n_str[g] - 1) >> 1) & 1, err, stop);
+      if (taken > 0 && ok) ok = wait_for(o_done + 2 * g + ((n_str[g] - 1) & 1), ((n_str[g] - 1) >> 1) & 1, err, stop);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
 
@@ -786,10 +802,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
         asm volatile("bar.sync 2, 256;" ::: "memory");
         if (g == 1) {
           joined[r] = m;
-          joined[TR + r] = any ? e : -INFINITY;
+          joined[TR + r] = taken > 0 ? e : -INFINITY;
           joined[2 * TR + r] = l;
         }
-        if (g == 1 && ok && any) {
+        if (g == 1 && ok && taken > 0) {
 #pragma unroll 1
           for (int c4 = 0; c4 < 4; ++c4) {
             float x[32];
