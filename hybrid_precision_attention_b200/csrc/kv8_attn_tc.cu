@@ -24,7 +24,8 @@
 //          bytes: the keys of 16 stand as t, t+1, t+8, t+9 for t = 0, 2, 4, 6, and
 //          P's columns follow the same order
 //   12, 13 copies of the pages' codes, K and V (bulk copies, no multicast)
-//   14     TMEM allocation, tcgen05.mma issue (event-driven, one thread)
+//   14, 15 tcgen05.mma issue, one warp a stream (one for both is the bottleneck: a wait
+//          that is met costs it 100 cycles); TMEM allocation
 // Bound: two row tiles and 128 keys take 2048 cycles of products, 2048 of
 // exponentials and, at 128 bytes a cycle, 3000 of shared memory (256 KB of
 // operands, 64 KB converted, 64 KB of codes in and out).
@@ -45,8 +46,8 @@ namespace {
 
 constexpr int TR = 128;                    // rows of a tile
 constexpr int STAGES = 4;                  // pages of K, and of V, as operands
-constexpr int W_CONV = 8, W_COPY = 12, W_MMA = 14;  // W_COPY: K, W_COPY + 1: V
-constexpr int THREADS = 15 * 32;
+constexpr int W_CONV = 8, W_COPY = 12, W_MMA = 14;  // W_COPY: K, W_COPY + 1: V; W_MMA + stream
+constexpr int THREADS = 16 * 32;
 constexpr float BIAS = 6.0f;               // log2 of the fp16 weight at both references
 constexpr float W_LIMIT = 32768.0f;        // sum of 32 fp16 weights above which the references are set anew
 constexpr int TASK_UNITS = 8;              // what a task costs besides its pages, in pages
@@ -68,7 +69,7 @@ struct Lay {
   static constexpr int RAWS = RAW + 2 * RK * HALF; // the two scales (16 bytes) of each K slot's page
   static constexpr int AUX = RAWS + RK * 16;     // 8 pages x (s_k, s_v, log2 s_v, 1 / s_v); the tail's 64 K and 64 V scales
   static constexpr int BARS = AUX + 8 * 16 + 512;
-  static constexpr int MISC = BARS + 48 * 8;     // TMEM base, flags, the plan's sums, walk and job
+  static constexpr int MISC = BARS + 48 * 8;     // TMEM base, flags, the plan's sums (16 warps), walk and job
   static constexpr int JOIN = RAW;               // NT = 1: (m, E, l) of stream 1's rows, once the task's copies are done with
   static constexpr int BYTES = MISC + 80 + 144 + 1024;  // with the alignment
 };
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   // of the slots of codes, of the stages of operands, of the streams, and [stream * 2 + page % 2]
   uint64_t *rk_full = bars, *rk_empty = bars + 4, *rv_full = bars + 8, *rv_empty = bars + 12, *k_full = bars + 16, *k_empty = bars + 20,
            *v_full = bars + 24, *v_empty = bars + 28, *s_full = bars + 32, *s_free = bars + 34, *p_full = bars + 36, *o_done = bars + 40;
-  uint64_t& drain = bars[44];
+  uint64_t* drain = bars + 44;
   uint32_t& tmem_sh = *reinterpret_cast<uint32_t*>(sm + L::MISC);
   int* flags = reinterpret_cast<int*>(sm + L::MISC + 4);                  // stop, last
   uint32_t* sums = reinterpret_cast<uint32_t*>(sm + L::MISC + 16);        // [warps]
@@ -271,19 +272,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
     }
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(k_full + i, 128);
-      mbar_init(k_empty + i, 1);
+      mbar_init(k_empty + i, NT);
       mbar_init(v_full + i, 128);
-      mbar_init(v_empty + i, 1);
+      mbar_init(v_empty + i, NT);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(s_free + i, 128);
+      mbar_init(drain + i, 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(p_full + i, 128);
       mbar_init(o_done + i, 1);
     }
-    mbar_init(&drain, 1);
     flags[0] = 0;
     fence_mbar_init();
   }
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   // running uses of each barrier, kept by the roles that wait on it
   int n_raw = 0;                  // copied pages (copy warps), those before the task's (converters)
   int n_page = 0;                 // pages before the task's (converters, MMA, the softmax's scales)
-  int n_str[2] = {0, 0};          // pages of each stream (softmax, MMA)
+  int n_mine = 0;                 // pages of the stream (softmax, MMA)
   bool ok = true;
   auto takes = [&](int g, int t) { return NT == 2 || (t & 1) == g; };
 
@@ -508,83 +509,47 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       }
       n_raw += full;
       n_page += nt;
-    } else if (warp == W_MMA) {
+    } else if (warp >= W_MMA) {
       // -------------------------------------------------------- MMA issue
       // the whole warp, in uniform control flow; its leader issues
-      if (ok) {
-        const uint32_t leader = elect_leader();
-        auto ready = [](uint64_t* bar, int parity) { return __any_sync(0xffffffffu, mbar_test_wait(bar, parity)); };
-        auto issue_qk = [&](int g, int st) {
-          tc_fence_after();
-          const uint32_t Qs = base + L::Q + (NT == 2 ? g * 32768 : 0), Ks = base + L::K + st * 16384;
+      const int g = warp - W_MMA;
+      const uint32_t leader = elect_leader();
+      auto await = [&](uint64_t* bar, int parity) {
+        if (__any_sync(0xffffffffu, mbar_try_wait(bar, parity & 1))) return true;
+        ok = wait_for(bar, parity & 1, err, stop);
+        ok = __all_sync(0xffffffffu, ok);
+        return ok;
+      };
+      // A stream's next page is scored as soon as the last one's scores have been read,
+      // a page's values are added when its weights are there.  A page's operand is
+      // free when every stream that takes it is done with it.
+      auto score = [&](int t, int j) {
+        const int T = n_page + t, st = T % STAGES;
+        if ((j > 0 && !await(s_free + g, j - 1)) || !await(k_full + st, T / STAGES)) return;
+        tc_fence_after();
+        const uint32_t Qs = base + L::Q + (NT == 2 ? g * 32768 : 0), Ks = base + L::K + st * 16384;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_f16_warp(leader, tmem + TM_S + 64 * g, sdesc_sw128(Qs + (kk >> 2) * 16384 + 32 * (kk & 3), 16, 1024),
-                     sdesc_sw128(Ks + (kk >> 2) * 8192 + 32 * (kk & 3), 16, 1024), IDESC_QK, kk > 0);
-          umma_commit_warp(leader, s_full + g);
-        };
-        auto issue_pv = [&](int g, int j, int st, bool first) {
-          tc_fence_after();
-          const uint32_t Vs = base + L::V + st * 16384;
+        for (int kk = 0; kk < 8; ++kk)
+          umma_f16_warp(leader, tmem + TM_S + 64 * g, sdesc_sw128(Qs + (kk >> 2) * 16384 + 32 * (kk & 3), 16, 1024),
+                        sdesc_sw128(Ks + (kk >> 2) * 8192 + 32 * (kk & 3), 16, 1024), IDESC_QK, kk > 0);
+        umma_commit_warp(leader, s_full + g);
+        umma_commit_warp(leader, k_empty + st);
+      };
+      constexpr int STEP = NT == 2 ? 1 : 2;
+      const int t0 = NT == 2 ? 0 : g;
+      if (ok && t0 < nt) score(t0, n_mine);
+      for (int t = t0; ok && t < nt; t += STEP, ++n_mine) {
+        const int T = n_page + t, st = T % STAGES, j = n_mine;
+        if (t + STEP < nt) score(t + STEP, j + 1);
+        if (!ok || !await(p_full + 2 * g + (j & 1), j >> 1) || !await(v_full + st, T / STAGES)) break;
+        tc_fence_after();
+        const uint32_t Vs = base + L::V + st * 16384;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_f16_ta_warp(leader, tmem + TM_O + 128 * g, tmem + TM_P + 64 * g + 32 * (j & 1) + 8 * kk,
-                             sdesc_sw128(Vs + 32 * kk, 16, 1024), IDESC_PV, !first || kk > 0 ? 1u : 0u);
-          umma_commit_warp(leader, o_done + 2 * g + (j & 1));
-        };
-        // A stream's page goes QK, weights, PV; the next one is scored as soon as its
-        // scores have been read.  Whichever stream is ready goes next.  A page's
-        // operand is released when every stream that takes it has been issued.
-        int tq[2], tp[2], jq[2], jp[2];  // next page of each stream to score / to add, and its number in the stream
-        for (int g = 0; g < 2; ++g) {
-          tq[g] = tp[g] = NT == 2 ? 0 : g;
-          jq[g] = jp[g] = n_str[g];
-        }
-        const int step = NT == 2 ? 1 : 2;
-        uint64_t t_last = 0;
-        uint32_t idle = 0;
-        while (tp[0] < nt || tp[1] < nt) {
-          bool progress = false;
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            {
-              const int t = tp[g], j = jp[g], T = n_page + t, st = T % STAGES;
-              if (t < tq[g] && ready(p_full + 2 * g + (j & 1), (j >> 1) & 1) && ready(v_full + st, (T / STAGES) & 1)) {
-                issue_pv(g, j, st, t < step);
-                if (NT == 1 || tp[g ^ 1] > t) umma_commit_warp(leader, v_empty + st);
-                tp[g] = t + step;
-                ++jp[g];
-                progress = true;
-              }
-            }
-            {
-              const int t = tq[g], j = jq[g], T = n_page + t, st = T % STAGES;
-              if (t < nt && (j == 0 || ready(s_free + g, (j - 1) & 1)) && ready(k_full + st, (T / STAGES) & 1)) {
-                issue_qk(g, st);
-                if (NT == 1 || tq[g ^ 1] > t) umma_commit_warp(leader, k_empty + st);
-                tq[g] = t + step;
-                ++jq[g];
-                progress = true;
-              }
-            }
-          }
-          if (progress) {
-            idle = 0;
-          } else if (++idle < 1024) {
-          } else if (__any_sync(0xffffffffu, *stop)) {
-            ok = false;
-            break;
-          } else if (idle == 1024) {
-            t_last = global_ns();  // the clock is read only once nothing has been ready for a while
-          } else if (__any_sync(0xffffffffu, global_ns() - t_last > 1000000000ull)) {
-            if (lane == 0) atomicOr(reinterpret_cast<unsigned int*>(err), HQ_DEVERR_TIMEOUT);
-            *stop = 1;
-            ok = false;
-            break;
-          }
-        }
-        n_str[0] = jq[0];
-        n_str[1] = jq[1];
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f16_ta_warp(leader, tmem + TM_O + 128 * g, tmem + TM_P + 64 * g + 32 * (j & 1) + 8 * kk, sdesc_sw128(Vs + 32 * kk, 16, 1024),
+                           IDESC_PV, t > t0 || kk > 0 ? 1u : 0u);
+        umma_commit_warp(leader, o_done + 2 * g + (j & 1));
+        umma_commit_warp(leader, v_empty + st);
       }
       n_page += nt;
     } else {
@@ -603,7 +568,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       int taken = 0;  // pages of the task
       for (int t = 0; t < nt; ++t) {
         if (!takes(g, t)) continue;
-        const int j = n_str[g], sb = 2 * g + (j & 1);
+        const int j = n_mine, sb = 2 * g + (j & 1);
         const uint32_t srow = trow + TM_S + 64 * g, prow = trow + TM_P + 64 * g + 32 * (j & 1);
         ok = ok && wait_for(s_full + g, j & 1, err, stop);
         // the weights' place: free once the page two before has been added
@@ -611,7 +576,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        ++n_str[g];
+        ++n_mine;
         ++taken;
         if (idle) {
           mbar_arrive(s_free + g);
@@ -785,7 +750,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
         mbar_arrive(p_full + sb);
       }
       n_page += nt;
-      if (taken > 0 && ok) ok = wait_for(o_done + 2 * g + ((n_str[g] - 1) & 1), ((n_str[g] - 1) >> 1) & 1, err, stop);
+      if (taken > 0 && ok) ok = wait_for(o_done + 2 * g + ((n_mine - 1) & 1), ((n_mine - 1) >> 1) & 1, err, stop);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
 
@@ -923,11 +888,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
 
   // Products and copies that were not waited for (only after a wait that gave up)
   // end before TMEM and shared memory are given back.
-  if (warp == W_MMA) {
-    umma_commit_warp(elect_leader(), &drain);
+  if (warp >= W_MMA) {
+    umma_commit_warp(elect_leader(), drain + (warp - W_MMA));
     int never = 0;
-    wait_for(&drain, 0, c.err, &never);
-    __syncwarp();
+    wait_for(drain + (warp - W_MMA), 0, c.err, &never);
+  }
+  __syncthreads();
+  if (warp == W_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
   }
