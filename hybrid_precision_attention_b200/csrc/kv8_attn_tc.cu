@@ -6,18 +6,18 @@
 // at a time, one TMEM lane a row.  Keys go a page (64 positions) at a time:
 //   S = Q K^T    kind::f16, K the page's codes as fp16 (exact), 128 x 64
 //   P = 2^(S s_k - m) s_v 2^(m - E + 6) as fp16 (the page's scales in float32)
-//   O += P V     kind::f16, P from TMEM, V the page's codes as fp16
+//   O += P V     kind::f16, P from TMEM (where it takes the place of S), V the
+//                page's codes as fp16
 // with the two running references m, E of kv8_attn.cu: they are set to the exact
-// maxima only when 32 of a row's weights sum to more than 2^15, whereupon what the
-// row has so far (sum, O, the page's P) is rescaled.
+// maxima only when a page's weights of a row sum to more than 2^15, whereupon what
+// the row has so far (sum, O) is rescaled.
 //
 // Warps of a CTA (one CTA an SM, persistent):
-//   0-7    softmax: two streams of 128 threads, a row each.  A page's scores are
-//          given back once they are in registers, and its weights go to one of two
-//          places, so that the next page is scored and the last one added while a
-//          page's weights are made.  NT = 2: the streams are two row tiles over the
-//          same pages; NT = 1 (up to 128 rows): the same rows, each stream taking
-//          every other page, joined at the end
+//   0-7    softmax: two streams of 128 threads, a row each, with two pages of
+//          scores each: one is scored and added while the other's weights are made.
+//          NT = 2: the streams are two row tiles over the same pages; NT = 1 (up to
+//          128 rows): the same rows, each stream taking every other page, joined at
+//          the end
 //   8-11   converters: codes of a page -> fp16 in the 128-byte-swizzled operand
 //          layouts, K as [key][d], V as [d][key], both K-major, four stages of each.
 //          The page's V order gives a thread 4 keys of one d, which it stores as 8
@@ -49,10 +49,10 @@ constexpr int STAGES = 4;                  // pages of K, and of V, as operands
 constexpr int W_CONV = 8, W_COPY = 12, W_MMA = 14;  // W_COPY: K, W_COPY + 1: V; W_MMA + stream
 constexpr int THREADS = 16 * 32;
 constexpr float BIAS = 6.0f;               // log2 of the fp16 weight at both references
-constexpr float W_LIMIT = 32768.0f;        // sum of 32 fp16 weights above which the references are set anew
+constexpr float W_LIMIT = 32768.0f;        // sum of a page's fp16 weights above which the references are set anew
 constexpr int TASK_UNITS = 8;              // what a task costs besides its pages, in pages
-constexpr uint32_t TMEM_COLS = 512;        // each stream: S 64 columns, P 2 x 32, O 128
-constexpr uint32_t TM_S = 0, TM_P = 128, TM_O = 256;
+constexpr uint32_t TMEM_COLS = 512;        // each stream: S 2 x 64 columns (P in the first 32 of each), O 128
+constexpr uint32_t TM_S = 0, TM_O = 256;
 // fp16, K-major A and B, f32 accumulate
 constexpr uint32_t IDESC_QK = idesc_make(0, 0, 0, TR, KV8_BLOCK), IDESC_PV = idesc_make(0, 0, 0, TR, D);
 constexpr int HALF = HQ_KV8_V;             // bytes of a page's K (or V) codes
@@ -183,9 +183,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BARS);
-  // of the slots of codes, of the stages of operands, of the streams, and [stream * 2 + page % 2]
+  // of the slots of codes, of the stages of operands, and [stream * 2 + page % 2]
   uint64_t *rk_full = bars, *rk_empty = bars + 4, *rv_full = bars + 8, *rv_empty = bars + 12, *k_full = bars + 16, *k_empty = bars + 20,
-           *v_full = bars + 24, *v_empty = bars + 28, *s_full = bars + 32, *s_free = bars + 34, *p_full = bars + 36, *o_done = bars + 40;
+           *v_full = bars + 24, *v_empty = bars + 28, *s_full = bars + 32, *p_full = bars + 36, *o_done = bars + 40;
   uint64_t* drain = bars + 44;
   uint32_t& tmem_sh = *reinterpret_cast<uint32_t*>(sm + L::MISC);
   int* flags = reinterpret_cast<int*>(sm + L::MISC + 4);                  // stop, last
@@ -276,12 +276,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       mbar_init(v_full + i, 128);
       mbar_init(v_empty + i, NT);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full + i, 1);
-      mbar_init(s_free + i, 128);
-      mbar_init(drain + i, 1);
-    }
+    for (int i = 0; i < 2; ++i) mbar_init(drain + i, 1);
     for (int i = 0; i < 4; ++i) {
+      mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 128);
       mbar_init(o_done + i, 1);
     }
@@ -520,36 +517,36 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
         ok = __all_sync(0xffffffffu, ok);
         return ok;
       };
-      // A stream's next page is scored as soon as the last one's scores have been read,
-      // a page's values are added when its weights are there.  A page's operand is
-      // free when every stream that takes it is done with it.
-      auto score = [&](int t, int j) {
-        const int T = n_page + t, st = T % STAGES;
-        if ((j > 0 && !await(s_free + g, j - 1)) || !await(k_full + st, T / STAGES)) return;
+      // A stream's page j takes the place of page j - 2, once that has been added.  A
+      // page's operand is free when every stream that takes it is done with it.
+      auto score = [&](int t, int j, bool again) {
+        const int T = n_page + t, st = T % STAGES, sb = 2 * g + (j & 1);
+        if ((again && !await(o_done + sb, (j >> 1) - 1)) || !await(k_full + st, T / STAGES)) return;
         tc_fence_after();
         const uint32_t Qs = base + L::Q + (NT == 2 ? g * 32768 : 0), Ks = base + L::K + st * 16384;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          umma_f16_warp(leader, tmem + TM_S + 64 * g, sdesc_sw128(Qs + (kk >> 2) * 16384 + 32 * (kk & 3), 16, 1024),
+          umma_f16_warp(leader, tmem + TM_S + 64 * sb, sdesc_sw128(Qs + (kk >> 2) * 16384 + 32 * (kk & 3), 16, 1024),
                         sdesc_sw128(Ks + (kk >> 2) * 8192 + 32 * (kk & 3), 16, 1024), IDESC_QK, kk > 0);
-        umma_commit_warp(leader, s_full + g);
+        umma_commit_warp(leader, s_full + sb);
         umma_commit_warp(leader, k_empty + st);
       };
       constexpr int STEP = NT == 2 ? 1 : 2;
       const int t0 = NT == 2 ? 0 : g;
-      if (ok && t0 < nt) score(t0, n_mine);
+      if (ok && t0 < nt) score(t0, n_mine, false);
+      if (ok && t0 + STEP < nt) score(t0 + STEP, n_mine + 1, false);
       for (int t = t0; ok && t < nt; t += STEP, ++n_mine) {
-        const int T = n_page + t, st = T % STAGES, j = n_mine;
-        if (t + STEP < nt) score(t + STEP, j + 1);
-        if (!ok || !await(p_full + 2 * g + (j & 1), j >> 1) || !await(v_full + st, T / STAGES)) break;
+        const int T = n_page + t, st = T % STAGES, j = n_mine, sb = 2 * g + (j & 1);
+        if (!await(p_full + sb, j >> 1) || !await(v_full + st, T / STAGES)) break;
         tc_fence_after();
         const uint32_t Vs = base + L::V + st * 16384;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_f16_ta_warp(leader, tmem + TM_O + 128 * g, tmem + TM_P + 64 * g + 32 * (j & 1) + 8 * kk, sdesc_sw128(Vs + 32 * kk, 16, 1024),
+          umma_f16_ta_warp(leader, tmem + TM_O + 128 * g, tmem + TM_S + 64 * sb + 8 * kk, sdesc_sw128(Vs + 32 * kk, 16, 1024),
                            IDESC_PV, t > t0 || kk > 0 ? 1u : 0u);
-        umma_commit_warp(leader, o_done + 2 * g + (j & 1));
+        umma_commit_warp(leader, o_done + sb);
         umma_commit_warp(leader, v_empty + st);
+        if (t + 2 * STEP < nt) score(t + 2 * STEP, j + 2, true);
       }
       n_page += nt;
     } else {
@@ -569,73 +566,58 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       for (int t = 0; t < nt; ++t) {
         if (!takes(g, t)) continue;
         const int j = n_mine, sb = 2 * g + (j & 1);
-        const uint32_t srow = trow + TM_S + 64 * g, prow = trow + TM_P + 64 * g + 32 * (j & 1);
-        ok = ok && wait_for(s_full + g, j & 1, err, stop);
-        // the weights' place: free once the page two before has been added
-        if (taken >= 2) ok = ok && wait_for(o_done + sb, ((j >> 1) - 1) & 1, err, stop);
+        const uint32_t srow = trow + TM_S + 64 * sb;
+        ok = ok && wait_for(s_full + sb, (j >> 1) & 1, err, stop);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         ++n_mine;
         ++taken;
         if (idle) {
-          mbar_arrive(s_free + g);
           mbar_arrive(p_full + sb);
           continue;
         }
-        float x[32];
-        tmem_ld32f(srow, x);
+        float x[64];
+        auto load = [&]() {
+          tmem_ld32f(srow, x);
+          tmem_ld32f(srow + 32, x + 32);
+          tmem_wait_ld();
+        };
+        load();
         const bool tail = t >= full;
         const float4 sc = *reinterpret_cast<const float4*>(aux + ((n_page + t) & 7) * 4);  // s_k, s_v, log2 s_v, 1 / s_v
         // columns [lo, hi] of the page are seen by this row
         const int hi = real ? qpos - (page0 + t) * KV8_BLOCK : KV8_BLOCK, lo = real && a.window > 0 ? hi - a.window + 1 : 0;
         const bool seen = __all_sync(0xffffffffu, !tail && hi >= KV8_BLOCK - 1 && lo <= 0);  // all columns, by 16-bit rows none
-        // scores of columns 32 c .. + 31 less mref: masked ones -inf
-        auto scores = [&](float (&x)[32], int c4, float mref) {
-          const float mul = qmul * sc.x;
-          if (seen) {
+        const float mul = qmul * sc.x;
+        // the scores (exponents of 2) of a page that is not seen whole, masked ones -inf
+        auto mask = [&]() {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = fmaf(x[i], mul, -mref);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int col = 32 * c4 + i;
-              const float f = tail ? qmul * tail_sc[col] : mul;
-              x[i] = col >= lo && col <= hi ? fmaf(x[i], f, -mref) : -INFINITY;
-            }
+          for (int i = 0; i < 64; ++i) {
+            const float f = tail ? qmul * tail_sc[i] : mul;
+            x[i] = i >= lo && i <= hi ? x[i] * f : -INFINITY;
           }
         };
-        // The references anew at columns 32 c4: the exact maximum of the columns
-        // from there on; sums, O and the page's weights so far are rescaled.
-        float sum = 0.f;
-        float off = 0.f;  // what the scores in x are less
-        auto renew = [&](int c4) {
+        // The references anew, from the exact maximum of the page; sum and O are rescaled.
+        auto renew = [&]() {
           float vtop = tail ? 0.f : fmaxf(sc.y, 0.f);  // ignores NaN
           if (tail)
             for (int i = 0; i < 64; ++i) vtop = fmaxf(vtop, tail_sc[64 + i]);
           if (!(vtop > 0.f)) vtop = 1.f;
+          load();
           float mt = -INFINITY;
-          if (c4 == 0) {
-#pragma unroll 1
-            for (int q4 = 0; q4 < 2; ++q4) {
-              float y[32];
-              tmem_ld32f(srow + 32 * q4, y);
-              tmem_wait_ld();
-              scores(y, q4, 0.f);
+          if (seen) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) mt = fmaxf(mt, y[i]);
-            }
+            for (int i = 0; i < 64; ++i) mt = fmaxf(mt, x[i] * mul);
           } else {
-            // the second half's scores are in registers, less `off`: their place may be taken
+            mask();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) mt = fmaxf(mt, x[i]);
-            mt += off;
+            for (int i = 0; i < 64; ++i) mt = fmaxf(mt, x[i]);
           }
           const float m_new = fmaxf(m, mt), e_new = fmaxf(e, mt + log2f(vtop));
           const float mb = m_new == -INFINITY ? 0.f : m_new, eb = e_new == -INFINITY ? 0.f : e_new;
-          const float al = ex2(m - mb), ao = ex2(e - eb);
-          l *= al;
-          sum *= al;
+          const float ao = ex2(e - eb);
+          l *= ex2(m - mb);
           m = m_new;
           e = e_new;
           // bounded, so that a weight that underflowed stays 0 beside a far larger earlier score
@@ -643,109 +625,77 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           ref = e_new == -INFINITY ? 0.f : ex2(-lef);
           if (taken > 1) {
             // the page before may still be being added
-            ok = wait_for(o_done + 2 * g + ((j - 1) & 1), ((j - 1) >> 1) & 1, err, stop);
+            ok = wait_for(o_done + (sb ^ 1), ((j - 1) >> 1) & 1, err, stop);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
 #pragma unroll 1
-            for (int q4 = 0; q4 < 4; ++q4) {
+            for (int c4 = 0; c4 < 4; ++c4) {
               uint32_t y[32];
-              tmem_ld32(orow + 32 * q4, y);
+              tmem_ld32(orow + 32 * c4, y);
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * ao);
-              tmem_st32(orow + 32 * q4, y);
+              tmem_st32(orow + 32 * c4, y);
             }
-          }
-          tmem_wait_st();
-          if (c4 == 1) {
-            uint32_t y[16];
-            tmem_ld16(prow, y);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
-              y[i] = pack_f16x2(w.x * ao, w.y * ao);
-            }
-            tmem_st16(prow, y);
             tmem_wait_st();
           }
+          load();
         };
-        bool scored = false;  // x holds scores (in exponents of 2), not products
-        int fresh = -1;  // columns at which the references were set
-        tmem_wait_ld();
-        if (__any_sync(0xffffffffu, m == -INFINITY)) {
-          renew(0);
-          fresh = 0;
-        }
-#pragma unroll 1
-        for (int c4 = 0; c4 < 2; ++c4) {
-          uint32_t pk[16];
-          float s0, s1;  // sums of the fp16 weights and of the softmax's
-          while (true) {
-            const float mref = m == -INFINITY ? 0.f : m;
+        bool fresh = __any_sync(0xffffffffu, m == -INFINITY);
+        if (fresh) renew();
+        uint32_t pk[32];
+        float s0, s1;  // sums of the fp16 weights and of the softmax's
+        while (true) {
+          const float mref = m == -INFINITY ? 0.f : m;
+          // Weights of a page that is seen whole take the value scale into the
+          // exponent, and their sum is divided by it: a product less per weight.
+          // Not where it is so small that weights would underflow.
+          const float lw = lef + sc.z;
+          if (__all_sync(0xffffffffu, seen && lw > -60.f)) {
+            const uint64_t mul2 = f32x2(mul, mul), off2 = f32x2(lw - mref, lw - mref);
+            uint64_t a0 = 0, a1 = 0;
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+              const float2 z = f32x2_split(f32x2_fma(f32x2(x[i], x[i + 1]), mul2, off2));
+              const float y0 = ex2(z.x), y1 = ex2(z.y);
+              uint64_t& acc = i & 2 ? a1 : a0;
+              acc = f32x2_add(acc, f32x2(y0, y1));
+              pk[i / 2] = pack_f16x2(y0, y1);
+            }
+            const float2 b0 = f32x2_split(f32x2_add(a0, a1));
+            s0 = b0.x + b0.y;
+            s1 = s0 * (ref * sc.w);
+          } else {
+            const float ef = ex2(lef), w = ef * sc.y;
+            if (seen) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) x[i] *= mul;
+            } else {
+              mask();
+            }
             s0 = s1 = 0.f;
-            // Weights of a page that is seen whole take the value scale into the
-            // exponent, and their sum is divided by it: a product less per weight.
-            // Not where it is so small that weights would underflow.
-            const float lw = lef + sc.z;
-            const bool plain = __all_sync(0xffffffffu, seen && lw > -60.f);
-            off = plain ? mref - lw : mref;
-            if (scored) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] -= off;
-            } else {
-              scores(x, c4, off);
-            }
-            if (plain) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float y0 = ex2(x[i]), y1 = ex2(x[i + 1]);
-                s0 += y0;
-                s1 += y1;
-                pk[i / 2] = pack_f16x2(y0, y1);
-              }
-              s0 += s1;
-              s1 = s0 * (ref * sc.w);
-            } else {
-              const float ef = ex2(lef), w = ef * sc.y;
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                float y0 = ex2(x[i]), y1 = ex2(x[i + 1]);
-                s1 += y0 + y1;
-                // a scale that is NaN stays behind the mask
-                const int col = 32 * c4 + i;
-                y0 = x[i] == -INFINITY ? 0.f : y0 * (tail ? ef * tail_sc[64 + col] : w);
-                y1 = x[i + 1] == -INFINITY ? 0.f : y1 * (tail ? ef * tail_sc[64 + col + 1] : w);
-                s0 += y0 + y1;
-                pk[i / 2] = pack_f16x2(y0, y1);
-              }
-            }
-            if (!__any_sync(0xffffffffu, !(s0 <= W_LIMIT)) || fresh == c4) break;  // also an infinity or NaN
-            renew(c4);
-            fresh = c4;
-            if (c4 == 0) {
-              tmem_ld32f(srow, x);
-              tmem_wait_ld();
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] += off;  // the scores themselves: -inf stays
-              scored = true;
+            for (int i = 0; i < 64; i += 2) {
+              float y0 = ex2(x[i] - mref), y1 = ex2(x[i + 1] - mref);
+              s1 += y0 + y1;
+              // a scale that is NaN stays behind the mask
+              y0 = x[i] == -INFINITY ? 0.f : y0 * (tail ? ef * tail_sc[64 + i] : w);
+              y1 = x[i + 1] == -INFINITY ? 0.f : y1 * (tail ? ef * tail_sc[64 + i + 1] : w);
+              s0 += y0 + y1;
+              pk[i / 2] = pack_f16x2(y0, y1);
             }
           }
-          if (c4 == 0) tmem_ld32f(srow + 32, x);  // the other half, while these weights are stored
-          sum += s1;
-          // P's columns: pairs of keys, those of 16 in V's order 0 1 8 9, 2 3 10 11, 4 5 12 13, 6 7 14 15
-          const uint32_t w[16] = {pk[0], pk[4], pk[1], pk[5], pk[2], pk[6], pk[3], pk[7],
-                                  pk[8], pk[12], pk[9], pk[13], pk[10], pk[14], pk[11], pk[15]};
-          tmem_st16(prow + 16 * c4, w);
-          if (c4 == 0) {
-            tmem_wait_ld();
-            tc_fence_before();
-            mbar_arrive(s_free + g);  // all scores are in registers
-          }
+          if (!__any_sync(0xffffffffu, !(s0 <= W_LIMIT)) || fresh) break;  // also an infinity or NaN
+          renew();
+          fresh = true;
         }
+        // P's columns: pairs of keys, those of 16 in V's order 0 1 8 9, 2 3 10 11, 4 5 12 13, 6 7 14 15
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = pk[(i & 24) + (i & 1) * 4 + ((i & 7) >> 1)];
+        tmem_st32(srow, w);
         tmem_wait_st();
-        l += sum;
+        l += s1;
         tc_fence_before();
         mbar_arrive(p_full + sb);
       }
