@@ -124,6 +124,21 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int32_t
   }
 }
 
+// Logarithm and inverse of a value scale: their errors, 2^-22 of it, go to a page's
+// weights and their sum alone (a scale that is not a normal number takes the path
+// that uses neither), and one thread makes them on every page's way, where the exact
+// functions took 600 cycles.
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -426,7 +441,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           for (int i = 0; i < 4; ++i) x[i] = src[(cw * 4 + i) * 32 + lane];
           if (ct == 0) {
             const float2 sc = *reinterpret_cast<const float2*>(sm + L::RAWS + sl * 16);
-            *reinterpret_cast<float4*>(aux + (T & 7) * 4) = make_float4(sc.x, sc.y, log2f(sc.y), 1.0f / sc.y);
+            *reinterpret_cast<float4*>(aux + (T & 7) * 4) = make_float4(sc.x, sc.y, lg2_approx(sc.y), rcp_approx(sc.y));
           }
           mbar_arrive(rk_empty + sl);
 #pragma unroll
