@@ -787,7 +787,9 @@ hq_status launch(Kv8AttnArgs& a, int sms, cudaStream_t st) {
 }
 
 // Rows of a kv head, in eights.
-constexpr int ROWS_MAX = 32;  // more go to the tcgen05 kernel
+// More go to the tcgen05 kernel (64 sequences of 1K-8K, 8 kv heads: 24 rows 182 us here,
+// 32 rows 419 us here, for want of registers, and 300 us there).
+constexpr int ROWS_MAX = 24;
 int row_eights(int64_t rows) { return static_cast<int>((rows + 7) / 8); }
 
 // One CTA of 8 warps on an SM, or two of 4.  Where CTAs finish several tasks
@@ -807,8 +809,7 @@ hq_status launch_f(Kv8AttnArgs& a, int sms, cudaStream_t st) {
   switch (row_eights(a.G * a.max_new)) {
     case 1: return launch_w<E, FMT, 1>(a, sms, st);
     case 2: return launch_w<E, FMT, 2>(a, sms, st);
-    case 3: return launch<E, FMT, 3, 8>(a, sms, st);
-    default: return launch<E, FMT, 4, 8>(a, sms, st);
+    default: return launch<E, FMT, 3, 8>(a, sms, st);
   }
 }
 

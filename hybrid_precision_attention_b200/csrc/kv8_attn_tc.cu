@@ -18,7 +18,7 @@
 //          NT = 2: the streams are two row tiles over the same pages; NT = 1 (up to
 //          128 rows): the same rows, each stream taking every other page, joined at
 //          the end
-//   8-11   converters: codes of a page -> fp16 in the 128-byte-swizzled operand
+//   8-11   converters, two warps for K and two for V: codes of a page -> fp16 in the 128-byte-swizzled operand
 //          layouts, K as [key][d], V as [d][key], both K-major, four stages of each.
 //          The page's V order gives a thread 4 keys of one d, which it stores as 8
 //          bytes: the keys of 16 stand as t, t+1, t+8, t+9 for t = 0, 2, 4, 6, and
@@ -50,7 +50,10 @@ constexpr int W_CONV = 8, W_COPY = 12, W_MMA = 14;  // W_COPY: K, W_COPY + 1: V;
 constexpr int THREADS = 16 * 32;
 constexpr float BIAS = 6.0f;               // log2 of the fp16 weight at both references
 constexpr float W_LIMIT = 32768.0f;        // sum of a page's fp16 weights above which the references are set anew
-constexpr int TASK_UNITS = 8;              // what a task costs besides its pages, in pages
+// what a task costs besides its pages, in pages (some 16000 cycles, two thirds of them
+// queries, epilogue and the first and last pages' latencies)
+template <int NT>
+constexpr int TASK_UNITS = NT == 2 ? 8 : 14;
 constexpr uint32_t TMEM_COLS = 512;        // each stream: S 2 x 64 columns (P in the first 32 of each), O 128
 constexpr uint32_t TM_S = 0, TM_O = 256;
 // fp16, K-major A and B, f32 accumulate
@@ -151,7 +154,7 @@ template <int NT>
 __device__ __noinline__ void enter(const Kv8AttnArgs& a, Walk& k, uint32_t total, Job& j) {
   k.sp = span_of<NT>(k.s, a.G, a.window, k.grp);
   k.pages = pages_of(k.sp);
-  k.units = min(static_cast<uint32_t>(k.pages + TASK_UNITS - k.t0), k.u1 - k.u);
+  k.units = min(static_cast<uint32_t>(k.pages + TASK_UNITS<NT> - k.t0), k.u1 - k.u);
   k.t1 = min(k.pages, k.t0 + static_cast<int>(k.units));
   const uint32_t parts = min(total, gridDim.x), run = total / parts, more = total - run * parts;
   // the first `more` runs have a unit more than the others
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       Kv8Seq s;
       kv8_seq(c, a.cu, a.kv_len, a.N, a.max_new, b, blockIdx.x == 0, s);
       const int groups = (s.n * a.G + ROWS - 1) / ROWS;
-      for (int i = 0; i < groups; ++i) n += pages_of(span_of<NT>(s, a.G, a.window, i)) + TASK_UNITS;
+      for (int i = 0; i < groups; ++i) n += pages_of(span_of<NT>(s, a.G, a.window, i)) + TASK_UNITS<NT>;
     }
     uint32_t x = n;
 #pragma unroll
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       k.h = rel / each;
       rel -= k.h * each;
       for (k.grp = 0;; ++k.grp) {
-        const uint32_t n = pages_of(span_of<NT>(k.s, a.G, a.window, k.grp)) + TASK_UNITS;
+        const uint32_t n = pages_of(span_of<NT>(k.s, a.G, a.window, k.grp)) + TASK_UNITS<NT>;
         if (rel < n) break;
         rel -= n;
       }
@@ -281,14 +284,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   if (threadIdx.x == 0) {
     for (int i = 0; i < RK; ++i) {
       mbar_init(rk_full + i, 1);
-      mbar_init(rk_empty + i, 128);
+      mbar_init(rk_empty + i, 64);
       mbar_init(rv_full + i, 1);
-      mbar_init(rv_empty + i, 128);
+      mbar_init(rv_empty + i, 64);
     }
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(k_full + i, 128);
+      mbar_init(k_full + i, 64);
       mbar_init(k_empty + i, NT);
-      mbar_init(v_full + i, 128);
+      mbar_init(v_full + i, 64);
       mbar_init(v_empty + i, NT);
     }
     for (int i = 0; i < 2; ++i) mbar_init(drain + i, 1);
@@ -327,63 +330,52 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
     int32_t* err = c.err + job.b;
 
     // ---------------------------------------------------------- queries -> shared memory
+    // half a warp a row, 16 bytes a lane; every load of the warp's 32 rows in flight at once
     float qmul = a.scale;
-    if (warp < 8 && (NT == 2 || warp < 4)) {
-      const int r = threadIdx.x & 127, rr = job.row0 + (NT == 2 ? (warp >> 2) * TR : 0) + r;
-      const uint32_t dst = base + L::Q + (NT == 2 ? (warp >> 2) * 32768 : 0) + r * 128;
-      const E* p = static_cast<const E*>(a.q) + static_cast<int64_t>(job.tok0 + rr / a.G) * a.q_tok +
-                   static_cast<int64_t>(job.h * a.G + rr % a.G) * a.q_head;
-      float inv = 1.0f;
-      if (IsBf16<E>::value && rr < rows) {
-        // bf16 rows become fp16 at a power of two that brings their largest value to [2^14, 2^15)
-        uint32_t m = 0;
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
+    if (warp < 8) {
+      const int r0 = (warp & 3) * 32, tile = NT == 2 ? warp >> 2 : 0, ch = lane & 15;  // stream 1 of NT = 1: the same rows
+      uint4 v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int rr = job.row0 + tile * TR + r0 + 2 * i + (lane >> 4);
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (rr < rows)
+          v[i] = reinterpret_cast<const uint4*>(static_cast<const E*>(a.q) + static_cast<int64_t>(job.tok0 + rr / a.G) * a.q_tok +
+                                                static_cast<int64_t>(job.h * a.G + rr % a.G) * a.q_head)[ch];
+      }
+      float* unit = reinterpret_cast<float*>(sm + L::RAW) + warp * 32;  // the copies' place: they wait for the queries
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + (lane >> 4);
+        if (IsBf16<E>::value) {
+          // bf16 rows become fp16 at a power of two that brings their largest value to [2^14, 2^15)
           E e[8];
-          *reinterpret_cast<uint4*>(e) = reinterpret_cast<const uint4*>(p)[i];
+          *reinterpret_cast<uint4*>(e) = v[i];
+          uint32_t m = 0;
 #pragma unroll
           for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(to_float(e[j])) & 0x7fffffffu);
-        }
-        if (m != 0 && m < 0x7f800000u) {
-          const int ex = max(static_cast<int>(m >> 23) - 127 - 14, -126);
-          qmul *= __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
-          inv = ex == -126 ? 0x1p126f : __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-        }
-      }
-#pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
-        if (rr < rows) {
-          E e[8];
-          *reinterpret_cast<uint4*>(e) = reinterpret_cast<const uint4*>(p)[i];
-          if (IsBf16<E>::value) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = pack_f16x2(to_float(e[2 * j]) * inv, to_float(e[2 * j + 1]) * inv);
-          } else {
-            *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(e);
+          for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          float inv = 1.0f, u = 1.0f;
+          if (m != 0 && m < 0x7f800000u) {
+            const int ex = max(static_cast<int>(m >> 23) - 127 - 14, -126);
+            u = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+            inv = ex == -126 ? 0x1p126f : __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
           }
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = pack_f16x2(to_float(e[2 * j]) * inv, to_float(e[2 * j + 1]) * inv);
+          v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          if (ch == 0) unit[r] = u;
         }
-        sts128(dst + (i >> 3) * 16384 + (((i & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+        if (NT == 2 || warp < 4)
+          sts128(base + L::Q + tile * 32768 + (ch >> 3) * 16384 + (r0 + r) * 128 + (((ch & 7) ^ (r & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+      }
+      if (IsBf16<E>::value) {
+        __syncwarp();
+        qmul *= unit[lane];
       }
       fence_proxy_async_smem();
-    }
-    if (NT == 1 && warp >= 4 && warp < 8) {
-      // stream 1 scores the same rows
-      const int rr = job.row0 + (threadIdx.x & 127);
-      if (IsBf16<E>::value && rr < rows) {
-        const E* p = static_cast<const E*>(a.q) + static_cast<int64_t>(job.tok0 + rr / a.G) * a.q_tok +
-                     static_cast<int64_t>(job.h * a.G + rr % a.G) * a.q_head;
-        uint32_t m = 0;
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-          E e[8];
-          *reinterpret_cast<uint4*>(e) = reinterpret_cast<const uint4*>(p)[i];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(to_float(e[j])) & 0x7fffffffu);
-        }
-        if (m != 0 && m < 0x7f800000u)
-          qmul *= __uint_as_float(static_cast<uint32_t>(max(static_cast<int>(m >> 23) - 127 - 14, -126) + 127) << 23);
-      }
     }
     __syncthreads();
 
@@ -415,109 +407,91 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       }
     } else if (warp >= W_CONV && warp < W_COPY) {
       // -------------------------------------------------------- converters
-      const int ct = threadIdx.x - W_CONV * 32, cw = ct >> 5;  // thread of 128, warp of 4
+      const int cw = (warp - W_CONV) & 1, ct = cw * 32 + lane;  // warp of two, thread of 64
       const int g = lane >> 2, t4 = lane & 3;
-      // K of page t: free once the page four before has been scored
-      auto convert_k = [&](int t) {
-        const int T = n_page + t, st = T % STAGES;
-        if (T >= STAGES) ok = wait_for(k_empty + st, (T / STAGES - 1) & 1, err, stop);
+      auto await = [&](uint64_t* bar, int parity) {
+        if (__any_sync(0xffffffffu, mbar_try_wait(bar, parity & 1))) return true;
+        ok = wait_for(bar, parity & 1, err, stop);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
-        const uint32_t dst = base + L::K + st * 16384;
-        uint32_t y[8] = {};
-        auto put = [&](int e) {  // 512-byte piece of codes: 8 keys x 64 d
-          const uint32_t row = dst + (e & 1) * 8192 + ((e >> 1) * 8 + g) * 128;
-          sts128(row + (((2 * t4) ^ g) << 4), y[0], y[1], y[2], y[3]);
-          sts128(row + (((2 * t4 + 1) ^ g) << 4), y[4], y[5], y[6], y[7]);
-        };
-        if (t < full) {
-          const int n = n_raw + t, sl = n % RK;
-          ok = wait_for(rk_full + sl, (n / RK) & 1, err, stop);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) return;
-          const uint4* src = reinterpret_cast<const uint4*>(sm + L::RAW + sl * HALF);
-          uint4 x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = src[(cw * 4 + i) * 32 + lane];
-          if (ct == 0) {
-            const float2 sc = *reinterpret_cast<const float2*>(sm + L::RAWS + sl * 16);
-            *reinterpret_cast<float4*>(aux + (T & 7) * 4) = make_float4(sc.x, sc.y, lg2_approx(sc.y), rcp_approx(sc.y));
+        return ok;
+      };
+      auto convert = [&](auto which) {
+        constexpr bool VAL = decltype(which)::value;  // values, else keys
+        uint64_t* slot_full = VAL ? rv_full : rk_full;
+        uint64_t* slot_empty = VAL ? rv_empty : rk_empty;
+        uint64_t* st_full = VAL ? v_full : k_full;
+        uint64_t* st_empty = VAL ? v_empty : k_empty;
+        // where the thread's part of a stage goes.  K: 16 d of one key, two 16-byte
+        // operand chunks; V: 4 keys of each of 4 d, 8 bytes each
+        auto put = [&](uint32_t dst, int e, const uint32_t (&y)[8]) {
+          if (VAL) {  // 512 bytes of codes: 16 keys (e / 4) x 32 d (e % 4)
+            const uint32_t row = dst + ((e & 3) * 32 + g) * 128 + ((((e >> 2) * 2 + (t4 >> 1)) ^ g) << 4) + (t4 & 1) * 8;
+            sts64(row, y[0], y[1]);
+            sts64(row + 8 * 128, y[2], y[3]);
+            sts64(row + 16 * 128, y[4], y[5]);
+            sts64(row + 24 * 128, y[6], y[7]);
+          } else {    // 8 keys (e / 2) x 64 d (e % 2)
+            const uint32_t row = dst + (e & 1) * 8192 + ((e >> 1) * 8 + g) * 128;
+            sts128(row + (((2 * t4) ^ g) << 4), y[0], y[1], y[2], y[3]);
+            sts128(row + (((2 * t4 + 1) ^ g) << 4), y[4], y[5], y[6], y[7]);
           }
-          mbar_arrive(rk_empty + sl);
+        };
+        for (int t = 0; t < full; ++t) {
+          const int T = n_page + t, st = T % STAGES, sl = (n_raw + t) % RK;
+          if (!await(slot_full + sl, (n_raw + t) / RK)) return;
+          const uint4* src = reinterpret_cast<const uint4*>(sm + L::RAW + ((VAL ? RK : 0) + sl) * HALF) + cw * 8 * 32 + lane;
+          uint4 x[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 8; ++i) x[i] = src[i * 32];
+          const float2 sc = VAL ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(sm + L::RAWS + sl * 16);
+          mbar_arrive(slot_empty + sl);
+          // The stage is free once the page four before has been scored (K) or added (V).
+          // Scoring that page took the place of the one four before it in its stream at
+          // least, so that the scales of eight pages before have been used.
+          if (T >= STAGES && !await(st_empty + st, T / STAGES - 1)) return;
+          if (!VAL && ct == 0)
+            *reinterpret_cast<float4*>(aux + (T & 7) * 4) = make_float4(sc.x, sc.y, lg2_approx(sc.y), rcp_approx(sc.y));
+          const uint32_t dst = base + (VAL ? L::V : L::K) + st * 16384;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t y[8];
             kv8_half4<FMT>(x[i].x, y[0], y[1]);
             kv8_half4<FMT>(x[i].y, y[2], y[3]);
             kv8_half4<FMT>(x[i].z, y[4], y[5]);
             kv8_half4<FMT>(x[i].w, y[6], y[7]);
-            put(cw * 4 + i);
+            put(dst, cw * 8 + i, y);
           }
-        } else {
-          const uint4* src = reinterpret_cast<const uint4*>(c.tail_k + (bh * 2 + ((page0 + t) & 1)) * KV8_BLOCK * D);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            *reinterpret_cast<uint4*>(y) = src[((cw * 4 + i) * 32 + lane) * 2];
-            *reinterpret_cast<uint4*>(y + 4) = src[((cw * 4 + i) * 32 + lane) * 2 + 1];
-            put(cw * 4 + i);
-          }
-          if (ct == 0) *reinterpret_cast<float4*>(aux + (T & 7) * 4) = make_float4(1.f, 1.f, 0.f, 1.f);
-          // the rows' scales; past the length 1: nothing there is seen
-          const int which = ct >> 6, r = ct & 63;
-          tail_sc[ct] = (page0 + t) * KV8_BLOCK + r < job.len
-                            ? c.tail_scale[(bh * 2 + which) * HQ_KV8_TAIL + ((page0 + t) & 1) * KV8_BLOCK + r]
-                            : 1.0f;
+          fence_proxy_async_smem();
+          mbar_arrive(st_full + st);
         }
-        fence_proxy_async_smem();
-        mbar_arrive(k_full + st);
-      };
-      // V of page t: free once the page four before has been added
-      auto convert_v = [&](int t) {
-        const int T = n_page + t, st = T % STAGES;
-        if (T >= STAGES) ok = wait_for(v_empty + st, (T / STAGES - 1) & 1, err, stop);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
-        // 16-byte chunk (16 tokens cw, 32 d i, d % 8 = g, token pair t4): 4 words of 4 tokens of one d
-        const uint32_t dst = base + L::V + st * 16384 + g * 128 + (((cw * 2 + (t4 >> 1)) ^ g) << 4) + (t4 & 1) * 8;
-        if (t < full) {
-          const int n = n_raw + t, sl = n % RK;
-          ok = wait_for(rv_full + sl, (n / RK) & 1, err, stop);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) return;
-          const uint4* src = reinterpret_cast<const uint4*>(sm + L::RAW + (RK + sl) * HALF);
-          uint4 x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = src[(cw * 4 + i) * 32 + lane];
-          mbar_arrive(rv_empty + sl);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t y[2];
-            kv8_half4<FMT>(x[i].x, y[0], y[1]);
-            sts64(dst + (i * 32) * 128, y[0], y[1]);
-            kv8_half4<FMT>(x[i].y, y[0], y[1]);
-            sts64(dst + (i * 32 + 8) * 128, y[0], y[1]);
-            kv8_half4<FMT>(x[i].z, y[0], y[1]);
-            sts64(dst + (i * 32 + 16) * 128, y[0], y[1]);
-            kv8_half4<FMT>(x[i].w, y[0], y[1]);
-            sts64(dst + (i * 32 + 24) * 128, y[0], y[1]);
+        if (full < nt) {
+          // the incomplete block, in 16 bits from where it lies
+          const int T = n_page + full, st = T % STAGES, half = (page0 + full) & 1;
+          if (T >= STAGES && !await(st_empty + st, T / STAGES - 1)) return;
+          const uint32_t dst = base + (VAL ? L::V : L::K) + st * 16384;
+          const uint4* src = reinterpret_cast<const uint4*>((VAL ? c.tail_v : c.tail_k) + (bh * 2 + half) * KV8_BLOCK * D);
+#pragma unroll 2
+          for (int i = 0; i < 8; ++i) {
+            uint32_t y[8];
+            *reinterpret_cast<uint4*>(y) = src[((cw * 8 + i) * 32 + lane) * 2];
+            *reinterpret_cast<uint4*>(y + 4) = src[((cw * 8 + i) * 32 + lane) * 2 + 1];
+            put(dst, cw * 8 + i, y);
           }
-        } else {
-          const uint4* src = reinterpret_cast<const uint4*>(c.tail_v + (bh * 2 + ((page0 + t) & 1)) * KV8_BLOCK * D);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 x = src[((cw * 4 + i) * 32 + lane) * 2], y = src[((cw * 4 + i) * 32 + lane) * 2 + 1];
-            sts64(dst + (i * 32) * 128, x.x, x.y);
-            sts64(dst + (i * 32 + 8) * 128, x.z, x.w);
-            sts64(dst + (i * 32 + 16) * 128, y.x, y.y);
-            sts64(dst + (i * 32 + 24) * 128, y.z, y.w);
+          if (!VAL) {
+            if (ct == 0) *reinterpret_cast<float4*>(aux + (T & 7) * 4) = make_float4(1.f, 1.f, 0.f, 1.f);
+            // the rows' scales; past the length 1: nothing there is seen
+            const float* ts = c.tail_scale + bh * 2 * HQ_KV8_TAIL + half * KV8_BLOCK + ct;
+            const bool in = (page0 + full) * KV8_BLOCK + ct < job.len;
+            tail_sc[ct] = in ? ts[0] : 1.0f;
+            tail_sc[64 + ct] = in ? ts[HQ_KV8_TAIL] : 1.0f;
           }
+          fence_proxy_async_smem();
+          mbar_arrive(st_full + st);
         }
-        fence_proxy_async_smem();
-        mbar_arrive(v_full + st);
       };
-      // K runs two pages ahead of V: a page is scored before its values are needed
-      for (int t = 0; ok && t < nt + 2; ++t) {
-        if (t < nt) convert_k(t);
-        if (ok && t >= 2) convert_v(t - 2);
+      if (ok) {
+        if (warp < W_CONV + 2) convert(std::false_type{});
+        else convert(std::true_type{});
       }
       n_raw += full;
       n_page += nt;
@@ -735,7 +709,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           joined[TR + r] = taken > 0 ? e : -INFINITY;
           joined[2 * TR + r] = l;
         }
-        if (g == 1 && ok && taken > 0) {
+        if (g == 1 && ok && taken > 0 && !idle) {
 #pragma unroll 1
           for (int c4 = 0; c4 < 4; ++c4) {
             float x[32];
@@ -784,7 +758,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
         }
         if (real && a.lse != nullptr) a.lse[tok * a.Hq + head] = m + log2f(l);
       };
-      if (owner && ok) {
+      if (owner && ok && !idle) {
         auto cols = [&](int c4, float (&x)[32]) {
           o_cols(c4, x);
           if (NT == 1) {
@@ -817,7 +791,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           flags[1] = last;
         }
         asm volatile("bar.sync 2, 256;" ::: "memory");
-        if (flags[1] && owner && ok) {
+        if (flags[1] && owner && ok && !idle) {
           auto piece = [&](int p) { return a.parts + (static_cast<size_t>(2 * p + (p == c0)) * NT + q) * PIECE; };
           float mm = -INFINITY, ee = -INFINITY, ll = 0.f;
           for (int p = c0; p <= c1; ++p) {
@@ -883,7 +857,7 @@ hq_status launch(const Kv8AttnArgs& a, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return cuda_fail(e, "kv8 attention setup");
   // units are counted in 32 bits
   const double groups = static_cast<double>(a.G) * a.max_new / (NT * TR) + 1;
-  if (groups * a.c.B * a.c.Hkv * (a.c.cap / KV8_BLOCK + TASK_UNITS) >= 4e9) return HQ_ERR_UNSUPPORTED;
+  if (groups * a.c.B * a.c.Hkv * (a.c.cap / KV8_BLOCK + TASK_UNITS<NT>) >= 4e9) return HQ_ERR_UNSUPPORTED;
   kv8_attn_tc_kernel<E, FMT, NT><<<sms, THREADS, L::BYTES, st>>>(a);
   return cuda_status(cudaGetLastError(), "kv8 attention launch");
 }
