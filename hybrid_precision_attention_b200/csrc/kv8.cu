@@ -7,7 +7,10 @@
 // two newest blocks so that up to 64 positions can be taken back.
 //
 // Both kernels are bound by memory: an append reads each new row once and
-// writes its codes once, a read-back the other way round.
+// writes its codes once, a read-back the other way round.  16-bit rows pass
+// through shared memory as they are: the page's order of values, pairs of tokens
+// of one d, is what the transposed 8x8 matrix loads and stores (ldmatrix,
+// stmatrix) exchange, so that no element moves by itself.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -17,7 +20,8 @@
 namespace hq {
 namespace {
 
-constexpr int TS = D + 4;  // row stride of the staged tile in floats: the V order's accesses (4 rows x 8 columns a step) hit 32 banks
+constexpr int T16 = D + 8;  // row stride of a tile of 16-bit elements: 8 rows' 16-byte chunks hit 32 banks
+constexpr int TS = D + 4;   // row stride of the staged tile in floats: the V order's accesses (4 rows x 8 columns a step) hit 32 banks
 static_assert(D == 128, "the page orders are written for 128");
 
 struct AppendArgs {
@@ -35,6 +39,33 @@ __device__ __forceinline__ void load8(const E* p, float (&x)[8]) {
   *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = to_float(e[i]);
+}
+
+// four 8x8 matrices of 16-bit elements, transposed: lane l gets of matrix i the
+// elements (rows 2 (l % 4), + 1; column l / 4), from the rows that lanes 8 i .. 8 i + 7 address
+__device__ __forceinline__ void ldmatrix_t4(uint32_t (&r)[4], const void* row) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(row))
+               : "memory");
+}
+// the same places written from those lanes
+__device__ __forceinline__ void stmatrix_t4(void* row, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(row)), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+template <class E>
+__device__ __forceinline__ float2 pair_of(uint32_t w) {
+  if (IsBf16<E>::value) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <class E>
+__device__ __forceinline__ uint32_t to_pair(float x, float y) {
+  uint32_t w;
+  if (IsBf16<E>::value) *reinterpret_cast<__nv_bfloat162*>(&w) = __floats2bfloat162_rn(x, y);
+  else *reinterpret_cast<__half2*>(&w) = __floats2half2_rn(x, y);
+  return w;
 }
 
 // One CTA per (block that new tokens touch, kv head, K or V).  Sequence b's
@@ -73,7 +104,75 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__
   float* tail_scale = c.tail_scale + (bh * 2 + which) * HQ_KV8_TAIL;
   const int p0 = blk * KV8_BLOCK, half = blk & 1;
 
-  if (p0 + KV8_BLOCK <= s.len) {
+  if (p0 + KV8_BLOCK <= s.len && p0 >= s.first) {
+    // the block is complete and all its rows are new
+    uint16_t* tile16 = reinterpret_cast<uint16_t*>(tile);
+    // magnitudes compare as integers: the 15 bits of each half
+    uint32_t hi = 0, lo = 0;
+    uint4 v[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int e = it * 256 + tid, r = e / 16;
+      v[it] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(p0 + r) * a.tok[which] + e % 16 * 8);
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int e = it * 256 + tid;
+      const uint32_t w[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        hi = max(hi, w[i] & 0x7fff0000u);
+        lo = max(lo, w[i] & 0x7fffu);
+      }
+      *reinterpret_cast<uint4*>(tile16 + e / 16 * T16 + e % 16 * 8) = v[it];
+    }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, max(hi >> 16, lo));
+    if ((tid & 31) == 0) atomicMax(&sh_amax, top);
+    __syncthreads();
+    const float scale = kv8_scale(__float_as_uint(pair_of<E>(sh_amax).x), FMT);
+    const long long idx = kv8_page_index(c, bh, blk);
+    if (idx < 0) {
+      if (tid == 0) kv8_err(c, b, HQ_DEVERR_PAGE);
+    } else {
+      uint8_t* page = c.pages + static_cast<size_t>(idx) * HQ_KV8_PAGE_BYTES;
+      const bool plain = kv8_scale_plain(scale);
+      const float r = 1.0f / scale;
+      const int lane = tid & 31;
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
+        const int e = it * 256 + tid;  // 16-byte chunk of the page's codes
+        uint32_t h[8], w[4];           // its elements: two of a word, four of a code word
+        if (which) {
+          // tokens 16 tt .. + 15, d 32 dq ..: matrices of 8 tokens x 8 d
+          const int tt = e / 128, dq = e / 32 % 4;
+          const uint16_t* row = tile16 + (tt * 16 + (lane >> 3 & 1) * 8 + (lane & 7)) * T16 + dq * 32 + (lane >> 4) * 8;
+          uint32_t m[4];
+          ldmatrix_t4(m, row);         // (tokens 0-7, 8-15) of d 0-7, then of d 8-15
+          h[0] = m[0], h[1] = m[1], h[2] = m[2], h[3] = m[3];
+          ldmatrix_t4(m, row + 16);
+          h[4] = m[0], h[5] = m[1], h[6] = m[2], h[7] = m[3];
+        } else {
+          const uint4* row = reinterpret_cast<const uint4*>(tile16 + (e / 64 * 8 + e / 4 % 8) * T16 + e / 32 % 2 * 64 + (e & 3) * 16);
+          *reinterpret_cast<uint4*>(h) = row[0];
+          *reinterpret_cast<uint4*>(h + 4) = row[1];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = pair_of<E>(h[2 * i]), y = pair_of<E>(h[2 * i + 1]);
+          float z[4] = {x.x, x.y, y.x, y.y};
+          if (plain) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[j] = kv8_quotient(z[j], scale, r);
+            w[i] = kv8_round4<FMT>(z);
+          } else {
+            w[i] = kv8_codes4<FMT>(z, scale);
+          }
+        }
+        reinterpret_cast<uint4*>(page + (which ? HQ_KV8_V : 0))[e] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (tid == 0) *reinterpret_cast<float*>(page + (which ? HQ_KV8_VSCALE : HQ_KV8_KSCALE)) = scale;
+    }
+  } else if (p0 + KV8_BLOCK <= s.len) {
     // the block is complete: its rows into the tile, new ones from the input,
     // earlier ones from the tail
     uint32_t amax = 0;
@@ -195,6 +294,51 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const __grid_constant__ R
     len = 0;
   }
   const size_t bh = static_cast<size_t>(b) * c.Hkv + h;
+  E* out = static_cast<E*>(a.out[which]) + b * a.batch + h * a.head;
+  if (sizeof(E) == 2 && p0 + KV8_BLOCK <= len) {
+    // a complete block to 16-bit rows
+    uint16_t* tile16 = reinterpret_cast<uint16_t*>(tile);
+    const uint8_t* page = kv8_page(c, bh, blk);
+    const float scale = *reinterpret_cast<const float*>(page + (which ? HQ_KV8_VSCALE : HQ_KV8_KSCALE));
+    const int lane = tid & 31;
+    uint4 u[2];
+#pragma unroll
+    for (int it = 0; it < 2; ++it) u[it] = reinterpret_cast<const uint4*>(page + (which ? HQ_KV8_V : 0))[it * 256 + tid];
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+      const int e = it * 256 + tid;
+      const uint32_t w[4] = {u[it].x, u[it].y, u[it].z, u[it].w};
+      uint32_t y[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t p, q;
+        kv8_half4<FMT>(w[i], p, q);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p)), g = __half22float2(*reinterpret_cast<const __half2*>(&q));
+        y[2 * i] = to_pair<E>(f.x * scale, f.y * scale);
+        y[2 * i + 1] = to_pair<E>(g.x * scale, g.y * scale);
+      }
+      if (which) {
+        const int tt = e / 128, dq = e / 32 % 4;
+        uint16_t* row = tile16 + (tt * 16 + (lane >> 3 & 1) * 8 + (lane & 7)) * T16 + dq * 32 + (lane >> 4) * 8;
+        const uint32_t m0[4] = {y[0], y[1], y[2], y[3]}, m1[4] = {y[4], y[5], y[6], y[7]};
+        stmatrix_t4(row, m0);
+        stmatrix_t4(row + 16, m1);
+      } else {
+        uint4* row = reinterpret_cast<uint4*>(tile16 + (e / 64 * 8 + e / 4 % 8) * T16 + e / 32 % 2 * 64 + (e & 3) * 16);
+        row[0] = *reinterpret_cast<const uint4*>(y);
+        row[1] = *reinterpret_cast<const uint4*>(y + 4);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int e = it * 256 + tid, r = e / 16, p = p0 + r;
+      if (p >= a.start && p < a.start + a.n)
+        *reinterpret_cast<uint4*>(out + static_cast<int64_t>(p - a.start) * a.tok + e % 16 * 8) =
+            *reinterpret_cast<const uint4*>(tile16 + r * T16 + e % 16 * 8);
+    }
+    return;
+  }
   if (p0 + KV8_BLOCK <= len) {
     const uint8_t* page = kv8_page(c, bh, blk);
     const float scale = *reinterpret_cast<const float*>(page + (which ? HQ_KV8_VSCALE : HQ_KV8_KSCALE));
@@ -232,7 +376,6 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const __grid_constant__ R
     }
   }
   __syncthreads();
-  E* out = static_cast<E*>(a.out[which]) + b * a.batch + h * a.head;
   constexpr int V = 16 / sizeof(E);
   for (int e = tid; e < KV8_BLOCK * D / V; e += 256) {
     const int r = e / (D / V), d = e % (D / V) * V, p = p0 + r;

@@ -100,6 +100,32 @@ __device__ __forceinline__ float kv8_scale(uint32_t amax_bits, int fmt) {
   if (amax_bits == 0u) return 1.0f;
   return __fdiv_rn(__uint_as_float(amax_bits), fmt == HQ_KV8_E4M3 ? 448.0f : 127.0f);
 }
+// The quotients x / scale, each rounded as the division rounds it, by Markstein's
+// method (1990): with r = 1 / scale correctly rounded, q = x r and the remainder
+// x - q scale (exact in a fused product), q + remainder * r is the correctly rounded
+// quotient.  Needs scale, its inverse and the remainders away from the subnormal and
+// overflowing ranges: 2^-80 < scale < 2^80 (remainders that underflow then belong to
+// quotients that round to zero).  Three operations against a division's dozen.
+__device__ __forceinline__ bool kv8_scale_plain(float scale) { return scale > 0x1p-80f && scale < 0x1p80f; }
+__device__ __forceinline__ float kv8_quotient(float x, float scale, float r) {
+  const float q = x * r;
+  return fmaf(fmaf(-q, scale, x), r, q);
+}
+// codes of four quotients, lowest byte first
+template <int FMT>
+__device__ __forceinline__ uint32_t kv8_round4(const float (&y)[4]) {
+  if (FMT == HQ_KV8_E4M3) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+  }
+  // |y| < 127.5 (amax / scale is 127 up to rounding): the sum with 1.5 * 2^23 is rounded
+  // to an integer, ties to even, and its low byte is the code
+  uint32_t z[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z[i] = __float_as_uint(y[i] + 12582912.0f);
+  return prmt(prmt(z[0], z[1], 0x0040u), prmt(z[2], z[3], 0x0040u), 0x5410u);
+}
 // codes of four values, lowest byte first; `scale` NaN: zeros
 template <int FMT>
 __device__ __forceinline__ uint32_t kv8_codes4(const float (&x)[4], float scale) {
