@@ -33,14 +33,6 @@ struct AppendArgs {
   const int32_t* kv_len;
 };
 
-template <class E>
-__device__ __forceinline__ void load8(const E* p, float (&x)[8]) {
-  E e[8];
-  *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = to_float(e[i]);
-}
-
 // four 8x8 matrices of 16-bit elements, transposed: lane l gets of matrix i the
 // elements (rows 2 (l % 4), + 1; column l / 4), from the rows that lanes 8 i .. 8 i + 7 address
 __device__ __forceinline__ void ldmatrix_t4(uint32_t (&r)[4], const void* row) {
@@ -73,8 +65,8 @@ __device__ __forceinline__ uint32_t to_pair(float x, float y) {
 // at most n / 64 + 2 blocks, so the ranges do not overlap and the host needs to
 // know N and B only.
 template <class E, int FMT>
-__global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__ AppendArgs a) {
-  __shared__ __align__(16) float tile[KV8_BLOCK * TS];
+__global__ void __launch_bounds__(256, 5) kv8_append_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ __align__(16) uint16_t tile[KV8_BLOCK * T16];
   __shared__ int sh_b;
   __shared__ uint32_t sh_amax;
   const hq_kv8_cache& c = a.c;
@@ -104,17 +96,29 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__
   float* tail_scale = c.tail_scale + (bh * 2 + which) * HQ_KV8_TAIL;
   const int p0 = blk * KV8_BLOCK, half = blk & 1;
 
-  if (p0 + KV8_BLOCK <= s.len && p0 >= s.first) {
-    // the block is complete and all its rows are new
-    uint16_t* tile16 = reinterpret_cast<uint16_t*>(tile);
-    // magnitudes compare as integers: the 15 bits of each half
-    uint32_t hi = 0, lo = 0;
+  if (p0 + KV8_BLOCK <= s.len) {
+    // the block is complete: its rows into the tile, new ones from the input,
+    // earlier ones from the tail (whose values are numbers of E as they were)
+    const long long idx = kv8_page_index(c, bh, blk);
     uint4 v[4];
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
-      const int e = it * 256 + tid, r = e / 16;
-      v[it] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(p0 + r) * a.tok[which] + e % 16 * 8);
+      const int e = it * 256 + tid, p = p0 + e / 16, d = e % 16 * 8;
+      if (p >= s.first) {
+        v[it] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(p) * a.tok[which] + d);
+      } else {
+        const int r = p - p0;
+        const float sc = tail_scale[half * KV8_BLOCK + r];
+        const uint16_t* t = tail + half * KV8_BLOCK * D;
+        E x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          x[i] = from_float<E>(__half2float(__ushort_as_half(t[which ? HQ_KV8_V_INDEX(r, d + i) : HQ_KV8_K_INDEX(r, d + i)])) * sc);
+        v[it] = *reinterpret_cast<const uint4*>(x);
+      }
     }
+    // magnitudes compare as integers: the 15 bits of each half
+    uint32_t hi = 0, lo = 0;
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const int e = it * 256 + tid;
@@ -124,19 +128,19 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__
         hi = max(hi, w[i] & 0x7fff0000u);
         lo = max(lo, w[i] & 0x7fffu);
       }
-      *reinterpret_cast<uint4*>(tile16 + e / 16 * T16 + e % 16 * 8) = v[it];
+      *reinterpret_cast<uint4*>(tile + e / 16 * T16 + e % 16 * 8) = v[it];
     }
     const uint32_t top = __reduce_max_sync(0xffffffffu, max(hi >> 16, lo));
     if ((tid & 31) == 0) atomicMax(&sh_amax, top);
     __syncthreads();
     const float scale = kv8_scale(__float_as_uint(pair_of<E>(sh_amax).x), FMT);
-    const long long idx = kv8_page_index(c, bh, blk);
     if (idx < 0) {
       if (tid == 0) kv8_err(c, b, HQ_DEVERR_PAGE);
     } else {
       uint8_t* page = c.pages + static_cast<size_t>(idx) * HQ_KV8_PAGE_BYTES;
       const bool plain = kv8_scale_plain(scale);
       const float r = 1.0f / scale;
+      const uint64_t minus2 = f32x2(-scale, -scale), r2 = f32x2(r, r);
       const int lane = tid & 31;
 #pragma unroll
       for (int it = 0; it < 2; ++it) {
@@ -145,89 +149,27 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__
         if (which) {
           // tokens 16 tt .. + 15, d 32 dq ..: matrices of 8 tokens x 8 d
           const int tt = e / 128, dq = e / 32 % 4;
-          const uint16_t* row = tile16 + (tt * 16 + (lane >> 3 & 1) * 8 + (lane & 7)) * T16 + dq * 32 + (lane >> 4) * 8;
+          const uint16_t* row = tile + (tt * 16 + (lane >> 3 & 1) * 8 + (lane & 7)) * T16 + dq * 32 + (lane >> 4) * 8;
           uint32_t m[4];
           ldmatrix_t4(m, row);         // (tokens 0-7, 8-15) of d 0-7, then of d 8-15
           h[0] = m[0], h[1] = m[1], h[2] = m[2], h[3] = m[3];
           ldmatrix_t4(m, row + 16);
           h[4] = m[0], h[5] = m[1], h[6] = m[2], h[7] = m[3];
         } else {
-          const uint4* row = reinterpret_cast<const uint4*>(tile16 + (e / 64 * 8 + e / 4 % 8) * T16 + e / 32 % 2 * 64 + (e & 3) * 16);
+          const uint4* row = reinterpret_cast<const uint4*>(tile + (e / 64 * 8 + e / 4 % 8) * T16 + e / 32 % 2 * 64 + (e & 3) * 16);
           *reinterpret_cast<uint4*>(h) = row[0];
           *reinterpret_cast<uint4*>(h + 4) = row[1];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 x = pair_of<E>(h[2 * i]), y = pair_of<E>(h[2 * i + 1]);
-          float z[4] = {x.x, x.y, y.x, y.y};
           if (plain) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[j] = kv8_quotient(z[j], scale, r);
+            const float2 qx = kv8_quotients(x, minus2, r2), qy = kv8_quotients(y, minus2, r2);
+            const float z[4] = {qx.x, qx.y, qy.x, qy.y};
             w[i] = kv8_round4<FMT>(z);
           } else {
+            const float z[4] = {x.x, x.y, y.x, y.y};
             w[i] = kv8_codes4<FMT>(z, scale);
-          }
-        }
-        reinterpret_cast<uint4*>(page + (which ? HQ_KV8_V : 0))[e] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      if (tid == 0) *reinterpret_cast<float*>(page + (which ? HQ_KV8_VSCALE : HQ_KV8_KSCALE)) = scale;
-    }
-  } else if (p0 + KV8_BLOCK <= s.len) {
-    // the block is complete: its rows into the tile, new ones from the input,
-    // earlier ones from the tail
-    uint32_t amax = 0;
-#pragma unroll
-    for (int it = 0; it < KV8_BLOCK * D / 8 / 256; ++it) {
-      const int e = it * 256 + tid, r = e / (D / 8), d = e % (D / 8) * 8, p = p0 + r;
-      float x[8];
-      if (p >= s.first) {
-        load8(src + static_cast<int64_t>(p) * a.tok[which] + d, x);
-      } else {
-        const float sc = tail_scale[half * KV8_BLOCK + r];
-        const uint16_t* t = tail + half * KV8_BLOCK * D;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          x[i] = __half2float(__ushort_as_half(t[which ? HQ_KV8_V_INDEX(r, d + i) : HQ_KV8_K_INDEX(r, d + i)])) * sc;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
-      float4* q = reinterpret_cast<float4*>(tile + r * TS + d);
-      q[0] = make_float4(x[0], x[1], x[2], x[3]);
-      q[1] = make_float4(x[4], x[5], x[6], x[7]);
-    }
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    if ((tid & 31) == 0) atomicMax(&sh_amax, amax);
-    __syncthreads();
-    const float scale = kv8_scale(sh_amax, FMT);
-    const long long idx = kv8_page_index(c, bh, blk);
-    if (idx < 0) {
-      if (tid == 0) kv8_err(c, b, HQ_DEVERR_PAGE);
-    } else {
-      uint8_t* page = c.pages + static_cast<size_t>(idx) * HQ_KV8_PAGE_BYTES;
-#pragma unroll
-      for (int it = 0; it < KV8_BLOCK * D / 16 / 256; ++it) {
-        const int e = it * 256 + tid;  // 16-byte chunk of the page's codes
-        uint32_t w[4];
-        float x[4];
-        if (which) {
-          // V: words of one d and tokens r, r + 1, r + 8, r + 9
-          const int r = e / 128 * 16 + (e & 3) * 2, d = e / 32 % 4 * 32 + e / 4 % 8;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float* t = tile + r * TS + d + 8 * i;
-            x[0] = t[0];
-            x[1] = t[TS];
-            x[2] = t[8 * TS];
-            x[3] = t[9 * TS];
-            w[i] = kv8_codes4<FMT>(x, scale);
-          }
-        } else {
-          // K: 16 consecutive d of one token
-          const int r = e / 64 * 8 + e / 4 % 8, d = e / 32 % 2 * 64 + (e & 3) * 16;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(tile + r * TS + d + 4 * i);
-            w[i] = kv8_codes4<FMT>(x, scale);
           }
         }
         reinterpret_cast<uint4*>(page + (which ? HQ_KV8_V : 0))[e] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -284,7 +226,8 @@ struct ReadArgs {
 // are dequantised into a row-major tile and its rows written out.
 template <class E, int FMT>
 __global__ void __launch_bounds__(256) kv8_read_kernel(const __grid_constant__ ReadArgs a) {
-  __shared__ __align__(16) float tile[KV8_BLOCK * TS];
+  constexpr int STR = sizeof(E) == 2 ? T16 : TS;
+  __shared__ __align__(16) E tile[KV8_BLOCK * STR];
   const hq_kv8_cache& c = a.c;
   const int h = blockIdx.y >> 1, which = blockIdx.y & 1, b = blockIdx.z, tid = threadIdx.x;
   const int blk = a.start / KV8_BLOCK + blockIdx.x, p0 = blk * KV8_BLOCK;
@@ -294,77 +237,58 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const __grid_constant__ R
     len = 0;
   }
   const size_t bh = static_cast<size_t>(b) * c.Hkv + h;
-  E* out = static_cast<E*>(a.out[which]) + b * a.batch + h * a.head;
-  if (sizeof(E) == 2 && p0 + KV8_BLOCK <= len) {
-    // a complete block to 16-bit rows
-    uint16_t* tile16 = reinterpret_cast<uint16_t*>(tile);
+  if (p0 + KV8_BLOCK <= len) {
     const uint8_t* page = kv8_page(c, bh, blk);
     const float scale = *reinterpret_cast<const float*>(page + (which ? HQ_KV8_VSCALE : HQ_KV8_KSCALE));
-    const int lane = tid & 31;
     uint4 u[2];
 #pragma unroll
     for (int it = 0; it < 2; ++it) u[it] = reinterpret_cast<const uint4*>(page + (which ? HQ_KV8_V : 0))[it * 256 + tid];
 #pragma unroll
     for (int it = 0; it < 2; ++it) {
-      const int e = it * 256 + tid;
+      const int e = it * 256 + tid, lane = tid & 31;
       const uint32_t w[4] = {u[it].x, u[it].y, u[it].z, u[it].w};
-      uint32_t y[8];
+      float x[16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t p, q;
         kv8_half4<FMT>(w[i], p, q);
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p)), g = __half22float2(*reinterpret_cast<const __half2*>(&q));
-        y[2 * i] = to_pair<E>(f.x * scale, f.y * scale);
-        y[2 * i + 1] = to_pair<E>(g.x * scale, g.y * scale);
+        x[4 * i] = f.x * scale;
+        x[4 * i + 1] = f.y * scale;
+        x[4 * i + 2] = g.x * scale;
+        x[4 * i + 3] = g.y * scale;
       }
-      if (which) {
-        const int tt = e / 128, dq = e / 32 % 4;
-        uint16_t* row = tile16 + (tt * 16 + (lane >> 3 & 1) * 8 + (lane & 7)) * T16 + dq * 32 + (lane >> 4) * 8;
-        const uint32_t m0[4] = {y[0], y[1], y[2], y[3]}, m1[4] = {y[4], y[5], y[6], y[7]};
-        stmatrix_t4(row, m0);
-        stmatrix_t4(row + 16, m1);
-      } else {
-        uint4* row = reinterpret_cast<uint4*>(tile16 + (e / 64 * 8 + e / 4 % 8) * T16 + e / 32 % 2 * 64 + (e & 3) * 16);
-        row[0] = *reinterpret_cast<const uint4*>(y);
-        row[1] = *reinterpret_cast<const uint4*>(y + 4);
-      }
-    }
-    __syncthreads();
+      // K: 16 d of one token; V: tokens r, r + 1, r + 8, r + 9 of d, d + 8, d + 16, d + 24
+      const int rk = e / 64 * 8 + e / 4 % 8, dk = e / 32 % 2 * 64 + (e & 3) * 16;
+      const int tt = e / 128, dq = e / 32 % 4;
+      if constexpr (sizeof(E) == 2) {
+        uint32_t y[8];
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int e = it * 256 + tid, r = e / 16, p = p0 + r;
-      if (p >= a.start && p < a.start + a.n)
-        *reinterpret_cast<uint4*>(out + static_cast<int64_t>(p - a.start) * a.tok + e % 16 * 8) =
-            *reinterpret_cast<const uint4*>(tile16 + r * T16 + e % 16 * 8);
-    }
-    return;
-  }
-  if (p0 + KV8_BLOCK <= len) {
-    const uint8_t* page = kv8_page(c, bh, blk);
-    const float scale = *reinterpret_cast<const float*>(page + (which ? HQ_KV8_VSCALE : HQ_KV8_KSCALE));
-#pragma unroll
-    for (int it = 0; it < KV8_BLOCK * D / 16 / 256; ++it) {
-      const int e = it * 256 + tid;
-      const uint4 u = reinterpret_cast<const uint4*>(page + (which ? HQ_KV8_V : 0))[e];
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t lo, hi;
-        kv8_half4<FMT>(w[i], lo, hi);
-        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-        const float x[4] = {f0.x * scale, f0.y * scale, f1.x * scale, f1.y * scale};
+        for (int i = 0; i < 8; ++i) y[i] = to_pair<E>(x[2 * i], x[2 * i + 1]);
         if (which) {
-          const int r = e / 128 * 16 + (e & 3) * 2, d = e / 32 % 4 * 32 + e / 4 % 8 + 8 * i;
-          float* t = tile + r * TS + d;
-          t[0] = x[0];
-          t[TS] = x[1];
-          t[8 * TS] = x[2];
-          t[9 * TS] = x[3];
+          E* row = tile + (tt * 16 + (lane >> 3 & 1) * 8 + (lane & 7)) * STR + dq * 32 + (lane >> 4) * 8;
+          const uint32_t m0[4] = {y[0], y[1], y[2], y[3]}, m1[4] = {y[4], y[5], y[6], y[7]};
+          stmatrix_t4(row, m0);
+          stmatrix_t4(row + 16, m1);
         } else {
-          const int r = e / 64 * 8 + e / 4 % 8, d = e / 32 % 2 * 64 + (e & 3) * 16 + 4 * i;
-          *reinterpret_cast<float4*>(tile + r * TS + d) = make_float4(x[0], x[1], x[2], x[3]);
+          uint4* row = reinterpret_cast<uint4*>(tile + rk * STR + dk);
+          row[0] = make_uint4(y[0], y[1], y[2], y[3]);
+          row[1] = make_uint4(y[4], y[5], y[6], y[7]);
         }
+      } else if (which) {
+        const int r = tt * 16 + (e & 3) * 2, d = dq * 32 + e / 4 % 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          E* t = tile + r * STR + d + 8 * i;
+          t[0] = x[4 * i];
+          t[STR] = x[4 * i + 1];
+          t[8 * STR] = x[4 * i + 2];
+          t[9 * STR] = x[4 * i + 3];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(tile + rk * STR + dk + 4 * i) = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
       }
     }
   } else if (p0 < len) {
@@ -372,18 +296,18 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const __grid_constant__ R
     const float* sc = c.tail_scale + (bh * 2 + which) * HQ_KV8_TAIL + (blk & 1) * KV8_BLOCK;
     for (int e = tid; e < (len - p0) * D; e += 256) {
       const int r = e / D, d = e % D;
-      tile[r * TS + d] = __half2float(__ushort_as_half(t[which ? HQ_KV8_V_INDEX(r, d) : HQ_KV8_K_INDEX(r, d)])) * sc[r];
+      tile[r * STR + d] = from_float<E>(__half2float(__ushort_as_half(t[which ? HQ_KV8_V_INDEX(r, d) : HQ_KV8_K_INDEX(r, d)])) * sc[r]);
     }
   }
   __syncthreads();
+  E* out = static_cast<E*>(a.out[which]) + b * a.batch + h * a.head;
   constexpr int V = 16 / sizeof(E);
-  for (int e = tid; e < KV8_BLOCK * D / V; e += 256) {
-    const int r = e / (D / V), d = e % (D / V) * V, p = p0 + r;
-    if (p < a.start || p >= a.start + a.n || (p >= len && !a.zero_rest)) continue;
-    E y[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) y[i] = from_float<E>(p < len ? tile[r * TS + d + i] : 0.f);
-    *reinterpret_cast<uint4*>(out + static_cast<int64_t>(p - a.start) * a.tok + d) = *reinterpret_cast<const uint4*>(y);
+  for (int it = 0; it < KV8_BLOCK * D / V / 256; ++it) {
+    const int e = it * 256 + tid, r = e / (D / V), d = e % (D / V) * V, p = p0 + r;
+    if (p < a.start || p >= a.start + a.n || (p >= len && !a.zero_rest)) continue;
+    *reinterpret_cast<uint4*>(out + static_cast<int64_t>(p - a.start) * a.tok + d) =
+        p < len ? *reinterpret_cast<const uint4*>(tile + r * STR + d) : make_uint4(0u, 0u, 0u, 0u);
   }
 }
 

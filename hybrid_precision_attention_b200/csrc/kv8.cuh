@@ -12,6 +12,34 @@ namespace hq {
 constexpr int KV8_BLOCK = 64;                      // positions of a page
 constexpr int KV8_COPY = HQ_KV8_KSCALE + 16;       // bytes of a page that are copied: codes, scales, padding to 16
 
+// ----------------------------------------------------------------- pairs of floats in one register pair
+
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f32x2_split(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(float x) { return x; }
@@ -107,40 +135,37 @@ __device__ __forceinline__ float kv8_scale(uint32_t amax_bits, int fmt) {
 // overflowing ranges: 2^-80 < scale < 2^80 (remainders that underflow then belong to
 // quotients that round to zero).  Three operations against a division's dozen.
 __device__ __forceinline__ bool kv8_scale_plain(float scale) { return scale > 0x1p-80f && scale < 0x1p80f; }
-__device__ __forceinline__ float kv8_quotient(float x, float scale, float r) {
-  const float q = x * r;
-  return fmaf(fmaf(-q, scale, x), r, q);
+__device__ __forceinline__ float2 kv8_quotients(float2 x, uint64_t minus_scale2, uint64_t r2) {
+  const uint64_t v = f32x2(x.x, x.y), q = f32x2_mul(v, r2);
+  return f32x2_split(f32x2_fma(f32x2_fma(q, minus_scale2, v), r2, q));
 }
-// codes of four quotients, lowest byte first
+// codes of four quotients (|y| <= 127.5 for int8), lowest byte first
 template <int FMT>
 __device__ __forceinline__ uint32_t kv8_round4(const float (&y)[4]) {
-  if (FMT == HQ_KV8_E4M3) {
+  if constexpr (FMT == HQ_KV8_E4M3) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
     return lo | hi << 16;
-  }
-  // |y| < 127.5 (amax / scale is 127 up to rounding): the sum with 1.5 * 2^23 is rounded
-  // to an integer, ties to even, and its low byte is the code
-  uint32_t z[4];
+  } else {
+    // |y| < 127.5 (amax / scale is 127 up to rounding): the sum with 1.5 * 2^23 is rounded
+    // to an integer, ties to even, and its low byte is the code
+    uint32_t z[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) z[i] = __float_as_uint(y[i] + 12582912.0f);
-  return prmt(prmt(z[0], z[1], 0x0040u), prmt(z[2], z[3], 0x0040u), 0x5410u);
+    for (int i = 0; i < 4; ++i) z[i] = __float_as_uint(y[i] + 12582912.0f);
+    return prmt(prmt(z[0], z[1], 0x0040u), prmt(z[2], z[3], 0x0040u), 0x5410u);
+  }
 }
 // codes of four values, lowest byte first; `scale` NaN: zeros
 template <int FMT>
 __device__ __forceinline__ uint32_t kv8_codes4(const float (&x)[4], float scale) {
   float y[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) y[i] = __fdiv_rn(x[i], scale);
-  if (FMT == HQ_KV8_E4M3) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
-    return scale == scale ? (lo | hi << 16) : 0u;
+  for (int i = 0; i < 4; ++i) {
+    y[i] = __fdiv_rn(x[i], scale);
+    // a subnormal scale may be far from amax / 127
+    if (FMT == HQ_KV8_INT8) y[i] = fminf(fmaxf(y[i], -127.0f), 127.0f);
   }
-  uint32_t r = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r |= (static_cast<uint32_t>(min(max(__float2int_rn(y[i]), -127), 127)) & 0xFFu) << (8 * i);
-  return scale == scale ? r : 0u;
+  return scale == scale ? kv8_round4<FMT>(y) : 0u;
 }
 
 // four codes -> two pairs of fp16, exact in both formats

@@ -199,6 +199,20 @@ def test_values_at_the_edges_of_the_types():
             p.check_stored()
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_scales_at_the_ends_of_float32(fmt):
+    """bf16 blocks whose scale is subnormal (the quotients pass the format's largest value and are clipped), tiny, and
+    as large as the type allows: codes by the division of the definition."""
+    p = Pair(1, 1, 512, fmt, "bf16", seed=30)
+    g = torch.Generator().manual_seed(31)
+    x = torch.randn(384, 1, 128, generator=g, dtype=torch.float64)
+    for i, s in enumerate((1e-39, 3e-38, 2.0 ** -100, 2.0 ** 90, 1e37, 1.0)):
+        x[64 * i:64 * i + 64] *= s
+    x = x.to(torch.bfloat16)
+    p.append([384], k=x, v=-x)
+    p.check_stored()
+
+
 def test_not_finite_rows_mark_their_block():
     p = Pair(2, 2, 256, "e4m3", "f16", seed=6)
     k, v = p.rows(200 + 70), p.rows(200 + 70)
