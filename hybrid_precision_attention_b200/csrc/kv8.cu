@@ -60,121 +60,138 @@ __device__ __forceinline__ uint32_t to_pair(float x, float y) {
   return w;
 }
 
-// One CTA per (block that new tokens touch, kv head, K or V).  Sequence b's
-// blocks are CTAs s_b, s_b + 1, .. with s_b = cu[b] / 64 + 2 b: n tokens touch
-// at most n / 64 + 2 blocks, so the ranges do not overlap and the host needs to
-// know N and B only.
+// One CTA per (block that new tokens touch, kv head), K and V: 32 KB of rows in
+// flight behind one chain of look-ups.  Sequence b's blocks are CTAs s_b, s_b + 1,
+// .. with s_b = cu[b] / 64 + 2 b: n tokens touch at most n / 64 + 2 blocks, so the
+// ranges do not overlap and the host needs to know N and B only.
 template <class E, int FMT>
-__global__ void __launch_bounds__(256, 5) kv8_append_kernel(const __grid_constant__ AppendArgs a) {
-  __shared__ __align__(16) uint16_t tile[KV8_BLOCK * T16];
+__global__ void __launch_bounds__(256, 4) kv8_append_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ __align__(16) uint16_t tiles[2][KV8_BLOCK * T16];
   __shared__ int sh_b;
-  __shared__ uint32_t sh_amax;
+  __shared__ Kv8Seq sh_s;
+  __shared__ uint32_t sh_amax[2];
   const hq_kv8_cache& c = a.c;
-  const int h = blockIdx.y, which = blockIdx.z, tid = threadIdx.x, item = blockIdx.x;
+  const int h = blockIdx.y, tid = threadIdx.x, item = blockIdx.x;
   if (tid == 0) {
     sh_b = -1;
-    sh_amax = 0;
+    sh_amax[0] = sh_amax[1] = 0;
   }
   __syncthreads();
   for (int b = tid; b < c.B; b += 256) {
-    const int lo = a.cu[b] / KV8_BLOCK + 2 * b, hi = a.cu[b + 1] / KV8_BLOCK + 2 * b + 2;
-    if (lo <= item && item < hi) sh_b = b;  // one b at most when cu ascends; any of them otherwise
+    // every sequence's numbers are read at once; one CTA says which sequences are skipped
+    Kv8Seq s;
+    const bool fits = kv8_seq(c, a.cu, a.kv_len, a.N, a.N, b, item == 0 && h == 0, s);
+    const int at = s.row0 / KV8_BLOCK + 2 * b;
+    if (fits && s.n > 0 && at <= item && item <= at + s.n / KV8_BLOCK + 1) {  // one b at most where cu ascends
+      sh_b = b;
+      sh_s = s;
+    }
   }
   __syncthreads();
   const int b = sh_b;
-  Kv8Seq s;
-  if (item == 0 && h == 0 && which == 0)  // one CTA says which sequences are skipped
-    for (int i = tid; i < c.B; i += 256) kv8_seq(c, a.cu, a.kv_len, a.N, a.N, i, true, s);
-  if (b < 0 || !kv8_seq(c, a.cu, a.kv_len, a.N, a.N, b, false, s) || s.n == 0) return;
+  if (b < 0) return;
+  const Kv8Seq s = sh_s;
   const int first_blk = s.first / KV8_BLOCK, last_blk = (s.len - 1) / KV8_BLOCK;
   const int blk = first_blk + item - (s.row0 / KV8_BLOCK + 2 * b);
-  if (blk > last_blk) return;
+  if (blk < first_blk || blk > last_blk) return;
   const size_t bh = static_cast<size_t>(b) * c.Hkv + h;
-  const E* src = static_cast<const E*>(a.x[which]) + static_cast<int64_t>(s.row0 - s.first) * a.tok[which] +
-                 h * a.head[which];  // + position * tok: that position's row
-  uint16_t* tail = (which ? c.tail_v : c.tail_k) + bh * HQ_KV8_TAIL * D;
-  float* tail_scale = c.tail_scale + (bh * 2 + which) * HQ_KV8_TAIL;
   const int p0 = blk * KV8_BLOCK, half = blk & 1;
+  // position p's row is src + p * tok
+  auto source = [&](int which) {
+    return static_cast<const E*>(a.x[which]) + static_cast<int64_t>(s.row0 - s.first) * a.tok[which] + h * a.head[which];
+  };
+  auto tail_of = [&](int which) { return (which ? c.tail_v : c.tail_k) + bh * HQ_KV8_TAIL * D; };
+  auto scales_of = [&](int which) { return c.tail_scale + (bh * 2 + which) * HQ_KV8_TAIL; };
 
   if (p0 + KV8_BLOCK <= s.len) {
-    // the block is complete: its rows into the tile, new ones from the input,
+    // the block is complete: its rows into the tiles, new ones from the input,
     // earlier ones from the tail (whose values are numbers of E as they were)
     const long long idx = kv8_page_index(c, bh, blk);
-    uint4 v[4];
+    uint4 v[2][4];
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int e = it * 256 + tid, p = p0 + e / 16, d = e % 16 * 8;
-      if (p >= s.first) {
-        v[it] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(p) * a.tok[which] + d);
-      } else {
-        const int r = p - p0;
-        const float sc = tail_scale[half * KV8_BLOCK + r];
-        const uint16_t* t = tail + half * KV8_BLOCK * D;
-        E x[8];
+    for (int which = 0; which < 2; ++which) {
+      const E* src = source(which);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          x[i] = from_float<E>(__half2float(__ushort_as_half(t[which ? HQ_KV8_V_INDEX(r, d + i) : HQ_KV8_K_INDEX(r, d + i)])) * sc);
-        v[it] = *reinterpret_cast<const uint4*>(x);
+      for (int it = 0; it < 4; ++it) {
+        const int e = it * 256 + tid, p = p0 + e / 16, d = e % 16 * 8;
+        if (p >= s.first) {
+          v[which][it] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(p) * a.tok[which] + d);
+        } else {
+          const int r = p - p0;
+          const float sc = scales_of(which)[half * KV8_BLOCK + r];
+          const uint16_t* t = tail_of(which) + half * KV8_BLOCK * D;
+          E x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            x[i] = from_float<E>(__half2float(__ushort_as_half(t[which ? HQ_KV8_V_INDEX(r, d + i) : HQ_KV8_K_INDEX(r, d + i)])) * sc);
+          v[which][it] = *reinterpret_cast<const uint4*>(x);
+        }
       }
     }
-    // magnitudes compare as integers: the 15 bits of each half
-    uint32_t hi = 0, lo = 0;
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int e = it * 256 + tid;
-      const uint32_t w[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
+    for (int which = 0; which < 2; ++which) {
+      // magnitudes compare as integers: the 15 bits of each half
+      uint32_t hi = 0, lo = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        hi = max(hi, w[i] & 0x7fff0000u);
-        lo = max(lo, w[i] & 0x7fffu);
+      for (int it = 0; it < 4; ++it) {
+        const int e = it * 256 + tid;
+        const uint32_t w[4] = {v[which][it].x, v[which][it].y, v[which][it].z, v[which][it].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          hi = max(hi, w[i] & 0x7fff0000u);
+          lo = max(lo, w[i] & 0x7fffu);
+        }
+        *reinterpret_cast<uint4*>(tiles[which] + e / 16 * T16 + e % 16 * 8) = v[which][it];
       }
-      *reinterpret_cast<uint4*>(tile + e / 16 * T16 + e % 16 * 8) = v[it];
+      const uint32_t top = __reduce_max_sync(0xffffffffu, max(hi >> 16, lo));
+      if ((tid & 31) == 0) atomicMax(&sh_amax[which], top);
     }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, max(hi >> 16, lo));
-    if ((tid & 31) == 0) atomicMax(&sh_amax, top);
     __syncthreads();
-    const float scale = kv8_scale(__float_as_uint(pair_of<E>(sh_amax).x), FMT);
     if (idx < 0) {
       if (tid == 0) kv8_err(c, b, HQ_DEVERR_PAGE);
     } else {
       uint8_t* page = c.pages + static_cast<size_t>(idx) * HQ_KV8_PAGE_BYTES;
-      const bool plain = kv8_scale_plain(scale);
-      const float r = 1.0f / scale;
-      const uint64_t minus2 = f32x2(-scale, -scale), r2 = f32x2(r, r);
       const int lane = tid & 31;
 #pragma unroll
-      for (int it = 0; it < 2; ++it) {
-        const int e = it * 256 + tid;  // 16-byte chunk of the page's codes
-        uint32_t h[8], w[4];           // its elements: two of a word, four of a code word
-        if (which) {
-          // tokens 16 tt .. + 15, d 32 dq ..: matrices of 8 tokens x 8 d
-          const int tt = e / 128, dq = e / 32 % 4;
-          const uint16_t* row = tile + (tt * 16 + (lane >> 3 & 1) * 8 + (lane & 7)) * T16 + dq * 32 + (lane >> 4) * 8;
-          uint32_t m[4];
-          ldmatrix_t4(m, row);         // (tokens 0-7, 8-15) of d 0-7, then of d 8-15
-          h[0] = m[0], h[1] = m[1], h[2] = m[2], h[3] = m[3];
-          ldmatrix_t4(m, row + 16);
-          h[4] = m[0], h[5] = m[1], h[6] = m[2], h[7] = m[3];
-        } else {
-          const uint4* row = reinterpret_cast<const uint4*>(tile + (e / 64 * 8 + e / 4 % 8) * T16 + e / 32 % 2 * 64 + (e & 3) * 16);
-          *reinterpret_cast<uint4*>(h) = row[0];
-          *reinterpret_cast<uint4*>(h + 4) = row[1];
-        }
+      for (int which = 0; which < 2; ++which) {
+        const float scale = kv8_scale(__float_as_uint(pair_of<E>(sh_amax[which]).x), FMT);
+        const bool plain = kv8_scale_plain(scale);
+        const float r = 1.0f / scale;
+        const uint64_t minus2 = f32x2(-scale, -scale), r2 = f32x2(r, r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x = pair_of<E>(h[2 * i]), y = pair_of<E>(h[2 * i + 1]);
-          if (plain) {
-            const float2 qx = kv8_quotients(x, minus2, r2), qy = kv8_quotients(y, minus2, r2);
-            const float z[4] = {qx.x, qx.y, qy.x, qy.y};
-            w[i] = kv8_round4<FMT>(z);
+        for (int it = 0; it < 2; ++it) {
+          const int e = it * 256 + tid;  // 16-byte chunk of the page's codes
+          uint32_t x[8], w[4];           // its elements: two of a word, four of a code word
+          if (which) {
+            // tokens 16 tt .. + 15, d 32 dq ..: matrices of 8 tokens x 8 d
+            const int tt = e / 128, dq = e / 32 % 4;
+            const uint16_t* row = tiles[1] + (tt * 16 + (lane >> 3 & 1) * 8 + (lane & 7)) * T16 + dq * 32 + (lane >> 4) * 8;
+            uint32_t m[4];
+            ldmatrix_t4(m, row);         // (tokens 0-7, 8-15) of d 0-7, then of d 8-15
+            x[0] = m[0], x[1] = m[1], x[2] = m[2], x[3] = m[3];
+            ldmatrix_t4(m, row + 16);
+            x[4] = m[0], x[5] = m[1], x[6] = m[2], x[7] = m[3];
           } else {
-            const float z[4] = {x.x, x.y, y.x, y.y};
-            w[i] = kv8_codes4<FMT>(z, scale);
+            const uint4* row = reinterpret_cast<const uint4*>(tiles[0] + (e / 64 * 8 + e / 4 % 8) * T16 + e / 32 % 2 * 64 + (e & 3) * 16);
+            *reinterpret_cast<uint4*>(x) = row[0];
+            *reinterpret_cast<uint4*>(x + 4) = row[1];
           }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 y = pair_of<E>(x[2 * i]), z = pair_of<E>(x[2 * i + 1]);
+            if (plain) {
+              const float2 qy = kv8_quotients(y, minus2, r2), qz = kv8_quotients(z, minus2, r2);
+              const float q[4] = {qy.x, qy.y, qz.x, qz.y};
+              w[i] = kv8_round4<FMT>(q);
+            } else {
+              const float q[4] = {y.x, y.y, z.x, z.y};
+              w[i] = kv8_codes4<FMT>(q, scale);
+            }
+          }
+          reinterpret_cast<uint4*>(page + (which ? HQ_KV8_V : 0))[e] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        reinterpret_cast<uint4*>(page + (which ? HQ_KV8_V : 0))[e] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (tid == 0) *reinterpret_cast<float*>(page + (which ? HQ_KV8_VSCALE : HQ_KV8_KSCALE)) = scale;
       }
-      if (tid == 0) *reinterpret_cast<float*>(page + (which ? HQ_KV8_VSCALE : HQ_KV8_KSCALE)) = scale;
     }
   }
   // The tail's half of this block's parity is written by one CTA alone, the
@@ -185,32 +202,44 @@ __global__ void __launch_bounds__(256, 5) kv8_append_kernel(const __grid_constan
   __syncthreads();
   const int t0 = (last_blk - ((last_blk - blk) & 1)) * KV8_BLOCK;
   const int warp = tid / 32, lane = tid % 32;
-  for (int p = max(t0, s.first) + warp; p < min(t0 + KV8_BLOCK, s.len); p += 8) {
-    const E* x = src + static_cast<int64_t>(p) * a.tok[which] + lane * 4;
-    E e[4];
-    *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(x);
-    uint32_t amax = 0;
+  const int begin = max(t0, s.first), rows = min(t0 + KV8_BLOCK, s.len) - begin;
+  for (int i0 = warp; i0 < 2 * rows; i0 += 4 * 8) {  // K and V rows in turn, four of a warp in flight
+    uint2 in[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) amax = max(amax, __float_as_uint(to_float(e[i])) & 0x7fffffffu);
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    float sc = 1.0f;
-    if (amax >= 0x7f800000u) {
-      sc = __uint_as_float(0x7fc00000u);
-    } else if (IsBf16<E>::value && amax != 0) {
-      // the power of two that brings amax to [2^14, 2^15), itself a normal number
-      const int ex = max(static_cast<int>(amax >> 23) - 127 - 14, -126);
-      sc = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + 8 * q, which = i & 1;
+      if (i < 2 * rows)
+        in[q] = *reinterpret_cast<const uint2*>(source(which) + static_cast<int64_t>(begin + i / 2) * a.tok[which] + lane * 4);
     }
-    uint16_t* t = tail + half * KV8_BLOCK * D;
-    const int r = p % KV8_BLOCK;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int d = lane * 4 + i;
-      // the division by a power of two is exact, the rounding is to fp16 (exact for fp16 rows)
-      const __half v = sc == sc ? __float2half_rn(to_float(e[i]) / sc) : __float2half_rn(0.f);
-      t[which ? HQ_KV8_V_INDEX(r, d) : HQ_KV8_K_INDEX(r, d)] = __half_as_ushort(v);
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + 8 * q, which = i & 1, p = begin + i / 2;
+      if (i >= 2 * rows) break;
+      E e[4];
+      *reinterpret_cast<uint2*>(e) = in[q];
+      uint32_t amax = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) amax = max(amax, __float_as_uint(to_float(e[j])) & 0x7fffffffu);
+      amax = __reduce_max_sync(0xffffffffu, amax);
+      float sc = 1.0f;
+      if (amax >= 0x7f800000u) {
+        sc = __uint_as_float(0x7fc00000u);
+      } else if (IsBf16<E>::value && amax != 0) {
+        // the power of two that brings amax to [2^14, 2^15), itself a normal number
+        const int ex = max(static_cast<int>(amax >> 23) - 127 - 14, -126);
+        sc = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+      }
+      uint16_t* t = tail_of(which) + half * KV8_BLOCK * D;
+      const int r = p % KV8_BLOCK;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int d = lane * 4 + j;
+        // the division by a power of two is exact, the rounding is to fp16 (exact for fp16 rows)
+        const __half y = sc == sc ? __float2half_rn(to_float(e[j]) / sc) : __float2half_rn(0.f);
+        t[which ? HQ_KV8_V_INDEX(r, d) : HQ_KV8_K_INDEX(r, d)] = __half_as_ushort(y);
+      }
+      if (lane == 0) scales_of(which)[p % HQ_KV8_TAIL] = sc;
     }
-    if (lane == 0) tail_scale[p % HQ_KV8_TAIL] = sc;
   }
 }
 
@@ -343,7 +372,7 @@ hq_status hq_kv8_append(const hq_kv8_cache* c, int32_t dtype, const void* k, int
   if (N == 0) return HQ_OK;
   if (!hq::aligned16(k) || !hq::aligned16(v) || (k_tok | k_head | v_tok | v_head) % 8) return HQ_ERR_INVALID;
   hq::AppendArgs a = {*c, {k, v}, {k_tok, v_tok}, {k_head, v_head}, N, cu, kv_len};
-  const dim3 grid(static_cast<unsigned>(N) / hq::KV8_BLOCK + 2u * c->B, c->Hkv, 2);
+  const dim3 grid(static_cast<unsigned>(N) / hq::KV8_BLOCK + 2u * c->B, c->Hkv);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == HQ_F16) {
     if (c->fmt == HQ_KV8_E4M3) hq::kv8_append_kernel<__half, HQ_KV8_E4M3><<<grid, 256, 0, s>>>(a);
