@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(const __grid_constan
   __shared__ uint32_t sh_amax[2];
   const hq_kv8_cache& c = a.c;
   const int h = blockIdx.y, tid = threadIdx.x, item = blockIdx.x;
+  chained();
   if (tid == 0) {
     sh_b = -1;
     sh_amax[0] = sh_amax[1] = 0;
@@ -260,6 +261,7 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const __grid_constant__ R
   const hq_kv8_cache& c = a.c;
   const int h = blockIdx.y >> 1, which = blockIdx.y & 1, b = blockIdx.z, tid = threadIdx.x;
   const int blk = a.start / KV8_BLOCK + blockIdx.x, p0 = blk * KV8_BLOCK;
+  chained();
   int len = a.kv_len[b];
   if (len > c.cap || len < 0) {
     if (tid == 0) kv8_err(c, b, len < 0 ? HQ_DEVERR_ROWS : HQ_DEVERR_CAPACITY);
@@ -374,14 +376,11 @@ hq_status hq_kv8_append(const hq_kv8_cache* c, int32_t dtype, const void* k, int
   hq::AppendArgs a = {*c, {k, v}, {k_tok, v_tok}, {k_head, v_head}, N, cu, kv_len};
   const dim3 grid(static_cast<unsigned>(N) / hq::KV8_BLOCK + 2u * c->B, c->Hkv);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == HQ_F16) {
-    if (c->fmt == HQ_KV8_E4M3) hq::kv8_append_kernel<__half, HQ_KV8_E4M3><<<grid, 256, 0, s>>>(a);
-    else hq::kv8_append_kernel<__half, HQ_KV8_INT8><<<grid, 256, 0, s>>>(a);
-  } else {
-    if (c->fmt == HQ_KV8_E4M3) hq::kv8_append_kernel<__nv_bfloat16, HQ_KV8_E4M3><<<grid, 256, 0, s>>>(a);
-    else hq::kv8_append_kernel<__nv_bfloat16, HQ_KV8_INT8><<<grid, 256, 0, s>>>(a);
-  }
-  return hq::cuda_status(cudaGetLastError(), "kv8 append launch");
+  auto go = [&](auto kernel) { return hq::cuda_status(hq::launch_chained(kernel, grid, 256, 0, s, a), "kv8 append launch"); };
+  const bool f8 = c->fmt == HQ_KV8_E4M3;
+  if (dtype == HQ_F16)
+    return f8 ? go(hq::kv8_append_kernel<__half, HQ_KV8_E4M3>) : go(hq::kv8_append_kernel<__half, HQ_KV8_INT8>);
+  return f8 ? go(hq::kv8_append_kernel<__nv_bfloat16, HQ_KV8_E4M3>) : go(hq::kv8_append_kernel<__nv_bfloat16, HQ_KV8_INT8>);
 }
 
 hq_status hq_kv8_read(const hq_kv8_cache* c, int32_t dtype, const int32_t* kv_len, int32_t start, int32_t n, void* k_out,
@@ -395,15 +394,15 @@ hq_status hq_kv8_read(const hq_kv8_cache* c, int32_t dtype, const int32_t* kv_le
   hq::ReadArgs a = {*c, kv_len, start, n, zero_rest, {k_out, v_out}, o_batch, o_head, o_tok};
   const dim3 grid((start + n - 1) / hq::KV8_BLOCK - start / hq::KV8_BLOCK + 1, 2 * c->Hkv, c->B);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto go = [&](auto fmt) {
+  auto go = [&](auto kernel) { return hq::cuda_status(hq::launch_chained(kernel, grid, 256, 0, s, a), "kv8 read launch"); };
+  auto form = [&](auto fmt) {
     constexpr int F = decltype(fmt)::value;
-    if (dtype == HQ_F16) hq::kv8_read_kernel<__half, F><<<grid, 256, 0, s>>>(a);
-    else if (dtype == HQ_BF16) hq::kv8_read_kernel<__nv_bfloat16, F><<<grid, 256, 0, s>>>(a);
-    else hq::kv8_read_kernel<float, F><<<grid, 256, 0, s>>>(a);
+    if (dtype == HQ_F16) return go(hq::kv8_read_kernel<__half, F>);
+    if (dtype == HQ_BF16) return go(hq::kv8_read_kernel<__nv_bfloat16, F>);
+    return go(hq::kv8_read_kernel<float, F>);
   };
-  if (c->fmt == HQ_KV8_E4M3) go(std::integral_constant<int, HQ_KV8_E4M3>{});
-  else go(std::integral_constant<int, HQ_KV8_INT8>{});
-  return hq::cuda_status(cudaGetLastError(), "kv8 read launch");
+  if (c->fmt == HQ_KV8_E4M3) return form(std::integral_constant<int, HQ_KV8_E4M3>{});
+  return form(std::integral_constant<int, HQ_KV8_INT8>{});
 }
 
 }  // extern "C"

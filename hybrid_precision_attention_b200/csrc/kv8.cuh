@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+#include <cuda_runtime.h>
 
 #include "common.cuh"
 
@@ -60,6 +61,29 @@ template <>
 struct IsBf16<__nv_bfloat16> {
   static constexpr bool value = true;
 };
+
+// Launch with programmatic dependent launch: the grid may start while the one before
+// it in the stream drains.  Every CTA of such a kernel calls chained() before it
+// touches memory: it waits until the grids before have completed, then lets the next
+// one start in turn.  (Kernels of 2 to 20 us, one behind another: 1 to 2 us less each.)
+template <class K, class A>
+inline cudaError_t launch_chained(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, const A& arg) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, arg);
+}
+__device__ __forceinline__ void chained() {
+  griddep_wait();
+  griddep_launch_dependents();
+}
 
 // Pool index of page j of (b, kv head) bh, -1 when the table's entry lies outside the pool.
 __device__ __forceinline__ long long kv8_page_index(const hq_kv8_cache& c, size_t bh, int j) {

@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
     fence_mbar_init();
   }
   if (threadIdx.x < 2) flags[threadIdx.x] = 0;
+  chained();
   // prefix[b]: units (of one task) of the sequences before b, in the low half,
   // and those of them that have blocks, in the high half
   uint64_t carry = 0;
@@ -782,8 +783,8 @@ hq_status launch(Kv8AttnArgs& a, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return cuda_fail(e, "kv8 attention setup");
   // units are counted in 32 bits
   if (static_cast<double>(a.c.B) * a.c.Hkv * (a.c.cap / KV8_BLOCK + TASK_UNITS) >= 4e9) return HQ_ERR_UNSUPPORTED;
-  kv8_attn_kernel<E, FMT, NB, W><<<C::CTAS * sms, C::THREADS, C::FIXED + a.c.B * 8, st>>>(a);
-  return cuda_status(cudaGetLastError(), "kv8 attention launch");
+  return cuda_status(launch_chained(kv8_attn_kernel<E, FMT, NB, W>, dim3(C::CTAS * sms), C::THREADS, C::FIXED + a.c.B * 8, st, a),
+                     "kv8 attention launch");
 }
 
 // Rows of a kv head, in eights.

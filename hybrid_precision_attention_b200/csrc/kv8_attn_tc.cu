@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // the roles' branches are uniform
 
   // ---------------------------------------------------------------- plan
+  chained();
   uint32_t carry = 0;
   for (int b0 = 0; b0 < B; b0 += THREADS) {
     const int b = b0 + threadIdx.x;
@@ -858,8 +859,7 @@ hq_status launch(const Kv8AttnArgs& a, int sms, cudaStream_t st) {
   // units are counted in 32 bits
   const double groups = static_cast<double>(a.G) * a.max_new / (NT * TR) + 1;
   if (groups * a.c.B * a.c.Hkv * (a.c.cap / KV8_BLOCK + TASK_UNITS<NT>) >= 4e9) return HQ_ERR_UNSUPPORTED;
-  kv8_attn_tc_kernel<E, FMT, NT><<<sms, THREADS, L::BYTES, st>>>(a);
-  return cuda_status(cudaGetLastError(), "kv8 attention launch");
+  return cuda_status(launch_chained(kv8_attn_tc_kernel<E, FMT, NT>, dim3(sms), THREADS, L::BYTES, st, a), "kv8 attention launch");
 }
 
 template <class E, int FMT>

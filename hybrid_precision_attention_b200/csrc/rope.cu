@@ -126,6 +126,7 @@ __device__ __forceinline__ E* row_of(const RopeArgs& a, int h, long long b, long
 
 template <class E, int V, bool HALF>
 __global__ void __launch_bounds__(256) rope_few_kernel(const __grid_constant__ RopeArgs a) {
+  chained();
   const int per = a.PG + a.CG, g = threadIdx.x % per;
   const long long tok = static_cast<long long>(blockIdx.x) * (blockDim.x / per) + threadIdx.x / per;
   const int h = blockIdx.y, z = h >= a.H0;
@@ -153,6 +154,7 @@ constexpr int HEADS = 8;     // heads of a thread, where there are threads enoug
 template <class E, int V, bool HALF>
 __global__ void __launch_bounds__(256) rope_many_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float2 table[256 * V];   // (cos, sin) of [token of the block][pair]
+  chained();
   const int per = a.PG + a.CG, slots = 256 / per, pairs = a.rot / 2;
   const int g = threadIdx.x % per, slot = threadIdx.x / per;
   const int k = slot / a.lanes, lane = slot - k * a.lanes;  // token of the block; the thread's heads: lane, lane + lanes, ..
@@ -223,12 +225,11 @@ hq_status launch_v(RopeArgs& a, cudaStream_t st) {
   if (few > 0x7fffffffll || many > 0x7fffffffll) return HQ_ERR_UNSUPPORTED;
   // from two blocks an SM on the heads share their sines; fewer leave SMs idle
   if (many >= 2 * 148) {
-    rope_many_kernel<E, V, HALF><<<static_cast<unsigned>(many), 256, 0, st>>>(a);
+    return cuda_status(launch_chained(rope_many_kernel<E, V, HALF>, dim3(static_cast<unsigned>(many)), 256, 0, st, a), "rope launch");
   } else {
     if (a.H > 65535) return HQ_ERR_UNSUPPORTED;
-    rope_few_kernel<E, V, HALF><<<dim3(static_cast<unsigned>(few), a.H), 256, 0, st>>>(a);
+    return cuda_status(launch_chained(rope_few_kernel<E, V, HALF>, dim3(static_cast<unsigned>(few), a.H), 256, 0, st, a), "rope launch");
   }
-  return cuda_status(cudaGetLastError(), "rope launch");
 }
 
 template <class E, bool HALF>
