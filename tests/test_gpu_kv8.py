@@ -603,6 +603,123 @@ def test_refusals_of_the_binding():
     assert not any(c.errors())
 
 
+# ----------------------------------------------------------------------------- where the kernels change
+
+@pytest.mark.parametrize("fmt,dtype", FORMS)
+@pytest.mark.parametrize("G,n", [(8, 3), (5, 5), (2, 13), (8, 16), (1, 129), (3, 43), (2, 128), (1, 257), (16, 17), (7, 40)])
+def test_row_counts_around_the_kernels_borders(fmt, dtype, G, n):
+    """24 and 25 rows of a kv head (the tcgen05 kernel begins), 128 and 129 (its second row tile), 256 and more (further
+    tasks), with sequences of fewer rows beside."""
+    p = Pair(3, 2, 640, fmt, dtype, seed=32)
+    p.append([600, max(n, 129), 300])
+    p.attend(G, [n, n, max(1, n // 3)])
+
+
+@pytest.mark.parametrize("window", [1, 30, 64, 129, 500])
+def test_window_of_many_rows(window):
+    p = Pair(2, 1, 1024, "int8", "f16", seed=33)
+    p.append([1000, 333])
+    p.attend(8, [100, 30], window=window)
+    p.attend(2, [50, 17], window=window)
+
+
+def test_many_rows_over_a_long_context():
+    """Pieces of one task on many CTAs, one and two row tiles."""
+    p = Pair(1, 1, 20096, "e4m3", "bf16", seed=34)
+    p.append([20001])
+    p.attend(4, [10])
+    p.attend(4, [40], window=15000)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_many_rows_and_blocks_whose_scales_lie_far_apart(dtype):
+    p = Pair(1, 1, 512, "e4m3", dtype, seed=35)
+    k, v = p.rows(400).double(), p.rows(400).double()
+    q = torch.zeros(8, 8, 128, dtype=torch.float64)
+    q[:, :, 0] = torch.tensor([6.0, -6.0, 3.0, 0.0, 1.0, -1.0, 0.1, -3.0])
+    k[:, 0, 0] = torch.where(torch.arange(400) // 64 % 2 == 0, 30.0, -30.0)
+    v = v * torch.where(torch.arange(400) // 64 % 2 == 0, 2.0 ** -13, 2.0 ** 12)[:, None, None]
+    p.append([400], k=k.to(TYPES[dtype]), v=v.to(TYPES[dtype]))
+    p.attend(8, [8], q=q.to(TYPES[dtype]))
+    p.attend(8, [8], q=(-q).to(TYPES[dtype]), window=100)
+
+
+def test_scores_that_rise_block_by_block():
+    """Each block's scores pass the last one's by far more than the references allow: they are set anew every time."""
+    for n in (1, 4, 40):
+        p = Pair(1, 1, 1024, "e4m3", "f16", seed=36)
+        k, v = p.rows(900), p.rows(900)
+        k[:, 0, 0] = torch.arange(900) // 64 * 4.0
+        q = torch.from_numpy(p.rng.standard_normal((n, 8, 128))).half()
+        q[:, :4, 0], q[:, 4:, 0] = 60.0, -60.0
+        p.append([900], k=k, v=v)
+        p.attend(8, [n], q=q)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_many_rows_and_not_finite_values_behind_the_mask(fmt):
+    p = Pair(1, 1, 512, fmt, "f16", seed=37)
+    k, v = p.rows(330), p.rows(330)
+    k[10, 0, 3], v[20, 0, 5] = float("nan"), float("inf")                # block 0
+    k[325, 0, 1], v[328, 0, 2] = float("inf"), float("nan")              # among 20 new tokens, in the tail
+    p.append([330], k=k, v=v)
+    _, out, _ = p.attend(8, [20], window=200)
+    assert torch.isfinite(out[:15]).all() and torch.isnan(out[15:]).all()
+    _, out, _ = p.attend(8, [20])
+    assert torch.isnan(out).all()
+    q = torch.from_numpy(p.rng.standard_normal((20, 8, 128))).half()     # a query that is not finite stays alone
+    q[3, 2, 9] = float("nan")
+    _, out, _ = p.attend(8, [20], window=200, q=q, check=False)
+    assert torch.isnan(out[3, 2]).all() and torch.isfinite(out[3, :2]).all() and torch.isfinite(out[:3]).all()
+
+
+def test_many_rows_to_strided_outputs_and_untouched_ones():
+    hq = _hq()
+    p = Pair(3, 2, 512, "e4m3", "bf16", seed=38)
+    p.append([300, 90, 500])
+    q = torch.randn(140, 12, 128, device="cuda").bfloat16()[:, 2:10]
+    buf, lse = torch.full((140, 9, 136), 5.0, device="cuda", dtype=torch.bfloat16), torch.full((140, 8), 5.0, device="cuda")
+    cu = _ints([3, 60, 60, 130])
+    hq.hq_kv8_attn(p.c, q, cu, p.len, 70, out=buf[:, :8, :128], lse=lse)
+    assert p.c.errors() == [0, 0, 0]
+    keep = [0, 1, 2] + list(range(130, 140))
+    assert (buf[keep] == 5).all() and (lse[keep] == 5).all() and (buf[:, 8] == 5).all() and (buf[:, :, 128:] == 5).all()
+    for b, (lo, hi) in ((0, (3, 60)), (2, (60, 130))):
+        check_rows(buf[lo:hi, :8, :128], lse[lo:hi], p.ref[b], q[lo:hi].double().cpu().numpy(), 128 ** -0.5, 0, "bf16")
+
+
+def test_calls_of_every_kernel_share_a_stream_and_its_scratch():
+    """One token, drafts and chunks in turn on one stream and on two at once, and captured: the same bits as alone."""
+    hq = _hq()
+    p = Pair(2, 2, 4096, "e4m3", "f16", seed=39)
+    p.append([4000, 2500])
+    cases = []
+    for G, n in ((4, [1, 1]), (8, [2, 1]), (4, [5, 6]), (4, [9, 20]), (4, [100, 300])):
+        q, out, _ = p.attend(G, n, check=False)
+        cases.append((q.cuda(), _ints([0, n[0], n[0] + n[1]]), max(n), out.clone()))
+    call = lambda x, **kw: hq.hq_kv8_attn(p.c, x[0], x[1], p.len, x[2], **kw)
+    for _ in range(3):
+        for x in cases + cases[::-1]:
+            assert torch.equal(call(x), x[3])
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream() for _ in range(2)]
+    got = [(call(x, stream=s[i % 2]), x[3]) for i, x in enumerate(cases * 4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in got)
+    graphs = []
+    for x in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = call(x)
+        graphs.append((g, out, x[3]))
+    for _ in range(3):
+        for i, (g, _, _) in enumerate(graphs):
+            with torch.cuda.stream(s[i % 2]):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for _, a, b in graphs)
+
+
 # ----------------------------------------------------------------------------- together
 
 @pytest.mark.parametrize("fmt,dtype", [("e4m3", "f16"), ("int8", "bf16")])
