@@ -814,8 +814,7 @@ hq_status launch_f(Kv8AttnArgs& a, int sms, cudaStream_t st) {
   }
 }
 
-constexpr int CTAS = 4;  // most on an SM
-size_t counters_bytes(int sms) { return (static_cast<size_t>(CTAS) * sms * 4 + 255) / 256 * 256; }
+constexpr int CTAS = 2;  // most on an SM: HQ_KV8_WS_ZERO holds a counter for each CTA of up to 512 SMs
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -830,7 +829,7 @@ hq_status device_sms(int* sms) {
 size_t attn_workspace(int64_t rows, int sms) {
   const size_t parts = rows > ROWS_MAX ? kv8_attn_tc_parts(rows, sms)
                                        : static_cast<size_t>(2) * CTAS * sms * 8 * std::max(row_eights(rows), 1) * (D + 4);
-  return counters_bytes(sms) + parts * sizeof(float);
+  return HQ_KV8_WS_ZERO + parts * sizeof(float);
 }
 
 bool sizes_ok(const hq_kv8_cache* c, int Hq, int max_new) {
@@ -885,7 +884,7 @@ hq_status hq_kv8_attn(const hq_kv8_cache* c, int32_t dtype, const void* q, int64
   a.kv_len = kv_len;
   a.scale = sm_scale * hq::LOG2E;
   a.counters = static_cast<unsigned int*>(ws);
-  a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + hq::counters_bytes(sms));
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + HQ_KV8_WS_ZERO);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (static_cast<int64_t>(a.G) * max_new > hq::ROWS_MAX) return hq::launch_kv8_attn_tc(a, dtype, sms, s);
   if (dtype == HQ_F16)

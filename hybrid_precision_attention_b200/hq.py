@@ -33,7 +33,7 @@ _DTYPE = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN, ROPE_BANDS = range(5)
 KV8_E4M3, KV8_INT8 = 0, 1
-KV8_PAGE_BYTES, KV8_TAIL = 16448, 128
+KV8_PAGE_BYTES, KV8_TAIL, KV8_WS_ZERO = 16448, 128, 4096
 
 
 class HqError(RuntimeError):
@@ -582,20 +582,22 @@ class Kv8Cache:
         return self.err.cpu().tolist()
 
     def workspace(self, Hq: int, max_new: int, stream_ptr: int) -> torch.Tensor:
-        """Zeroed scratch of an attention call, one per launch stream: calls on different streams may run at the
-        same time.  A captured graph gets its own from its memory pool, cleared in the graph: replays of two graphs
-        share nothing."""
+        """Scratch of an attention call with zeroed counters, one per launch stream: calls on different streams may run
+        at the same time.  A captured call gets its own from the graph's memory pool, its counters cleared in the graph:
+        replays of two graphs share nothing."""
         n = self._ws_bytes.get((Hq, max_new))
         if n is None:
             n = int(_lib.hq_kv8_attn_workspace_bytes(self.ref, Hq, max_new))
             if n == 0:
                 raise HqError(f"hq_kv8_attn: {Hq} query heads over {self.Hkv} kv heads, {max_new} new tokens")
             self._ws_bytes[(Hq, max_new)] = n
-        if torch._C._cuda_isCurrentStreamCapturing():
-            return torch.zeros(n, dtype=torch.uint8, device=self.device)
-        w = self._ws.get(stream_ptr)
+        capturing = torch._C._cuda_isCurrentStreamCapturing()
+        w = None if capturing else self._ws.get(stream_ptr)
         if w is None or w.numel() < n:
-            w = self._ws[stream_ptr] = torch.zeros(n, dtype=torch.uint8, device=self.device)
+            w = torch.empty(n, dtype=torch.uint8, device=self.device)
+            w[:KV8_WS_ZERO].zero_()
+            if not capturing:
+                self._ws[stream_ptr] = w
         return w
 
 

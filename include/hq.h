@@ -507,9 +507,11 @@ HQ_API hq_status hq_kv8_read(const hq_kv8_cache* c, int32_t dtype, const int32_t
                              void* k_out, void* v_out, int64_t o_batch, int64_t o_head, int64_t o_tok,
                              int32_t zero_rest, hq_stream_t stream);
 
-/* Device workspace of hq_kv8_attn for these sizes (0: invalid).  It starts with
- * counters: zero-fill it once before its first use; the kernels return them to zero.  A
- * workspace must not be shared by calls that can run at the same time. */
+/* Device workspace of hq_kv8_attn for these sizes (0: invalid).  Its first
+ * HQ_KV8_WS_ZERO bytes are counters: zero them once before its first use; the kernels
+ * return them to zero.  A workspace must not be shared by calls that can run at the
+ * same time. */
+#define HQ_KV8_WS_ZERO 4096
 HQ_API size_t hq_kv8_attn_workspace_bytes(const hq_kv8_cache* c, int32_t Hq, int32_t max_new);
 
 /*
