@@ -14,9 +14,9 @@
 // both layouts).  Many tokens: a block takes a few tokens with all their heads, its
 // threads make the tokens' sines once, into shared memory, and each rotates its
 // pairs of up to 8 heads, the first ones' loads in flight while the sines are made.
-// Few tokens: a head a thread, the shortest chain (16 tokens 2.2 us).
-// 8192 tokens x 40 heads x 128, bf16: 31 us, 5.3 TB/s (a row pointer worked out for
-// every head and each element converted by itself: 55 us); 5331 x 24 heads, f32: 22.5 us.
+// Few tokens: a head a thread, the shortest chain (16 tokens 2.1 us, most of it the launch).
+// 8192 tokens x 40 heads x 128, bf16: 31 us, 5.4 TB/s (a row pointer worked out for
+// every head and each element converted by itself: 55 us); 5331 x 24 heads, f32: 22 us, 5.9 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -223,8 +223,9 @@ hq_status launch_v(RopeArgs& a, cudaStream_t st) {
   a.lanes = lanes;
   const long long many = (a.tokens + a.TB - 1) / a.TB, few = (a.tokens + slots - 1) / slots;
   if (few > 0x7fffffffll || many > 0x7fffffffll) return HQ_ERR_UNSUPPORTED;
-  // from two blocks an SM on the heads share their sines; fewer leave SMs idle
-  if (many >= 2 * 148) {
+  // heads share their sines from half as many blocks as SMs on (40 heads x 128, bf16: 592
+  // tokens 4.8 us against 5.3 us, 1184 6.0 against 8.0; 300 tokens 4.8 against 4.4, 16 4.6 against 2.0)
+  if (many >= 148 / 2) {
     return cuda_status(launch_chained(rope_many_kernel<E, V, HALF>, dim3(static_cast<unsigned>(many)), 256, 0, st, a), "rope launch");
   } else {
     if (a.H > 65535) return HQ_ERR_UNSUPPORTED;

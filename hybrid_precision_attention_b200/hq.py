@@ -571,6 +571,9 @@ class Kv8Cache:
         _need(self.tail_scale, torch.float32, (B, Hkv, 2, KV8_TAIL), "tail_scale")
         self.err = z((B,), torch.int32)
         self.device, self.index = self.err.device, self.err.get_device()
+        for name in ("tail_k", "tail_v", "tail_scale"):
+            if getattr(self, name).get_device() != self.index:
+                raise HqError(f"{name}: on {getattr(self, name).device}, the pages on {self.device}")
         self.c = HqKv8CacheStruct(B, Hkv, D, cap, fmt, pages.shape[0] if page_table is not None else 0, *[
             None if t is None else t.data_ptr() for t in (pages, page_table, self.tail_k, self.tail_v, self.tail_scale, self.err)])
         self.ref = ctypes.byref(self.c)
@@ -579,7 +582,10 @@ class Kv8Cache:
 
     def errors(self) -> list:
         """Every sequence's DEVERR_* bits."""
-        return self.err.cpu().tolist()
+        bits = self.err.cpu().tolist()
+        if any(b & DEVERR_TIMEOUT for b in bits):
+            self._ws.clear()  # a call that gave up may have left counts in its scratch
+        return bits
 
     def workspace(self, Hq: int, max_new: int, stream_ptr: int) -> torch.Tensor:
         """Scratch of an attention call with zeroed counters, one per launch stream: calls on different streams may run
@@ -656,7 +662,7 @@ def hq_kv8_attn(cache: Kv8Cache, q, cu, kv_len, max_new: int, sm_scale: float = 
                 lse=None, return_lse: bool = False, ws=None, stream=None):
     """Attention of the newest tokens (appended before): q [N, Hq, D] holds sequence b's queries as rows
     cu[b] .. cu[b+1]-1, at most max_new of them, at its last positions; causal, with window > 0 over that many
-    positions.  Returns out [N, Hq, D], with return_lse (out, lse float [N, Hq], base 2)."""
+    positions.  Returns out [N, Hq, D] (``out`` must not overlap q), with return_lse (out, lse float [N, Hq], base 2)."""
     dev = cache.index
     if stream is not None or _device() != dev:
         with _On(dev, stream):

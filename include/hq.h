@@ -491,7 +491,8 @@ HQ_API hq_status hq_kv8_validate(const hq_kv8_cache* c);
  * two blocks' rows stand in the tail.  A call may start up to 64 positions before the
  * end of what was appended (drafted tokens that were rejected): the rows from there on
  * are replaced.  cu int32 [B+1], kv_len int32 [B] (device).  A sequence with
- * kv_len > cap (HQ_DEVERR_CAPACITY) or inconsistent rows (HQ_DEVERR_ROWS) is left as it is.
+ * kv_len > cap (HQ_DEVERR_CAPACITY) or inconsistent rows (HQ_DEVERR_ROWS) is left as it is;
+ * where cu descends, so that rows belong to two sequences, so may others be.
  */
 HQ_API hq_status hq_kv8_append(const hq_kv8_cache* c, int32_t dtype, const void* k, int64_t k_tok, int64_t k_head,
                                const void* v, int64_t v_tok, int64_t v_head, int32_t N, const int32_t* cu,
@@ -509,8 +510,8 @@ HQ_API hq_status hq_kv8_read(const hq_kv8_cache* c, int32_t dtype, const int32_t
 
 /* Device workspace of hq_kv8_attn for these sizes (0: invalid).  Its first
  * HQ_KV8_WS_ZERO bytes are counters: zero them once before its first use; the kernels
- * return them to zero.  A workspace must not be shared by calls that can run at the
- * same time. */
+ * return them to zero (after a HQ_DEVERR_TIMEOUT they may not be: zero them again).  A
+ * workspace must not be shared by calls that can run at the same time. */
 #define HQ_KV8_WS_ZERO 4096
 HQ_API size_t hq_kv8_attn_workspace_bytes(const hq_kv8_cache* c, int32_t Hq, int32_t max_new);
 
@@ -522,7 +523,8 @@ HQ_API size_t hq_kv8_attn_workspace_bytes(const hq_kv8_cache* c, int32_t Hq, int
  *     out[row, h] = sum_j p_j v_j,  p = softmax_j(q[row, h] . k_j * sm_scale),
  * each key and value as cached (read through the page table; no 16-bit copy is made).
  * Query head h reads kv head h / (Hq / Hkv).
- *   q, out [N, Hq, D] HQ_F16 or HQ_BF16, strides in elements (multiples of 8), D contiguous
+ *   q, out [N, Hq, D] HQ_F16 or HQ_BF16, strides in elements (multiples of 8), D
+ *          contiguous; they must not overlap
  *   lse    float [N, Hq] contiguous or NULL: log2 of the softmax's denominator,
  *          log2 sum_j 2^(s_j), s_j = q.k_j * sm_scale * log2 e
  * Rows outside [cu[0], cu[B]) and rows of a sequence that is skipped

@@ -720,6 +720,30 @@ def test_calls_of_every_kernel_share_a_stream_and_its_scratch():
         assert all(torch.equal(a, b) for _, a, b in graphs)
 
 
+def test_scratch_after_a_wait_that_gave_up():
+    """errors() that tells of a timeout lets go of scratch whose counters may not be zero."""
+    hq = _hq()
+    p = Pair(1, 1, 4096, "e4m3", "f16", seed=40)
+    p.append([4000])
+    q, out, _ = p.attend(4, [1])
+    assert len(p.c._ws) == 1
+    for w in p.c._ws.values():
+        w[:hq.KV8_WS_ZERO] = 1
+    p.c.err[0] = hq.DEVERR_TIMEOUT
+    assert p.c.errors() == [hq.DEVERR_TIMEOUT]
+    p.c.err.zero_()
+    assert torch.equal(hq.hq_kv8_attn(p.c, q.cuda(), _ints([0, 1]), p.len, 1), out)
+
+
+def test_output_in_the_queries_place_is_refused():
+    hq = _hq()
+    p = Pair(1, 1, 128, "e4m3", "f16", seed=41)
+    p.append([5])
+    q = torch.randn(1, 4, 128, device="cuda").half()
+    with pytest.raises(hq.HqError, match="hq_kv8_attn"):
+        hq.hq_kv8_attn(p.c, q, _ints([0, 1]), p.len, 1, out=q)
+
+
 # ----------------------------------------------------------------------------- together
 
 @pytest.mark.parametrize("fmt,dtype", [("e4m3", "f16"), ("int8", "bf16")])
