@@ -21,10 +21,12 @@
 // whole is finished there; the pieces of the others go to the workspace and the
 // CTA that delivers a task's last piece joins them in order, so that results do
 // not depend on timing.  Short tasks are not cut.  Within a CTA NG groups of warps
-// take every NG-th block of a task, 16 or 32 tokens a warp.  Each warp keeps a
-// ring of its own slices of the pages in flight by bulk copies (a slice is free again as soon as it is in registers, and
-// no other warp is waited for) and its own running references, sums and
-// accumulators.
+// take every NG-th block of a task, 32 tokens a warp.  Each warp keeps a ring of
+// its own slices of the pages in flight by bulk copies (no other warp is waited
+// for) and its own running references, sums and accumulators.  Registers are what
+// bounds the tokens of a step and the warps: the query operands stand in shared memory
+// and values stay in the slot until they are needed (with both in registers 24
+// rows left room for 16 tokens a step: 64 sequences of 1K to 8K 183 us, now 131 us).
 //
 // Two running references per row: m for the scores and, for the accumulators, E
 // for score + log2(value scale), so that blocks whose scales lie far apart keep
@@ -36,11 +38,11 @@
 // largest fp16 weight is then 2^15 and the smallest normal one 2^-20 of the
 // reference.
 //
-// Measured (8 kv heads): 64 sequences of 1K to 16K, a token each, 8 rows: 186 us, 6.2 TB/s of
-// codes, the copy rate; 16 rows over 64 of 4K to 8K 137 us, 4.3 TB/s, where the products (legacy
-// matrix instructions, 192 a page) take as long as the copies; 16 windows of 4096, 20 rows:
-// 51 us, 2.7 TB/s, bound by them.  One sequence of 32K: 20.6 us, 3.3 TB/s: 6 us of it are the
-// 28 pages of a CTA, the others launch, plan, first copies and the join of 19 pieces.
+// Measured (8 kv heads): 64 sequences of 1K to 16K, a token each, 8 rows: 182 us, 6.4 TB/s of
+// codes, the copy rate; 16 rows, 64 of 4K to 8K: 135 us, 6.0 TB/s; 24 rows, 64 of 1K to 8K:
+// 131 us, 4.6 TB/s; 16 windows of 4096, 20 rows: 44 us, 3.1 TB/s, bound by the latencies of a
+// step (two warps a scheduler) and by the tasks' ends.  One sequence of 32K: 18.6 us, 3.6 TB/s:
+// 6 us of it are a CTA's 28 pages, the others launch, plan, first copies and the join of 19 pieces.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -58,16 +60,13 @@ namespace {
 constexpr float P_BIAS = 6.0f;     // log2 of the fp16 weight at both references
 constexpr float P_SLACK = 8.0f;    // how far (log2) a score may pass m
 constexpr float V_LIMIT = 128.0f;  // 2^(P_BIAS + 1): how far a value scale may pass its reference; 2^8 * 2^7 < 65504
-constexpr int TASK_UNITS = 6;      // what a task costs besides its blocks, in blocks (about 3000 cycles of 500 each)
+constexpr int TASK_UNITS = 12;     // what a task costs besides its blocks, in blocks (about 6000 cycles of 500 each)
 constexpr int OS = D + 4;          // row stride (floats) of accumulators in shared memory: 4 rows of a store step 8 banks apart
 
 template <int NB, int W>
 struct Cfg {
   static constexpr int R = 8 * NB;            // rows of a task
-  // 16-token tiles of a page that a warp takes in one step: two while a
-  // thread's accumulators and query operands (48 NB registers) leave room for
-  // their codes (32 registers a tile)
-  static constexpr int MT = NB <= 2 ? 2 : 1;
+  static constexpr int MT = 2;                // 16-token tiles of a page that a warp takes in one step
   static constexpr int WARPS = W;             // of up to 255 registers
   static constexpr int CTAS = 8 / W;          // on an SM
   static constexpr int THREADS = WARPS * 32;
@@ -75,13 +74,14 @@ struct Cfg {
   static constexpr int NG = WARPS / PW;       // groups
   static constexpr int SLICE = MT * 16 * D;   // bytes of a warp's part of a page's K (or V) codes
   static constexpr int SLOT = 2 * SLICE + 16; // K slice, V slice, scales
-  static constexpr int SLOTS = MT == 2 ? 2 : 5;    // ring of a warp
+  static constexpr int SLOTS = 2;             // ring of a warp
   static constexpr int OW = W < 4 ? W : 4;    // warps whose accumulators are in shared memory at a time
   static constexpr int OBUF = OW * 8 * OS * 4;     // of 8 rows
   static constexpr int RED = WARPS * R * 16;       // (m, E, l) of each warp's rows
+  static constexpr int Q = NB * 2048 + R * 4;      // query operands [NB][4][lane] of 16 bytes; multipliers of rows
   static constexpr int RING = WARPS * SLOTS * SLOT;
   static constexpr int AHEAD = 72;                 // a warp's copy cursor
-  static constexpr int FIXED = OBUF + RED + RING + WARPS * (SLOTS * 8 + AHEAD) + 32 * 8 + 16;
+  static constexpr int FIXED = OBUF + RED + Q + RING + WARPS * (SLOTS * 8 + AHEAD) + 32 * 8 + 16;
 };
 
 // blocks of sequence s that its queries see: [begin, end)
@@ -113,7 +113,9 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
   extern __shared__ __align__(128) uint8_t sm[];
   float* obuf = reinterpret_cast<float*>(sm);                       // [warp][row of 8][OS]
   float4* red = reinterpret_cast<float4*>(sm + C::OBUF);            // [warp][row] (m, E, l, -)
-  uint8_t* rings = sm + C::OBUF + C::RED;
+  uint4* q_sh = reinterpret_cast<uint4*>(sm + C::OBUF + C::RED);
+  float* q_mul = reinterpret_cast<float*>(q_sh + NB * 128);
+  uint8_t* rings = sm + C::OBUF + C::RED + C::Q;
   uint64_t* bars = reinterpret_cast<uint64_t*>(rings + C::RING);
   uint64_t* sums = bars + C::WARPS * SLOTS;                         // the plan's sums and maxima of each warp
   uint8_t* ahead = reinterpret_cast<uint8_t*>(sums + 32);
@@ -271,9 +273,9 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
   };
   static_assert(sizeof(Ahead) <= C::AHEAD, "the cursor's place");
   Ahead& ah = *reinterpret_cast<Ahead*>(ahead + warp * C::AHEAD);
-  uint4 qv[NB][4];  // a task's queries are fetched while the one before it is joined, the first's here
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) load_q(k, nb, qv[nb]);
+  // a task's queries are fetched while the one before it is joined, the first's here
+  uint4 qv[4];
+  if (warp < NB) load_q(k, warp, qv);
   auto first_of = [&](int t0, int ordinal) { return t0 + (g4 + ordinal) % NG; };
   struct Pages {
     int n, at, b;         // how many (0: the run has no more), the next one, their sequence
@@ -335,45 +337,59 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
   int slot = 0, phase = 0, taken = 0;
   bool ok = true;
 
+  // query rows as B operands: lane (g, t4) holds row g (+ 8 nb), elements
+  // 64 j + 16 t4 + 4 u + {0..3} at step 4 j + u, the elements that the K codes'
+  // 16-byte chunk t4 of half j gives at that step.  Returns the row's multiplier.
+  auto operands = [&](const uint4 (&v)[4], uint32_t (&f)[16]) {
+    float mul = 1.0f;
+    const E* e = reinterpret_cast<const E*>(v);
+    if (IsBf16<E>::value) {
+      // bf16 rows become fp16 at a power of two that brings their largest value to [2^14, 2^15)
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(to_float(e[i])) & 0x7fffffffu);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      float inv = 1.0f;
+      if (m != 0 && m < 0x7f800000u) {
+        const int ex = max(static_cast<int>(m >> 23) - 127 - 14, -126);  // at most 113
+        mul = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+        inv = ex == -126 ? 0x1p126f : __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) f[i] = pack_f16x2(to_float(e[2 * i]) * inv, to_float(e[2 * i + 1]) * inv);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) f[i] = reinterpret_cast<const uint32_t*>(v)[i];
+    }
+    return mul;
+  };
+  // the fetched queries into shared memory, 8 rows a warp; a barrier follows
+  auto stage_q = [&]() {
+    if (warp < NB) {
+      uint32_t f[16];
+      const float mul = operands(qv, f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q_sh[(warp * 4 + i) * 32 + lane] = make_uint4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+      if (t4 == 0) q_mul[8 * warp + g] = mul * a.scale;
+    }
+  };
+  stage_q();
+  __syncthreads();
+
   int ordinal = 0;
   for (uint32_t u = u_first;;) {
     const size_t bh = static_cast<size_t>(k.b) * c.Hkv + k.h;
     const int rows = k.s.n * a.G;
 
-    // query rows as B operands: lane (g, t4) holds row g (+ 8 nb), elements
-    // 64 j + 16 t4 + 4 u + {0..3} at step 4 j + u, the elements that the K codes'
-    // 16-byte chunk t4 of half j gives at that step
-    uint32_t qf[NB][16];
     float qs[NB][2];   // multiplier of the scores of rows 2 t4, 2 t4 + 1
     int qp[NB][2];     // their positions (rows past the last: where they see all)
     float m_run[NB][2], e_run[NB][2], l_run[NB][2], ef[NB][2];  // ef = 2^(m - E + P_BIAS)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      float mul = 1.0f;
-      const uint4(&v)[4] = qv[nb];
-      const E* e = reinterpret_cast<const E*>(v);
-      if (IsBf16<E>::value) {
-        // bf16 rows become fp16 at a power of two that brings their largest value to [2^14, 2^15)
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(to_float(e[i])) & 0x7fffffffu);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        float inv = 1.0f;
-        if (m != 0 && m < 0x7f800000u) {
-          const int ex = max(static_cast<int>(m >> 23) - 127 - 14, -126);  // at most 113
-          mul = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
-          inv = ex == -126 ? 0x1p126f : __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) qf[nb][i] = pack_f16x2(to_float(e[2 * i]) * inv, to_float(e[2 * i + 1]) * inv);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) qf[nb][i] = reinterpret_cast<const uint32_t*>(v)[i];
-      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        qs[nb][i] = __shfl_sync(0xffffffffu, mul, (2 * t4 + i) * 4) * a.scale;
+        qs[nb][i] = q_mul[8 * nb + 2 * t4 + i];
         const int rr = 8 * nb + 2 * t4 + i;
         // rows past the last have zero queries: their reference starts at their
         // score, 0, and no tile of theirs is ever masked or out of range
@@ -407,15 +423,22 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int i = 0; i < 4; ++i) sc[j][nb][i] = 0.f;
+      uint4 qw[NB];
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
+      for (int s = 0; s < 8; ++s) {
+        if (s % 2 == 0) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) qw[nb] = q_sh[(nb * 4 + s / 2) * 32 + lane];
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           uint32_t f[4];
           kf(j, s, f);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma16816(sc[j][nb], f[0], f[1], f[2], f[3], qf[nb][2 * s], qf[nb][2 * s + 1]);
+          for (int nb = 0; nb < NB; ++nb)
+            mma16816(sc[j][nb], f[0], f[1], f[2], f[3], s & 1 ? qw[nb].z : qw[nb].x, s & 1 ? qw[nb].w : qw[nb].y);
         }
+      }
       bool far = false;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -552,13 +575,9 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const uint8_t* src = ring + slot * SLOT;
-      uint4 kw[MT][4], vw[MT][4];
+      uint4 kw[MT][4], vw[MT];  // the values from the slot as they are needed, for want of registers
 #pragma unroll
       for (int i = 0; i < 4 * MT; ++i) kw[i / 4][i % 4] = reinterpret_cast<const uint4*>(src + i * 512)[lane];
-      if (MT == 2) {
-#pragma unroll
-        for (int i = 0; i < 4 * MT; ++i) vw[i / 4][i % 4] = reinterpret_cast<const uint4*>(src + SLICE + i * 512)[lane];
-      }
       const float2 sc = *reinterpret_cast<const float2*>(src + 2 * SLICE);
       auto release = [&]() {
         __syncwarp();  // every lane has its part: the slot takes the next slice
@@ -566,7 +585,6 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
         if (issue(slot)) ++issued;
         if (++slot == SLOTS) slot = 0, phase ^= 1;
       };
-      if (MT == 2) release();
       auto word = [](const uint4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; };
       auto kf = [&](int j, int s, uint32_t (&f)[4]) {
         // chunk (token half a, d half h) = 2 a + h; word s % 4 of it
@@ -574,10 +592,9 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
         kv8_half4<FMT>(word(kw[j][2 + (s >> 2)], s & 3), f[1], f[3]);
       };
       auto vf = [&](int j, int d, uint32_t (&f)[4]) {
-        // many rows: values from the slot as they are needed, for want of registers
-        if (MT == 1 && (d & 1) == 0) vw[j][d >> 1] = reinterpret_cast<const uint4*>(src + SLICE + (d >> 1) * 512)[lane];
-        kv8_half4<FMT>(word(vw[j][d >> 1], (d & 1) * 2), f[0], f[2]);
-        kv8_half4<FMT>(word(vw[j][d >> 1], (d & 1) * 2 + 1), f[1], f[3]);
+        if ((d & 1) == 0) vw[j] = reinterpret_cast<const uint4*>(src + SLICE + (4 * j + (d >> 1)) * 512)[lane];
+        kv8_half4<FMT>(word(vw[j], (d & 1) * 2), f[0], f[2]);
+        kv8_half4<FMT>(word(vw[j], (d & 1) * 2 + 1), f[1], f[3]);
       };
       const float ks[2] = {sc.x, sc.x}, vs[2] = {sc.y, sc.y};
       constexpr std::integral_constant<int, MT> all{};
@@ -586,15 +603,14 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
         tiles(all, std::false_type{}, kf, vf, ks, vs, sc.y, pos);
       else
         tiles(all, std::true_type{}, kf, vf, ks, vs, sc.y, pos);
-      if (MT == 1) release();
+      release();
     }
 
     const uint32_t u_next = u + k.units;
     Task k_next = k;
     if (u_next < u1) {
       next_task(u_next, k_next);
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) load_q(k_next, nb, qv[nb]);
+      if (warp < NB) load_q(k_next, warp, qv);
     }
 
     // ------------------------------------------------------------ the CTA's piece of the task
@@ -632,6 +648,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       __syncthreads();  // red is there; the buffer's earlier readers are done
+      if (nb == 0 && u_next < u1) stage_q();  // every warp is through with the task's
       float f[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -794,7 +811,7 @@ hq_status launch(Kv8AttnArgs& a, int sms, cudaStream_t st) {
 }
 
 // Rows of a kv head, in eights.
-// More go to the tcgen05 kernel (64 sequences of 1K-8K, 8 kv heads: 24 rows 182 us here,
+// More go to the tcgen05 kernel (64 sequences of 1K-8K, 8 kv heads: 24 rows 131 us here,
 // 32 rows 419 us here, for want of registers, and 300 us there).
 constexpr int ROWS_MAX = 24;
 int row_eights(int64_t rows) { return static_cast<int>((rows + 7) / 8); }
@@ -803,10 +820,12 @@ int row_eights(int64_t rows) { return static_cast<int>((rows + 7) / 8); }
 // each, one of two streams while the other joins its warps' results (8 kv heads, 128
 // sequences of 500-3000: 88 us against 100 us, 64 of 100-700 23 against 28; of
 // 1K-16K both 184 us); where tasks are few, twice the pieces are to be joined and
-// twice the plans made (one 32K sequence: 22.4 us against 20.6 us).
+// twice the plans made (one 32K sequence: 8 rows 22.4 us against 20.6 us, 24 rows 40.7
+// against 31.7).  A task of more rows takes longer to join (16 windows of 4096, 20 rows:
+// 44.4 us against 45.6 us; 8 rows, 16 of 4K-8K: 42.7 against 41.1).
 template <class E, int FMT, int NB>
 hq_status launch_w(Kv8AttnArgs& a, int sms, cudaStream_t st) {
-  if (static_cast<int64_t>(a.c.B) * a.c.Hkv >= 2 * sms)
+  if (static_cast<int64_t>(a.c.B) * a.c.Hkv >= (NB == 1 ? 2 * sms : sms / 2))
     return launch<E, FMT, NB, 4>(a, sms, st);
   return launch<E, FMT, NB, 8>(a, sms, st);
 }
@@ -816,7 +835,7 @@ hq_status launch_f(Kv8AttnArgs& a, int sms, cudaStream_t st) {
   switch (row_eights(a.G * a.max_new)) {
     case 1: return launch_w<E, FMT, 1>(a, sms, st);
     case 2: return launch_w<E, FMT, 2>(a, sms, st);
-    default: return launch<E, FMT, 3, 8>(a, sms, st);
+    default: return launch_w<E, FMT, 3>(a, sms, st);
   }
 }
 
