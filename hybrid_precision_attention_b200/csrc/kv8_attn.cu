@@ -16,7 +16,7 @@
 // thread's 16-byte load is its operand for four steps, with no conflict and no
 // shuffle.  P^T comes from S^T by a register transpose (movmatrix).
 //
-// Work: the tasks (sequence, kv head, 8 NB rows) have their blocks laid end to
+// Work: the tasks (sequence, kv head, 8 NB rows of it) have their blocks laid end to
 // end and cut into gridDim runs, equal to a block.  A task that one CTA holds
 // whole is finished there; the pieces of the others go to the workspace and the
 // CTA that delivers a task's last piece joins them in order, so that results do
@@ -80,7 +80,7 @@ struct Cfg {
   static constexpr int RED = WARPS * R * 16;       // (m, E, l) of each warp's rows
   static constexpr int Q = NB * 2048 + R * 4;      // query operands [NB][4][lane] of 16 bytes; multipliers of rows
   static constexpr int RING = WARPS * SLOTS * SLOT;
-  static constexpr int AHEAD = 72;                 // a warp's copy cursor
+  static constexpr int AHEAD = 80;                 // a warp's copy cursor
   static constexpr int FIXED = OBUF + RED + Q + RING + WARPS * (SLOTS * 8 + AHEAD) + 32 * 8 + 16;
 };
 
@@ -133,21 +133,23 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
   }
   if (threadIdx.x < 2) flags[threadIdx.x] = 0;
   chained();
-  // prefix[b]: units (of one task) of the sequences before b, in the low half,
-  // and those of them that have blocks, in the high half
+  auto groups_of = [&](const Kv8Seq& s) { return (s.n * a.G + R - 1) / R; };  // of rows
+  // prefix[b]: units (of one kv head) of the sequences before b, in the low half,
+  // and their tasks in the high half
   uint64_t carry = 0;
   int longest = 0;
   for (int b0 = 0; b0 < B; b0 += C::THREADS) {
     const int b = b0 + threadIdx.x;
-    int n = 0;
+    int n = 0, groups = 0;
     if (b < B) {
       Kv8Seq s;
       kv8_seq(c, a.cu, a.kv_len, a.N, a.max_new, b, blockIdx.x == 0, s);
       int begin, end;
       seq_blocks(s, a.window, begin, end);
       n = end - begin;
+      groups = groups_of(s);
     }
-    const uint64_t mine = n > 0 ? 1ull << 32 | static_cast<uint32_t>(n + TASK_UNITS) : 0ull;
+    const uint64_t mine = n > 0 ? static_cast<uint64_t>(groups) << 32 | static_cast<uint32_t>(groups * (n + TASK_UNITS)) : 0ull;
     uint64_t x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
   // what it costs besides them; or, where every task is short and none need share
   // a CTA with another, one unit, so that no task is cut (its pieces' way through
   // the workspace takes longer than 24 blocks).
-  const uint32_t per_seq = c.Hkv;  // tasks of a sequence: its kv heads
+  const uint32_t per_seq = c.Hkv;  // what the prefixes count comes once for each kv head
   const uint32_t tasks = static_cast<uint32_t>(carry >> 32) * per_seq;
   const bool uncut = longest <= 24 && tasks <= gridDim.x;
   const uint32_t total = uncut ? tasks : static_cast<uint32_t>(carry) * per_seq;
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
   // A task of the CTA's run: [t0, t1) of its blocks are ours (none where the run
   // begins behind them), `units` of the run.
   struct Task {
-    int b, h, begin, blocks, t0, t1;
+    int b, h, row0, begin, blocks, t0, t1;  // rows row0 .. row0 + R - 1 of the kv head
     uint32_t units;
     Kv8Seq s;
   };
@@ -216,18 +218,23 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
     seq_of(k);
     const uint32_t rel = u - before_of(lo) * per_seq;
     const uint32_t each = uncut ? 1u : k.blocks + TASK_UNITS, task = rel / each;
-    k.h = task;
+    const int groups = groups_of(k.s);
+    k.h = task / groups;
+    k.row0 = (task - k.h * groups) * R;
     k.t0 = rel - task * each;
     span_of(u, k);
   };
   auto next_task = [&](uint32_t u, Task& k) {  // the task after k, which begins with unit u < u1
     k.t0 = 0;
-    if (++k.h == c.Hkv) {
-      k.h = 0;
-      do {
-        ++k.b;
-        seq_of(k);
-      } while (k.blocks == 0);
+    if ((k.row0 += R) >= k.s.n * a.G) {
+      k.row0 = 0;
+      if (++k.h == c.Hkv) {
+        k.h = 0;
+        do {
+          ++k.b;
+          seq_of(k);
+        } while (k.blocks == 0);
+      }
     }
     span_of(u, k);
   };
@@ -243,9 +250,9 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
     next_task(u_first, k);
   }
 
-  // raw query rows 8 nb + g of a task (elements 16 t4 .. and 64 + 16 t4 ..)
+  // raw query rows 8 nb + g of a task's (elements 16 t4 .. and 64 + 16 t4 ..)
   auto load_q = [&](const Task& k, int nb, uint4 (&v)[4]) {
-    const int r = 8 * nb + g;
+    const int r = k.row0 + 8 * nb + g;
     if (r < k.s.n * a.G) {
       const E* p = static_cast<const E*>(a.q) + static_cast<int64_t>(k.s.row0 + r / a.G) * a.q_tok +
                    static_cast<int64_t>(k.h * a.G + r % a.G) * a.q_head + 16 * t4;
@@ -390,7 +397,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         qs[nb][i] = q_mul[8 * nb + 2 * t4 + i];
-        const int rr = 8 * nb + 2 * t4 + i;
+        const int rr = k.row0 + 8 * nb + 2 * t4 + i;
         // rows past the last have zero queries: their reference starts at their
         // score, 0, and no tile of theirs is ever masked or out of range
         qp[nb][i] = rr < rows ? k.s.first + rr / a.G : INT_MAX;
@@ -400,7 +407,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
       }
     }
     // positions of the task's first and last real rows
-    const int q_lo = k.s.first, q_hi = k.s.len - 1;
+    const int q_lo = k.s.first + k.row0 / a.G, q_hi = k.s.first + (min(k.row0 + R, rows) - 1) / a.G;
 
     float o[NB][8][4];
 #pragma unroll
@@ -632,7 +639,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
     constexpr int PART = R * (D + 4);
     float* part = a.parts + static_cast<size_t>(2 * blockIdx.x + (k.t0 == 0)) * PART;
     auto finish = [&](int r, float m, float e, float l, float4 x) {
-      const int rr = r;
+      const int rr = k.row0 + r;
       if (rr >= rows) return;
       // accumulators are at 2^(P_BIAS - E), the sum at 2^-m: the quotient's exponent
       const float f = m == -INFINITY ? 0.f : ex2(e - m - P_BIAS) / l;
@@ -805,16 +812,22 @@ hq_status launch(Kv8AttnArgs& a, int sms, cudaStream_t st) {
   });
   if (e != cudaSuccess) return cuda_fail(e, "kv8 attention setup");
   // units are counted in 32 bits
-  if (static_cast<double>(a.c.B) * a.c.Hkv * (a.c.cap / KV8_BLOCK + TASK_UNITS) >= 4e9) return HQ_ERR_UNSUPPORTED;
+  if (static_cast<double>(a.c.B) * a.c.Hkv * (a.c.cap / KV8_BLOCK + TASK_UNITS) * 2 >= 4e9) return HQ_ERR_UNSUPPORTED;
   return cuda_status(launch_chained(kv8_attn_kernel<E, FMT, NB, W>, dim3(C::CTAS * sms), C::THREADS, C::FIXED + a.c.B * 8, st, a),
                      "kv8 attention launch");
 }
 
-// Rows of a kv head, in eights.
-// More go to the tcgen05 kernel (64 sequences of 1K-8K, 8 kv heads: 24 rows 131 us here,
-// 32 rows 419 us here, for want of registers, and 300 us there).
-constexpr int ROWS_MAX = 24;
-int row_eights(int64_t rows) { return static_cast<int>((rows + 7) / 8); }
+// Rows of a kv head, and rows of a task in eights: up to 24 rows in one task, up to 48 in
+// two, which read the pages one after the other, the second mostly from L2.  More go
+// to the tcgen05 kernel, whose pages take the same time for up to 128 rows.  8 kv heads,
+// here and there: 32 rows, 64 sequences of 1K-8K 196 and 296 us, one of 32K 31 and 71, 64 of
+// 100-700 45 and 122; 48 rows 247 and 313, 40 and 71, 67 and 134; from 64 rows on three tasks would
+// take 370 us against 303 where batches are large.
+constexpr int ROWS_MAX = 48;
+int task_eights(int64_t rows) {
+  const int n = static_cast<int>((rows + 7) / 8);
+  return n <= 3 ? std::max(n, 1) : (n + 1) / 2;
+}
 
 // One CTA of 8 warps on an SM, or two of 4.  Where CTAs finish several tasks
 // each, one of two streams while the other joins its warps' results (8 kv heads, 128
@@ -832,7 +845,7 @@ hq_status launch_w(Kv8AttnArgs& a, int sms, cudaStream_t st) {
 
 template <class E, int FMT>
 hq_status launch_f(Kv8AttnArgs& a, int sms, cudaStream_t st) {
-  switch (row_eights(a.G * a.max_new)) {
+  switch (task_eights(a.G * a.max_new)) {
     case 1: return launch_w<E, FMT, 1>(a, sms, st);
     case 2: return launch_w<E, FMT, 2>(a, sms, st);
     default: return launch_w<E, FMT, 3>(a, sms, st);
@@ -853,7 +866,7 @@ hq_status device_sms(int* sms) {
 
 size_t attn_workspace(int64_t rows, int sms) {
   const size_t parts = rows > ROWS_MAX ? kv8_attn_tc_parts(rows, sms)
-                                       : static_cast<size_t>(2) * CTAS * sms * 8 * std::max(row_eights(rows), 1) * (D + 4);
+                                       : static_cast<size_t>(2) * CTAS * sms * 8 * task_eights(rows) * (D + 4);
   return HQ_KV8_WS_ZERO + parts * sizeof(float);
 }
 

@@ -1,5 +1,5 @@
 // kv8_attn_tc.cu — attention of many new tokens (prompt chunks, long drafts) over
-// the 8-bit block cache on tcgen05 tensor cores.
+// the 8-bit block cache on tcgen05 tensor cores: more than 48 rows of a kv head.
 //
 // The rows of a kv head (its G query heads x the sequence's n new tokens, row
 // r = i G + g, so that a page is read once for all of them) are taken NT x 128

@@ -615,6 +615,19 @@ def test_row_counts_around_the_kernels_borders(fmt, dtype, G, n):
     p.attend(G, [n, n, max(1, n // 3)])
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("G,n", [(8, 4), (3, 11), (1, 47), (16, 3), (4, 12), (7, 7), (8, 8)])
+def test_row_counts_of_two_tasks(dtype, G, n):
+    """25 to 48 rows are two tasks of a kv head, 49 go to the tcgen05 kernel; sequences of one task, of none and of
+    cut tasks beside, with windows."""
+    p = Pair(5, 2, 4096, "e4m3", dtype, seed=42)
+    p.append([4000, 100, 77, 1, 2000])
+    p.attend(G, [n, max(1, 24 // G), 0, 1, n])
+    p.attend(G, [n, n, 1, 0, min(n, 3)], window=65)
+    p.append([1, 28, 0, 0, 48])
+    p.attend(G, [n, n, n, 1, 1], window=1500)
+
+
 @pytest.mark.parametrize("window", [1, 30, 64, 129, 500])
 def test_window_of_many_rows(window):
     p = Pair(2, 1, 1024, "int8", "f16", seed=33)
