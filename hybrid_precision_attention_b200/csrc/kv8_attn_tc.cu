@@ -55,6 +55,11 @@ constexpr float BIAS = 6.0f;               // log2 of the fp16 weight at both re
 constexpr float W_LIMIT = 32768.0f;        // sum of a page's fp16 weights above which the references are set anew
 // what a task costs besides its pages, in pages (some 16000 cycles, two thirds of them
 // queries, epilogue and the first and last pages' latencies)
+// A piece's way through the workspace takes as long as 12 pages: where there is a CTA for
+// every task, tasks are cut only if that saves more (8 kv heads, 512 rows: 8 x 128 tokens
+// 24 us uncut, 29 cut; 4096 rows of 2048 tokens 53 and 63; 4 x 60 tokens over 2000, where most
+// CTAs would stand idle, 60 and 47)
+constexpr int UNCUT = 12;
 template <int NT>
 constexpr int TASK_UNITS = NT == 2 ? 8 : 14;
 constexpr uint32_t TMEM_COLS = 512;        // each stream: S 2 x 64 columns (P in the first 32 of each), O 128
@@ -75,7 +80,7 @@ struct Lay {
   static constexpr int RAWS = RAW + 2 * RK * HALF; // the two scales (16 bytes) of each K slot's page
   static constexpr int AUX = RAWS + RK * 16;     // 8 pages x (s_k, s_v, log2 s_v, 1 / s_v); the tail's 64 K and 64 V scales
   static constexpr int BARS = AUX + 8 * 16 + 512;
-  static constexpr int MISC = BARS + 48 * 8;     // TMEM base, flags, the plan's sums (16 warps), walk and job
+  static constexpr int MISC = BARS + 48 * 8;     // TMEM base, flags, units of all runs, walk and job
   static constexpr int JOIN = RAW;               // NT = 1: (m, E, l) of stream 1's rows, once the task's copies are done with
   static constexpr int BYTES = MISC + 80 + 144 + 1024;  // with the alignment
 };
@@ -104,6 +109,7 @@ struct Walk {
   int b, h, grp, pages, t0, t1;  // no pages are ours where the run begins behind them
   uint32_t u, u1;                // the task's first unit of ours, the run's end
   uint32_t units;                // ours of the task
+  int uncut;                     // a task is one unit
   Kv8Seq s;
   Span sp;
 };
@@ -157,8 +163,8 @@ template <int NT>
 __device__ __noinline__ void enter(const Kv8AttnArgs& a, Walk& k, uint32_t total, Job& j) {
   k.sp = span_of<NT>(k.s, a.G, a.window, k.grp);
   k.pages = pages_of(k.sp);
-  k.units = min(static_cast<uint32_t>(k.pages + TASK_UNITS<NT> - k.t0), k.u1 - k.u);
-  k.t1 = min(k.pages, k.t0 + static_cast<int>(k.units));
+  k.units = k.uncut ? 1u : min(static_cast<uint32_t>(k.pages + TASK_UNITS<NT> - k.t0), k.u1 - k.u);
+  k.t1 = k.uncut ? k.pages : min(k.pages, k.t0 + static_cast<int>(k.units));
   const uint32_t parts = min(total, gridDim.x), run = total / parts, more = total - run * parts;
   // the first `more` runs have a unit more than the others
   auto cta_of = [&](uint32_t u) { return u < more * (run + 1) ? u / (run + 1) : more + (u - more * (run + 1)) / run; };
@@ -175,7 +181,7 @@ __device__ __noinline__ void enter(const Kv8AttnArgs& a, Walk& k, uint32_t total
   j.head = k.t0 == 0;
   j.whole = j.nt == k.pages;
   j.c0 = cta_of(k.u - k.t0);
-  j.c1 = cta_of(k.u - k.t0 + k.pages - 1);
+  j.c1 = k.uncut ? j.c0 : cta_of(k.u - k.t0 + k.pages - 1);
 }
 // The run's next task, or none (j.nt = 0).
 template <int NT>
@@ -210,67 +216,87 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
   uint64_t* drain = bars + 44;
   uint32_t& tmem_sh = *reinterpret_cast<uint32_t*>(sm + L::MISC);
   int* flags = reinterpret_cast<int*>(sm + L::MISC + 4);                  // stop, last
-  uint32_t* sums = reinterpret_cast<uint32_t*>(sm + L::MISC + 16);        // [warps]
+  uint32_t& units_all = *reinterpret_cast<uint32_t*>(sm + L::MISC + 16); // of all runs
   Walk& walk = *reinterpret_cast<Walk*>(sm + L::MISC + 80);
   Job& job = *reinterpret_cast<Job*>(sm + L::MISC + 80 + sizeof(Walk));
   static_assert(sizeof(Walk) + sizeof(Job) <= 144, "their place");
   float* joined = reinterpret_cast<float*>(sm + L::JOIN);                 // [3][TR]
-  uint32_t* prefix = reinterpret_cast<uint32_t*>(sm + L::Q);  // units of the sequences before b, of one kv head: until the queries come
-  static_assert(HQ_KV8_MAX_BATCH * 4 <= 32768, "the plan fits where the queries go");
+  uint64_t* prefix = reinterpret_cast<uint64_t*>(sm + L::Q);  // the plan, until the queries come
+  uint64_t* plan = prefix + HQ_KV8_MAX_BATCH;                 // sums and maxima of each warp
+  static_assert((HQ_KV8_MAX_BATCH + 32) * 8 <= 32768, "the plan fits where the queries go");
   const hq_kv8_cache& c = a.c;
   const int B = c.B;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // the roles' branches are uniform
 
   // ---------------------------------------------------------------- plan
   chained();
-  uint32_t carry = 0;
+  // prefix[b]: units (of one kv head) of the sequences before b, in the low half, and
+  // their tasks in the high half
+  uint64_t carry = 0;
+  int longest = 0;
   for (int b0 = 0; b0 < B; b0 += THREADS) {
     const int b = b0 + threadIdx.x;
-    uint32_t n = 0;
+    uint64_t n = 0;
+    int top = 0;
     if (b < B) {
       Kv8Seq s;
       kv8_seq(c, a.cu, a.kv_len, a.N, a.max_new, b, blockIdx.x == 0, s);
       const int groups = (s.n * a.G + ROWS - 1) / ROWS;
-      for (int i = 0; i < groups; ++i) n += pages_of(span_of<NT>(s, a.G, a.window, i)) + TASK_UNITS<NT>;
+      for (int i = 0; i < groups; ++i) {
+        const int pages = pages_of(span_of<NT>(s, a.G, a.window, i));
+        n += 1ull << 32 | static_cast<uint32_t>(pages + TASK_UNITS<NT>);
+        top = max(top, pages);
+      }
     }
-    uint32_t x = n;
+    uint64_t x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) sums[warp] = x;
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 31) {
+      plan[warp] = x;
+      plan[16 + warp] = top;
+    }
     __syncthreads();
-    uint32_t before = carry;
+    uint64_t before = carry;
     for (int w = 0; w < THREADS / 32; ++w) {
-      if (w < warp) before += sums[w];
-      carry += sums[w];
+      if (w < warp) before += plan[w];
+      carry += plan[w];
+      longest = max(longest, static_cast<int>(plan[16 + w]));
     }
     if (b < B) prefix[b] = before + x - n;
     __syncthreads();
   }
   if (threadIdx.x == 0) {
-    const uint32_t total = carry * c.Hkv, parts = min(total, gridDim.x);
+    // the units that are dealt out: pages and what a task costs besides them, or whole tasks
+    const uint32_t tasks = static_cast<uint32_t>(carry >> 32) * c.Hkv;
+    const uint32_t pages = static_cast<uint32_t>(carry) * c.Hkv - tasks * TASK_UNITS<NT>;
+    const bool uncut = tasks <= gridDim.x && longest <= UNCUT + static_cast<int>(pages / gridDim.x);
+    auto half = [&](uint64_t x) { return uncut ? static_cast<uint32_t>(x >> 32) : static_cast<uint32_t>(x); };
+    const uint32_t total = half(carry) * c.Hkv, parts = min(total, gridDim.x);
     job.nt = 0;
     if (blockIdx.x < parts) {
       const uint32_t run = total / parts, more = total - run * parts;
       Walk k;
+      k.uncut = uncut;
       k.u = run * blockIdx.x + min(blockIdx.x, more);
       k.u1 = k.u + run + (blockIdx.x < more);
       const uint32_t want = k.u / c.Hkv;
       int lo = 0, hi = B;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= want) lo = mid; else hi = mid;
+        if (half(prefix[mid]) <= want) lo = mid; else hi = mid;
       }
       k.b = lo;
       kv8_seq(c, a.cu, a.kv_len, a.N, a.max_new, lo, false, k.s);
-      const uint32_t each = (lo + 1 < B ? prefix[lo + 1] : carry) - prefix[lo];  // units of a kv head
-      uint32_t rel = k.u - prefix[lo] * c.Hkv;
+      const uint32_t each = half(lo + 1 < B ? prefix[lo + 1] : carry) - half(prefix[lo]);  // units of a kv head
+      uint32_t rel = k.u - half(prefix[lo]) * c.Hkv;
       k.h = rel / each;
       rel -= k.h * each;
       for (k.grp = 0;; ++k.grp) {
-        const uint32_t n = pages_of(span_of<NT>(k.s, a.G, a.window, k.grp)) + TASK_UNITS<NT>;
+        const uint32_t n = uncut ? 1u : pages_of(span_of<NT>(k.s, a.G, a.window, k.grp)) + TASK_UNITS<NT>;
         if (rel < n) break;
         rel -= n;
       }
@@ -278,7 +304,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       enter<NT>(a, k, total, job);
       if (job.nt == 0) next_task<NT>(a, k, total, job);  // the run begins behind a task's pages
       walk = k;
-      sums[0] = total;
+      units_all = total;
     }
   }
   __syncthreads();
@@ -822,7 +848,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
     __syncthreads();  // the task's shared and tensor memory is free
     tc_fence_after();
     if (threadIdx.x == 0) {
-      next_task<NT>(a, walk, sums[0], job);
+      next_task<NT>(a, walk, units_all, job);
       if (*stop) job.nt = 0;
     }
     __syncthreads();
