@@ -608,8 +608,8 @@ def test_refusals_of_the_binding():
 @pytest.mark.parametrize("fmt,dtype", FORMS)
 @pytest.mark.parametrize("G,n", [(8, 3), (5, 5), (2, 13), (8, 16), (1, 129), (3, 43), (2, 128), (1, 257), (16, 17), (7, 40)])
 def test_row_counts_around_the_kernels_borders(fmt, dtype, G, n):
-    """24 and 25 rows of a kv head (the tcgen05 kernel begins), 128 and 129 (its second row tile), 256 and more (further
-    tasks), with sequences of fewer rows beside."""
+    """24 and 25 rows of a kv head (a second task), 128 and 129 (the tcgen05 kernel's second row tile), 256 and more
+    (further tasks), with sequences of fewer rows beside."""
     p = Pair(3, 2, 640, fmt, dtype, seed=32)
     p.append([600, max(n, 129), 300])
     p.attend(G, [n, n, max(1, n // 3)])
