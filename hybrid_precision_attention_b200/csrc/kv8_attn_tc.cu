@@ -30,8 +30,8 @@
 // exponentials and, at 128 bytes a cycle, 3000 of shared memory (256 KB of
 // operands, 64 KB converted, 64 KB of codes in and out).
 // Measured: the last 2048 tokens of 16K, 32 query heads over 8: 469 us in a short run,
-// 1100 TFLOP/s, 564 us, 913 TFLOP/s, where runs go on and power bounds the clock; 64
-// sequences x 8 tokens x 8 query heads a kv head over 1K-8K: 303 us, one row tile of 64 rows.
+// 1100 TFLOP/s, 550 us, 936 TFLOP/s, where runs go on and power bounds the clock; 64
+// sequences x 8 tokens x 8 query heads a kv head over 1K-8K: 300 us, one row tile of 64 rows.
 //
 // Work: runs of equal units (pages) as in kv8_attn.cu; pieces of a task that
 // CTAs share are joined by the CTA that delivers the last one, in order.
