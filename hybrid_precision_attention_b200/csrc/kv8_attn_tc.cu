@@ -509,11 +509,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           }
           if (!VAL) {
             if (ct == 0) *reinterpret_cast<float4*>(aux + (T & 7) * 4) = make_float4(1.f, 1.f, 0.f, 1.f);
-            // the rows' scales; past the length 1: nothing there is seen
+            // the rows' scales; past the length nothing is seen, and no value counts for a reference
             const float* ts = c.tail_scale + bh * 2 * HQ_KV8_TAIL + half * KV8_BLOCK + ct;
             const bool in = (page0 + full) * KV8_BLOCK + ct < job.len;
             tail_sc[ct] = in ? ts[0] : 1.0f;
-            tail_sc[64 + ct] = in ? ts[HQ_KV8_TAIL] : 1.0f;
+            tail_sc[64 + ct] = in ? ts[HQ_KV8_TAIL] : 0.0f;
           }
           fence_proxy_async_smem();
           mbar_arrive(st_full + st);
@@ -619,12 +619,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
         };
         // The references anew, from the exact maximum of the page; sum and O are rescaled.
         auto renew = [&]() {
-          float vtop = tail ? 0.f : fmaxf(sc.y, 0.f);  // ignores NaN
-          if (tail)
-            for (int i = 0; i < 64; ++i) vtop = fmaxf(vtop, tail_sc[64 + i]);
-          if (!(vtop > 0.f)) vtop = 1.f;
           load();
-          float mt = -INFINITY;
+          float mt = -INFINITY, et = -INFINITY;  // largest score, largest score + log2(value scale); NaN is passed over
           if (seen) {
 #pragma unroll
             for (int i = 0; i < 64; ++i) mt = fmaxf(mt, x[i] * mul);
@@ -633,7 +629,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < 64; ++i) mt = fmaxf(mt, x[i]);
           }
-          const float m_new = fmaxf(m, mt), e_new = fmaxf(e, mt + log2f(vtop));
+          if (tail) {
+            // each position has its own scale: those that the row does not see are at -inf
+#pragma unroll
+            for (int i = 0; i < 64; ++i) et = fmaxf(et, x[i] + lg2_approx(tail_sc[64 + i]));
+          } else {
+            et = mt + log2f(sc.y > 0.f ? sc.y : 1.f);
+          }
+          const float m_new = fmaxf(m, mt), e_new = fmaxf(e, et);
           const float mb = m_new == -INFINITY ? 0.f : m_new, eb = e_new == -INFINITY ? 0.f : e_new;
           const float ao = ex2(e - eb);
           l *= ex2(m - mb);

@@ -795,3 +795,46 @@ def test_read_back_installs_a_hybrid_cache():
     st = h.state()
     assert st["T"] == 400 and st["err"] == 0
     assert torch.equal(h.kr[0, :, 399 % h.R], K[0, :, 399]) and torch.equal(h.vr[0, :, 399 % h.R], V[0, :, 399])
+
+
+# ----------------------------------------------------------------------------- values of any magnitude
+
+# half the smallest number of the output's type: where the outputs themselves are small, check_rows' 2^-25 would pass anything
+TINY = {"f16": 2.0 ** -25, "bf16": 2.0 ** -134}
+
+
+def check_relative(p, b, q, out, sm=128 ** -0.5, window=0):
+    """check_rows' bound on the output, relative to sum p |v| alone."""
+    want, _, mass, size = p.ref[b].attend(q.double().cpu().numpy(), sm, window)
+    got = out.double().cpu().numpy()
+    tol = torch.finfo(TYPES[p.dtype]).eps / 2 * np.abs(want) + (2.0 ** -11 + 2.0 ** -15 + 3 * 2.0 ** -18 * size[..., None]) * mass + TINY[p.dtype]
+    err = np.abs(got - want)
+    assert (err <= tol).all(), (err / tol).max()
+
+
+# rows of a kv head: one task of the first kernel, two of them, one row tile of the second, two tiles
+ROWS = [(4, 1), (4, 5), (8, 5), (8, 8), (8, 32)]
+
+
+@pytest.mark.parametrize("G,n", ROWS)
+@pytest.mark.parametrize("L", [40, 63, 65, 100])
+def test_an_incomplete_block_of_small_values(G, n, L):
+    """bf16 rows of the 16-bit tail stand at a scale of their own, far below 1: positions past the length, and those that
+    a query does not see yet, leave no trace in the weights' reference."""
+    for window in (0, 20):
+        for size in (1e-2, 1e-3, 1e-4, 1e-6, 1e-20):
+            p = Pair(1, 1, 256, "e4m3", "bf16", seed=43)
+            k, v = p.rows(L), p.rows(L).double() * size
+            p.append([L], k=k, v=v.bfloat16())
+            q, out, _ = p.attend(G, [n], window=window, check=False)
+            check_relative(p, 0, q, out, window=window)
+
+
+@pytest.mark.parametrize("G,n", [(8, 8), (8, 32)])
+def test_new_tokens_of_unlike_size(G, n):
+    """Each token's values are 4 times the one's before: what a query does not see yet is far above what it sees."""
+    p = Pair(1, 1, 256, "e4m3", "bf16", seed=44)
+    v = p.rows(40).double() * 2.0 ** (2.0 * (torch.arange(40) - 29))[:, None, None]
+    p.append([40], k=p.rows(40), v=v.bfloat16())
+    q, out, _ = p.attend(G, [n], check=False)
+    check_relative(p, 0, q, out)
