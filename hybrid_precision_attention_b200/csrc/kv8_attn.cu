@@ -60,6 +60,10 @@ namespace {
 constexpr float P_BIAS = 6.0f;     // log2 of the fp16 weight at both references
 constexpr float P_SLACK = 8.0f;    // how far (log2) a score may pass m
 constexpr float V_LIMIT = 128.0f;  // 2^(P_BIAS + 1): how far a value scale may pass its reference; 2^8 * 2^7 < 65504
+// log2 of the largest factor of weights, 2^(m - E + P_BIAS): E stays above m + P_BIAS - P_TOP, so that the factor and
+// the inverse that undoes it at the end are both normal numbers (value scales below 2^(P_BIAS - P_TOP) then give
+// smaller weights), and a weight that underflowed stays 0 beside a far larger earlier score
+constexpr float P_TOP = 120.0f;
 constexpr int TASK_UNITS = 12;     // what a task costs besides its blocks, in blocks (about 6000 cycles of 500 each)
 constexpr int OS = D + 4;          // row stride (floats) of accumulators in shared memory: 4 rows of a store step 8 banks apart
 
@@ -478,14 +482,13 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-            const float m_new = fmaxf(m_run[nb][i], mt), e_new = fmaxf(e_run[nb][i], mt + lv);
+            const float m_new = fmaxf(m_run[nb][i], mt), e_new = fmaxf(fmaxf(e_run[nb][i], mt + lv), m_new + (P_BIAS - P_TOP));
             const float mb = m_new == -INFINITY ? 0.f : m_new, eb = e_new == -INFINITY ? 0.f : e_new;
             l_run[nb][i] *= ex2(m_run[nb][i] - mb);
             ao[i] = ex2(e_run[nb][i] - eb);
             m_run[nb][i] = m_new;
             e_run[nb][i] = e_new;
-            // bounded, so that a weight that underflowed stays 0 beside a far larger earlier score
-            ef[nb][i] = e_new == -INFINITY ? 0.f : ex2(fminf(mb - eb + P_BIAS, 100.f));
+            ef[nb][i] = e_new == -INFINITY ? 0.f : ex2(mb - eb + P_BIAS);
           }
 #pragma unroll
           for (int d = 0; d < 8; ++d)
@@ -642,10 +645,10 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
       const int rr = k.row0 + r;
       if (rr >= rows) return;
       // accumulators are at 2^(P_BIAS - E), the sum at 2^-m: the quotient's exponent
-      const float f = m == -INFINITY ? 0.f : ex2(e - m - P_BIAS) / l;
+      const float f = m == -INFINITY ? 0.f : ex2(e - m - P_BIAS), inv = 1.0f / l;
       const int64_t tok = k.s.row0 + rr / a.G;
       const int head = k.h * a.G + rr % a.G;
-      E y[4] = {from_float<E>(x.x * f), from_float<E>(x.y * f), from_float<E>(x.z * f), from_float<E>(x.w * f)};
+      E y[4] = {from_float<E>(x.x * inv * f), from_float<E>(x.y * inv * f), from_float<E>(x.z * inv * f), from_float<E>(x.w * inv * f)};
       *reinterpret_cast<uint2*>(static_cast<E*>(a.out) + tok * a.o_tok + head * a.o_head + 4 * lane) =
           *reinterpret_cast<const uint2*>(y);
       if (a.lse != nullptr && lane == 0) a.lse[tok * a.Hq + head] = m + log2f(l);

@@ -52,6 +52,7 @@ constexpr int STAGES = 4;                  // pages of K, and of V, as operands
 constexpr int W_CONV = 8, W_COPY = 12, W_MMA = 14;  // W_COPY: K, W_COPY + 1: V; W_MMA + stream
 constexpr int THREADS = 16 * 32;
 constexpr float BIAS = 6.0f;               // log2 of the fp16 weight at both references
+constexpr float W_TOP = 120.0f;            // of the factor 2^(m - E + BIAS): E stays above m + BIAS - W_TOP (kv8_attn.cu, P_TOP)
 constexpr float W_LIMIT = 32768.0f;        // sum of a page's fp16 weights above which the references are set anew
 // what a task costs besides its pages, in pages (some 16000 cycles, two thirds of them
 // queries, epilogue and the first and last pages' latencies)
@@ -636,14 +637,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           } else {
             et = mt + log2f(sc.y > 0.f ? sc.y : 1.f);
           }
-          const float m_new = fmaxf(m, mt), e_new = fmaxf(e, et);
+          const float m_new = fmaxf(m, mt), e_new = fmaxf(fmaxf(e, et), m_new + (BIAS - W_TOP));
           const float mb = m_new == -INFINITY ? 0.f : m_new, eb = e_new == -INFINITY ? 0.f : e_new;
           const float ao = ex2(e - eb);
           l *= ex2(m - mb);
           m = m_new;
           e = e_new;
-          // bounded, so that a weight that underflowed stays 0 beside a far larger earlier score
-          lef = e_new == -INFINITY ? -INFINITY : fminf(mb - eb + BIAS, 100.f);
+          lef = e_new == -INFINITY ? -INFINITY : mb - eb + BIAS;
           ref = e_new == -INFINITY ? 0.f : ex2(-lef);
           if (taken > 1) {
             // the page before may still be being added
@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       const float f1 = ej == -INFINITY ? 1.f : ex2(e - eb), f2 = ej == -INFINITY ? 1.f : ex2(e2 - eb);
       auto write = [&](float m, float e, float l, auto cols) {  // the row's output from its accumulators
         // accumulators are at 2^(BIAS - E), the sum at 2^-m
-        const float f = m == -INFINITY ? 0.f : ex2(e - m - BIAS) / l;
+        const float f = m == -INFINITY ? 0.f : ex2(e - m - BIAS), inv = 1.0f / l;
         const int64_t tok = job.tok0 + rr / a.G;
         const int head = job.h * a.G + rr % a.G;
         E* dst = static_cast<E*>(a.out) + tok * a.o_tok + head * a.o_head;
@@ -784,7 +784,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
             for (int i = 0; i < 32; i += 8) {
               E y[8];
 #pragma unroll
-              for (int z = 0; z < 8; ++z) y[z] = from_float<E>(x[i + z] * f);
+              for (int z = 0; z < 8; ++z) y[z] = from_float<E>(x[i + z] * inv * f);
               *reinterpret_cast<uint4*>(dst + 32 * c4 + i) = *reinterpret_cast<const uint4*>(y);
             }
           }

@@ -804,10 +804,32 @@ TINY = {"f16": 2.0 ** -25, "bf16": 2.0 ** -134}
 
 
 def check_relative(p, b, q, out, sm=128 ** -0.5, window=0):
-    """check_rows' bound on the output, relative to sum p |v| alone."""
-    want, _, mass, size = p.ref[b].attend(q.double().cpu().numpy(), sm, window)
+    """check_rows' bound on the output, relative to sum p |v| alone, with the weights' smallest step.
+
+    A weight w_j = p_j s_j (s_j the scale of key j's value, c_j = v_j / s_j what the product takes) is rounded to fp16 at
+    2^6 / E, E the reference of such weights, at most their largest (it is set to the largest met so far, and otherwise
+    stays).  Below 2^-14 the step of fp16 is 2^-24 whatever the weight, its half 2^-25 = 2^-31 E: the sum over j of that
+    times |c_j|, 2^-31 max_j w_j sum_j |c_j|, is beyond what 2^-11 of each weight counts.  It tells only where values of
+    one channel lie below the others' by more than the weights' 2^20.  s_j is the block's scale, and for 16-bit rows
+    between 2^-15 and 2^-14 of the row's largest value: the larger counts in w_j, the smaller in c_j."""
+    ref, q = p.ref[b], q.double().cpu().numpy()
+    want, _, mass, size = ref.attend(q, sm, window)
     got = out.double().cpu().numpy()
-    tol = torch.finfo(TYPES[p.dtype]).eps / 2 * np.abs(want) + (2.0 ** -11 + 2.0 ** -15 + 3 * 2.0 ** -18 * size[..., None]) * mass + TINY[p.dtype]
+    K, V = ref.cached(0), ref.cached(1)
+    scale = ref.blocks(1)[1].astype(np.float64).repeat(64, axis=-1)
+    top = np.abs(V[:, scale.shape[1]:]).max(-1)
+    large, small = np.concatenate((scale, top * 2.0 ** -14), 1), np.concatenate((scale, top * 2.0 ** -15), 1)
+    code = np.abs(V) / np.where(small == 0, 1, small)[..., None]
+    n, Hq, _ = q.shape
+    G, step = Hq // K.shape[0], np.zeros_like(want)
+    for i in range(n):
+        t = ref.len - n + i
+        lo = max(0, t - window + 1) if window > 0 else 0
+        for h in range(Hq):
+            s = K[h // G, lo:t + 1] @ q[i, h] * sm
+            w = np.exp(s - s.max())
+            step[i, h] = 2.0 ** -31 * (w * large[h // G, lo:t + 1]).max() / w.sum() * code[h // G, lo:t + 1].sum(0)
+    tol = torch.finfo(TYPES[p.dtype]).eps / 2 * np.abs(want) + (2.0 ** -11 + 2.0 ** -15 + 3 * 2.0 ** -18 * size[..., None]) * mass + step + TINY[p.dtype]
     err = np.abs(got - want)
     assert (err <= tol).all(), (err / tol).max()
 
@@ -838,3 +860,23 @@ def test_new_tokens_of_unlike_size(G, n):
     p.append([40], k=p.rows(40), v=v.bfloat16())
     q, out, _ = p.attend(G, [n], check=False)
     check_relative(p, 0, q, out)
+
+
+@pytest.mark.parametrize("G,n", ROWS)
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_values_at_the_ends_of_float32(G, n, fmt):
+    """Values whose scales lie at 2^-117 and above (bf16): the factor that the weights take and what undoes it agree."""
+    for L in (320, 350):
+        for e in (60, -80, -95, -104):
+            p = Pair(1, 1, 384, fmt, "bf16", seed=45)
+            k, v = p.rows(L), p.rows(L).double() * 2.0 ** e
+            p.append([L], k=k, v=v.bfloat16())
+            q, out, _ = p.attend(G, [n], check=False)
+            check_relative(p, 0, q, out)
+    # blocks and rows from one end to the other, the newest the smallest
+    p = Pair(1, 1, 384, fmt, "bf16", seed=46)
+    v = p.rows(350).double() * 2.0 ** (-20.0 * (torch.arange(350) // 64))[:, None, None]
+    p.append([350], k=p.rows(350), v=v.bfloat16())
+    for window in (0, 20):
+        q, out, _ = p.attend(G, [n], window=window, check=False)
+        check_relative(p, 0, q, out, window=window)
