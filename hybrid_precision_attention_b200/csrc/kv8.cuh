@@ -130,6 +130,35 @@ __device__ __forceinline__ bool kv8_seq(const hq_kv8_cache& c, const int32_t* cu
   return true;
 }
 
+// Rows of the 16-bit tail enter the value product at a power of two that brings their largest
+// value to [2^14, 2^15), as bf16 rows are stored (exact: fp16 rows only go up), and the weight
+// takes its inverse: a weight's fp16 range is then spent on the row's own magnitude, and a row
+// of zeros has no weight at all.  From the bits of the row's largest magnitude (finite):
+__device__ __forceinline__ int kv8_tail_shift(uint32_t top) { return max(0, 29 - max(static_cast<int>(top >> 10), 1)); }
+__device__ __forceinline__ float kv8_tail_vscale(float scale, uint32_t top) {  // NaN stays
+  if (top == 0) return scale == scale ? 0.f : scale;
+  return scale * __uint_as_float(static_cast<uint32_t>(127 - kv8_tail_shift(top)) << 23);
+}
+// two rows' values times 2^shift, in two steps, for 2^28 is no fp16; tops: their largest magnitudes
+struct TailUp {
+  __half2 a, b;
+  __device__ __forceinline__ explicit TailUp(uint32_t tops) {
+    const int x = kv8_tail_shift(tops & 0x7fffu), y = kv8_tail_shift(tops >> 16 & 0x7fffu);
+    auto pow2 = [](int k) { return __ushort_as_half(static_cast<unsigned short>((k + 15) << 10)); };
+    a = __halves2half2(pow2(min(x, 15)), pow2(min(y, 15)));
+    b = __halves2half2(pow2(max(x - 15, 0)), pow2(max(y - 15, 0)));
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t w) const {
+    const __half2 r = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&w), a), b);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+};
+// larger magnitudes of two pairs
+__device__ __forceinline__ uint32_t kv8_top2(uint32_t x, uint32_t y) {
+  const __half2 r = __hmax2(__habs2(*reinterpret_cast<const __half2*>(&x)), __habs2(*reinterpret_cast<const __half2*>(&y)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // Arguments of the attention kernels (strides in elements).
 struct Kv8AttnArgs {
   hq_kv8_cache c;

@@ -422,11 +422,11 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
         for (int i = 0; i < 4; ++i) o[nb][mt][i] = 0.f;
 
     // NT 16-token tiles: kf, vf give the A operands of step s / output rows 16 d
-    // .. 16 d + 15 of tile j; ks, vs the scales of its tokens g, g + 8 (vtop: the
-    // largest vs of all); pos the first token's position
-    auto tiles = [&](auto count, auto masked, auto kf, auto vf, const float (&ks)[2], const float (&vs)[2], float vtop, int pos) {
+    // .. 16 d + 15 of tile j; ks, vs the scales of its tokens g, g + 8 (`own`: of each token its
+    // own, else the same of all); pos the first token's position
+    auto tiles = [&](auto count, auto masked, auto own, auto kf, auto vf, const float (&ks)[2], const float (&vs)[2], int pos) {
       constexpr int NT = decltype(count)::value;
-      constexpr bool MASK = decltype(masked)::value;
+      constexpr bool MASK = decltype(masked)::value, OWN = decltype(own)::value;
       float sc[NT][NB][4];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -450,10 +450,10 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
             mma16816(sc[j][nb], f[0], f[1], f[2], f[3], s & 1 ? qw[nb].z : qw[nb].x, s & 1 ? qw[nb].w : qw[nb].y);
         }
       }
-      bool far = false;
+      bool far = OWN;  // the first of the task's
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        far |= fmaxf(ef[nb][0], ef[nb][1]) * vtop > V_LIMIT;
+        if (!OWN) far |= fmaxf(ef[nb][0], ef[nb][1]) * vs[0] > V_LIMIT;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float mul = qs[nb][i & 1] * ks[i >> 1];
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
         }
       }
       if (__any_sync(0xffffffffu, far)) {
-        const float lv = log2f(vtop);
+        const float lv[2] = {log2f(vs[0]), log2f(vs[1])};
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           float ao[2];
@@ -482,7 +482,16 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-            const float m_new = fmaxf(m_run[nb][i], mt), e_new = fmaxf(fmaxf(e_run[nb][i], mt + lv), m_new + (P_BIAS - P_TOP));
+            float et = mt + lv[0];  // the largest score + log2(value scale) of what the row sees; NaN is passed over
+            if (OWN) {
+              et = -INFINITY;
+#pragma unroll
+              for (int j = 0; j < NT; ++j) et = fmaxf(et, fmaxf(sc[j][nb][i] + lv[0], sc[j][nb][2 + i] + lv[1]));
+              et = fmaxf(et, __shfl_xor_sync(0xffffffffu, et, 4));
+              et = fmaxf(et, __shfl_xor_sync(0xffffffffu, et, 8));
+              et = fmaxf(et, __shfl_xor_sync(0xffffffffu, et, 16));
+            }
+            const float m_new = fmaxf(m_run[nb][i], mt), e_new = fmaxf(fmaxf(e_run[nb][i], et), m_new + (P_BIAS - P_TOP));
             const float mb = m_new == -INFINITY ? 0.f : m_new, eb = e_new == -INFINITY ? 0.f : e_new;
             l_run[nb][i] *= ex2(m_run[nb][i] - mb);
             ao[i] = ex2(e_run[nb][i] - eb);
@@ -551,17 +560,26 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
         }
         const bool in0 = pos + g < k.s.len, in1 = pos + g + 8 < k.s.len;
         const float ks[2] = {in0 ? ts[0] : 1.f, in1 ? ts[8] : 1.f};
-        const float vs[2] = {in0 ? ts[HQ_KV8_TAIL] : 0.f, in1 ? ts[HQ_KV8_TAIL + 8] : 0.f};
+        float vs[2] = {in0 ? ts[HQ_KV8_TAIL] : 0.f, in1 ? ts[HQ_KV8_TAIL + 8] : 0.f};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           *reinterpret_cast<uint4*>(&vw[i][0]) = tv[(i * 32 + lane) * 2];
           *reinterpret_cast<uint4*>(&vw[i][4]) = tv[(i * 32 + lane) * 2 + 1];
         }
-        float vtop = fmaxf(vs[0], vs[1]);  // ignores NaN
-        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 4));
-        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 8));
-        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 16));
-        if (!(vtop > 0.f)) vtop = 1.f;
+        // the largest magnitudes of tokens 2 t4, 2 t4 + 1 (even words) and of those 8 behind (odd words)
+        uint32_t top[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) top[i & 1] = kv8_top2(top[i & 1], vw[i / 8][i % 8]);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+#pragma unroll
+          for (int o = 4; o < 32; o *= 2) top[z] = kv8_top2(top[z], __shfl_xor_sync(0xffffffffu, top[z], o));
+          const TailUp up(top[z]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) vw[i / 4][i % 4 * 2 + z] = up(vw[i / 4][i % 4 * 2 + z]);
+          // of token g (+ 8): with the lanes whose t4 is g / 2
+          vs[z] = kv8_tail_vscale(vs[z], __shfl_sync(0xffffffffu, top[z], g >> 1) >> (g & 1) * 16 & 0x7fffu);
+        }
         auto kf = [&](int, int s, uint32_t (&f)[4]) {
           f[0] = kw[s >> 2][(s & 3) * 2];
           f[2] = kw[s >> 2][(s & 3) * 2 + 1];
@@ -575,7 +593,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
           f[1] = vw[d >> 1][w + 2];
           f[3] = vw[d >> 1][w + 3];
         };
-        tiles(std::integral_constant<int, 1>{}, std::true_type{}, kf, vf, ks, vs, vtop, pos);
+        tiles(std::integral_constant<int, 1>{}, std::true_type{}, std::true_type{}, kf, vf, ks, vs, pos);
       }
     }
 
@@ -610,9 +628,9 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
       constexpr std::integral_constant<int, MT> all{};
       // seen whole by every row?
       if (pos + 16 * MT - 1 <= q_lo && (a.window <= 0 || pos > q_hi - a.window))
-        tiles(all, std::false_type{}, kf, vf, ks, vs, sc.y, pos);
+        tiles(all, std::false_type{}, std::false_type{}, kf, vf, ks, vs, pos);
       else
-        tiles(all, std::true_type{}, kf, vf, ks, vs, sc.y, pos);
+        tiles(all, std::true_type{}, std::false_type{}, kf, vf, ks, vs, pos);
       release();
     }
 

@@ -501,20 +501,42 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           if (T >= STAGES && !await(st_empty + st, T / STAGES - 1)) return;
           const uint32_t dst = base + (VAL ? L::V : L::K) + st * 16384;
           const uint4* src = reinterpret_cast<const uint4*>((VAL ? c.tail_v : c.tail_k) + (bh * 2 + half) * KV8_BLOCK * D);
-#pragma unroll 2
-          for (int i = 0; i < 8; ++i) {
-            uint32_t y[8];
-            *reinterpret_cast<uint4*>(y) = src[((cw * 8 + i) * 32 + lane) * 2];
-            *reinterpret_cast<uint4*>(y + 4) = src[((cw * 8 + i) * 32 + lane) * 2 + 1];
-            put(dst, cw * 8 + i, y);
+          const float* ts = c.tail_scale + (bh * 2 + VAL) * HQ_KV8_TAIL + half * KV8_BLOCK;
+          const int held = job.len - (page0 + full) * KV8_BLOCK;  // rows of the block
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i) {
+            uint32_t y[4][8];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int e = cw * 8 + i * 4 + w;
+              *reinterpret_cast<uint4*>(y[w]) = src[(e * 32 + lane) * 2];
+              *reinterpret_cast<uint4*>(y[w] + 4) = src[(e * 32 + lane) * 2 + 1];
+            }
+            if (VAL) {
+              // the 16 rows at their own magnitude; past the length nothing is seen, and no value counts for a reference
+              const int r0 = (cw * 2 + i) * 16 + 2 * t4;
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {  // rows r0, r0 + 1; those 8 behind
+                uint32_t top = 0;
+#pragma unroll
+                for (int w = 0; w < 16; ++w) top = kv8_top2(top, y[w / 4][w % 4 * 2 + z]);
+#pragma unroll
+                for (int o = 4; o < 32; o *= 2) top = kv8_top2(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const TailUp up(top);
+#pragma unroll
+                for (int w = 0; w < 16; ++w) y[w / 4][w % 4 * 2 + z] = up(y[w / 4][w % 4 * 2 + z]);
+                if (g < 2) {
+                  const int r = r0 + 8 * z + g;
+                  tail_sc[64 + r] = r < held ? kv8_tail_vscale(ts[r], top >> g * 16 & 0x7fffu) : 0.0f;
+                }
+              }
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) put(dst, cw * 8 + i * 4 + w, y[w]);
           }
           if (!VAL) {
             if (ct == 0) *reinterpret_cast<float4*>(aux + (T & 7) * 4) = make_float4(1.f, 1.f, 0.f, 1.f);
-            // the rows' scales; past the length nothing is seen, and no value counts for a reference
-            const float* ts = c.tail_scale + bh * 2 * HQ_KV8_TAIL + half * KV8_BLOCK + ct;
-            const bool in = (page0 + full) * KV8_BLOCK + ct < job.len;
-            tail_sc[ct] = in ? ts[0] : 1.0f;
-            tail_sc[64 + ct] = in ? ts[HQ_KV8_TAIL] : 0.0f;
+            tail_sc[ct] = ct < held ? ts[ct] : 1.0f;
           }
           fence_proxy_async_smem();
           mbar_arrive(st_full + st);
@@ -605,6 +627,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
         };
         load();
         const bool tail = t >= full;
+        if (tail) {
+          // the converters of its values have the rows' scales
+          ok = wait_for(v_full + (n_page + t) % STAGES, (n_page + t) / STAGES & 1, err, stop);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
         const float4 sc = *reinterpret_cast<const float4*>(aux + ((n_page + t) & 7) * 4);  // s_k, s_v, log2 s_v, 1 / s_v
         // columns [lo, hi] of the page are seen by this row
         const int hi = real ? qpos - (page0 + t) * KV8_BLOCK : KV8_BLOCK, lo = real && a.window > 0 ? hi - a.window + 1 : 0;

@@ -880,3 +880,30 @@ def test_values_at_the_ends_of_float32(G, n, fmt):
     for window in (0, 20):
         q, out, _ = p.attend(G, [n], window=window, check=False)
         check_relative(p, 0, q, out, window=window)
+
+
+@pytest.mark.parametrize("G,n", ROWS)
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_zero_rows_beside_small_values(G, n, dtype):
+    """Rows of the 16-bit tail whose values are all zero (a padding token's) have no magnitude; fp16 rows, stored as they
+    are, have their own: neither sets the reference of the others' weights."""
+    for L, zero in ((40, [3, 39]), (100, [70]), (100, list(range(64, 99))), (65, [64]), (300, [256, 270]), (47, list(range(47)))):
+        for size in (1e-1, 1e-2, 1e-4, 1e-6) if dtype == "bf16" else (1.0, 1e-2, 1e-3):
+            p = Pair(1, 1, 384, "e4m3", dtype, seed=47)
+            k, v = p.rows(L), p.rows(L).double() * size
+            v[zero] = 0
+            p.append([L], k=k, v=v.to(TYPES[dtype]))
+            q, out, _ = p.attend(G, [n], check=False)
+            check_relative(p, 0, q, out)
+
+
+@pytest.mark.parametrize("G,n", ROWS)
+def test_not_finite_and_zero_rows_of_the_tail(G, n):
+    """A row that is not finite still marks what sees it where the others are zero or tiny."""
+    p = Pair(1, 1, 256, "e4m3", "bf16", seed=48)
+    k, v = p.rows(100), p.rows(100).double() * 1e-4
+    v[64:99] = 0
+    v[99, 0, 3] = float("nan")
+    p.append([100], k=k, v=v.bfloat16())
+    _, out, _ = p.attend(G, [n], check=False)
+    assert torch.isnan(out[-1]).all() and torch.isfinite(out[:-1]).all()
