@@ -606,7 +606,17 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
       uint4 kw[MT][4], vw[MT];  // the values from the slot as they are needed, for want of registers
 #pragma unroll
       for (int i = 0; i < 4 * MT; ++i) kw[i / 4][i % 4] = reinterpret_cast<const uint4*>(src + i * 512)[lane];
-      const float2 sc = *reinterpret_cast<const float2*>(src + 2 * SLICE);
+      float2 sc = *reinterpret_cast<const float2*>(src + 2 * SLICE);
+      if (sc.y == 1.0f) {
+        // the scale of a block of zeros, too, which says nothing of a magnitude: no weight, no part in the reference
+        uint32_t any = 0;
+#pragma unroll 1
+        for (int i = 0; i < 4 * MT; ++i) {
+          const uint4 w = reinterpret_cast<const uint4*>(src + SLICE + i * 512)[lane];
+          any |= w.x | w.y | w.z | w.w;
+        }
+        if (!__any_sync(0xffffffffu, (any & (FMT == HQ_KV8_E4M3 ? 0x7f7f7f7fu : 0xffffffffu)) != 0)) sc.y = 0.f;
+      }
       auto release = [&]() {
         __syncwarp();  // every lane has its part: the slot takes the next slice
         ++taken;

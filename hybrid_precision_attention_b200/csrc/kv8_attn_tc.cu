@@ -159,6 +159,18 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
+// Whether a page's value codes all stand for zero; a whole warp asks.
+template <int FMT>
+__device__ __noinline__ bool no_values(const uint8_t* codes) {
+  uint32_t any = 0;
+#pragma unroll 1
+  for (int i = threadIdx.x & 31; i < HALF / 16; i += 32) {
+    const uint4 w = reinterpret_cast<const uint4*>(codes)[i];
+    any |= w.x | w.y | w.z | w.w;
+  }
+  return !__any_sync(0xffffffffu, (any & (FMT == HQ_KV8_E4M3 ? 0x7f7f7f7fu : 0xffffffffu)) != 0);
+}
+
 // The run's task at k.u (k.t0 of its pages belong to the CTAs before).
 template <int NT>
 __device__ __noinline__ void enter(const Kv8AttnArgs& a, Walk& k, uint32_t total, Job& j) {
@@ -474,7 +486,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           uint4 x[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = src[i * 32];
-          const float2 sc = VAL ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(sm + L::RAWS + sl * 16);
+          float2 sc = VAL ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(sm + L::RAWS + sl * 16);
+          // also the scale of a block of zeros, which says nothing of a magnitude: no weight, no part in the reference
+          if (!VAL && cw == 0 && sc.y == 1.0f && no_values<FMT>(kv8_page(c, bh, page0 + t) + HQ_KV8_V)) sc.y = 0.f;
           mbar_arrive(slot_empty + sl);
           // The stage is free once the page four before has been scored (K) or added (V).
           // Scoring that page took the place of the one four before it in its stream at
@@ -663,7 +677,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < 64; ++i) et = fmaxf(et, x[i] + lg2_approx(tail_sc[64 + i]));
           } else {
-            et = mt + log2f(sc.y > 0.f ? sc.y : 1.f);
+            et = mt + sc.z;
           }
           const float m_new = fmaxf(m, mt), e_new = fmaxf(fmaxf(e, et), m_new + (BIAS - W_TOP));
           const float mb = m_new == -INFINITY ? 0.f : m_new, eb = e_new == -INFINITY ? 0.f : e_new;

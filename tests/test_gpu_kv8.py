@@ -816,7 +816,8 @@ def check_relative(p, b, q, out, sm=128 ** -0.5, window=0):
     want, _, mass, size = ref.attend(q, sm, window)
     got = out.double().cpu().numpy()
     K, V = ref.cached(0), ref.cached(1)
-    scale = ref.blocks(1)[1].astype(np.float64).repeat(64, axis=-1)
+    codes, scale = ref.blocks(1)
+    scale = np.where(codes.any(axis=(-1, -2)), scale.astype(np.float64), 0).repeat(64, axis=-1)  # zeros have no magnitude
     top = np.abs(V[:, scale.shape[1]:]).max(-1)
     large, small = np.concatenate((scale, top * 2.0 ** -14), 1), np.concatenate((scale, top * 2.0 ** -15), 1)
     code = np.abs(V) / np.where(small == 0, 1, small)[..., None]
@@ -907,3 +908,28 @@ def test_not_finite_and_zero_rows_of_the_tail(G, n):
     p.append([100], k=k, v=v.bfloat16())
     _, out, _ = p.attend(G, [n], check=False)
     assert torch.isnan(out[-1]).all() and torch.isfinite(out[:-1]).all()
+
+
+@pytest.mark.parametrize("G,n", ROWS)
+@pytest.mark.parametrize("fmt,dtype", FORMS)
+def test_zero_blocks_beside_small_values(G, n, fmt, dtype):
+    """A block whose values are all zero (of either sign) has scale 1 and no magnitude, wherever it stands; a block whose
+    scale is 1 with some rows of zeros has that of the others."""
+    for zero in ([0], [2], [4], [0, 1, 2, 3], [0, 3, 4]):
+        for size in (1e-2, 1e-4, 1e-6) if dtype == "bf16" else (1.0, 1e-3):
+            p = Pair(1, 1, 384, fmt, dtype, seed=49)
+            k, v = p.rows(340), p.rows(340).double() * size
+            for z in zero:
+                v[64 * z:64 * z + 64] *= 0  # 0 and -0
+            p.append([340], k=k, v=v.to(TYPES[dtype]))
+            q, out, _ = p.attend(G, [n], check=False)
+            check_relative(p, 0, q, out)
+    for place in (0, 40, 63):  # the block's scale is 1 by one row
+        p = Pair(1, 1, 384, fmt, dtype, seed=50)
+        k, v = p.rows(340), p.rows(340).double() * 1e-2
+        v[64:128] *= 0
+        v[64 + place] = {"e4m3": 448.0, "int8": 127.0}[fmt]
+        p.append([340], k=k, v=v.to(TYPES[dtype]))
+        for window in (0, 250):
+            q, out, _ = p.attend(G, [n], window=window, check=False)
+            check_relative(p, 0, q, out, window=window)
