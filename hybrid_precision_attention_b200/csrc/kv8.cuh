@@ -130,6 +130,12 @@ __device__ __forceinline__ bool kv8_seq(const hq_kv8_cache& c, const int32_t* cu
   return true;
 }
 
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Rows of the 16-bit tail enter the value product at a power of two that brings their largest
 // value to [2^14, 2^15), as bf16 rows are stored (exact: fp16 rows only go up), and the weight
 // takes its inverse: a weight's fp16 range is then spent on the row's own magnitude, and a row

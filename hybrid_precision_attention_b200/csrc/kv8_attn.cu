@@ -33,10 +33,12 @@
 // their precision.  A weight 2^(s - m) is summed in float32; its product with the
 // value scale enters the matrix product as fp16 at 2^(s + log2 vscale - E + 6).
 // The references are the exact maxima when they are set and stay as they are
-// until a score passes m by 2^8 or a scale its reference by 2: the common block
+// until a score passes m by 2^8 or a weight E by 2^9: the common block
 // costs one comparison per score and one vote, and no cross-lane maximum.  The
 // largest fp16 weight is then 2^15 and the smallest normal one 2^-20 of the
-// reference.
+// reference.  (A bound on the weights by m in place of the weights themselves had E
+// set anew on page after page where the largest score belonged to a small value: 24 rows
+// 143 us against 135.)
 //
 // Measured (8 kv heads): 64 sequences of 1K to 16K, a token each, 8 rows: 182 us, 6.4 TB/s of
 // codes, the copy rate; 16 rows, 64 of 4K to 8K: 135 us, 6.0 TB/s; 24 rows, 64 of 1K to 8K:
@@ -59,7 +61,7 @@ namespace {
 
 constexpr float P_BIAS = 6.0f;     // log2 of the fp16 weight at both references
 constexpr float P_SLACK = 8.0f;    // how far (log2) a score may pass m
-constexpr float V_LIMIT = 128.0f;  // 2^(P_BIAS + 1): how far a value scale may pass its reference; 2^8 * 2^7 < 65504
+constexpr float W_TOP = 15.0f;     // log2 of the largest fp16 weight
 // log2 of the largest factor of weights, 2^(m - E + P_BIAS): E stays above m + P_BIAS - P_TOP, so that the factor and
 // the inverse that undoes it at the end are both normal numbers (value scales below 2^(P_BIAS - P_TOP) then give
 // smaller weights), and a weight that underflowed stays 0 beside a far larger earlier score
@@ -453,7 +455,10 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
       bool far = OWN;  // the first of the task's
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        if (!OWN) far |= fmaxf(ef[nb][0], ef[nb][1]) * vs[0] > V_LIMIT;
+        // how far a score may pass m: by P_SLACK, and no further than its weight stays below 2^W_TOP
+        float most[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) most[i] = OWN ? P_SLACK : fminf(P_SLACK, W_TOP - lg2_approx(ef[nb][i] * vs[0]));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float mul = qs[nb][i & 1] * ks[i >> 1];
@@ -465,12 +470,13 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
               const int d = qp[nb][i & 1] - (pos + 16 * j + g + 8 * (i >> 1));
               if (d < 0 || (a.window > 0 && d >= a.window && qp[nb][i & 1] != INT_MAX)) sc[j][nb][i] = -INFINITY;
             }
-            far |= sc[j][nb][i] - m_run[nb][i & 1] > P_SLACK;
+            far |= sc[j][nb][i] - m_run[nb][i & 1] > most[i & 1];
           }
         }
       }
       if (__any_sync(0xffffffffu, far)) {
         const float lv[2] = {log2f(vs[0]), log2f(vs[1])};
+        const float low = (OWN ? 0.f : fmaxf(lv[0], 0.f)) + (P_BIAS - P_TOP);  // the factor times the scale is finite, too
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           float ao[2];
@@ -491,7 +497,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
               et = fmaxf(et, __shfl_xor_sync(0xffffffffu, et, 8));
               et = fmaxf(et, __shfl_xor_sync(0xffffffffu, et, 16));
             }
-            const float m_new = fmaxf(m_run[nb][i], mt), e_new = fmaxf(fmaxf(e_run[nb][i], et), m_new + (P_BIAS - P_TOP));
+            const float m_new = fmaxf(m_run[nb][i], mt), e_new = fmaxf(fmaxf(e_run[nb][i], et), m_new + low);
             const float mb = m_new == -INFINITY ? 0.f : m_new, eb = e_new == -INFINITY ? 0.f : e_new;
             l_run[nb][i] *= ex2(m_run[nb][i] - mb);
             ao[i] = ex2(e_run[nb][i] - eb);
@@ -510,7 +516,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
       for (int nb = 0; nb < NB; ++nb) {
         float w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = ef[nb][i & 1] * vs[i >> 1];
+        for (int i = 0; i < 4; ++i) w[i] = OWN ? vs[i >> 1] : ef[nb][i & 1] * vs[i >> 1];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           float p[4];
@@ -523,7 +529,7 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
           for (int i = 0; i < 2; ++i) l_run[nb][i] += p[i] + p[2 + i];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            p[i] *= w[i];
+            p[i] = (OWN ? p[i] * ef[nb][i & 1] : p[i]) * w[i];
             if (MASK && sc[j][nb][i] == -INFINITY) p[i] = 0.f;  // a scale that is NaN stays behind the mask
           }
           pf[j][nb][0] = movmatrix_t(pack_f16x2(p[0], p[1]));

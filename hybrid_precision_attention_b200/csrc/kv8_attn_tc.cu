@@ -137,15 +137,10 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int32_t
   }
 }
 
-// Logarithm and inverse of a value scale: their errors, 2^-22 of it, go to a page's
+// Inverse (and logarithm, lg2_approx) of a value scale: their errors, 2^-22 of it, go to a page's
 // weights and their sum alone (a scale that is not a normal number takes the path
 // that uses neither), and one thread makes them on every page's way, where the exact
 // functions took 600 cycles.
-__device__ __forceinline__ float lg2_approx(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -679,7 +674,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           } else {
             et = mt + sc.z;
           }
-          const float m_new = fmaxf(m, mt), e_new = fmaxf(fmaxf(e, et), m_new + (BIAS - W_TOP));
+          // a page's factor times its scale is finite, too
+          const float low = (tail ? 0.f : fmaxf(sc.z, 0.f)) + (BIAS - W_TOP);
+          const float m_new = fmaxf(m, mt), e_new = fmaxf(fmaxf(e, et), m_new + low);
           const float mb = m_new == -INFINITY ? 0.f : m_new, eb = e_new == -INFINITY ? 0.f : e_new;
           const float ao = ex2(e - eb);
           l *= ex2(m - mb);
@@ -743,8 +740,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
               float y0 = ex2(x[i] - mref), y1 = ex2(x[i + 1] - mref);
               s1 += y0 + y1;
               // a scale that is NaN stays behind the mask
-              y0 = x[i] == -INFINITY ? 0.f : y0 * (tail ? ef * tail_sc[64 + i] : w);
-              y1 = x[i + 1] == -INFINITY ? 0.f : y1 * (tail ? ef * tail_sc[64 + i + 1] : w);
+              y0 = x[i] == -INFINITY ? 0.f : tail ? y0 * ef * tail_sc[64 + i] : y0 * w;
+              y1 = x[i + 1] == -INFINITY ? 0.f : tail ? y1 * ef * tail_sc[64 + i + 1] : y1 * w;
               s0 += y0 + y1;
               pk[i / 2] = pack_f16x2(y0, y1);
             }

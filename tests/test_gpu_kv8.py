@@ -933,3 +933,23 @@ def test_zero_blocks_beside_small_values(G, n, fmt, dtype):
         for window in (0, 250):
             q, out, _ = p.attend(G, [n], window=window, check=False)
             check_relative(p, 0, q, out, window=window)
+
+
+@pytest.mark.parametrize("G,n", ROWS)
+@pytest.mark.parametrize("where", [0, 64, 339])
+def test_a_key_without_values_takes_the_weight(G, n, where):
+    """One key takes nearly all of the weight, by 2^40 to 2^105, and its values are zero: what the others, of values up to
+    2^40, add up to is the output."""
+    for far in (40.0, 80.0, 105.0):
+        for size in (2.0 ** -20, 1.0, 2.0 ** 40):
+            p = Pair(1, 1, 384, "e4m3", "bf16", seed=51)
+            k, v = p.rows(340).double(), p.rows(340).double() * size
+            k[:, 0, 0] = 0
+            k[where, 0], v[where] = 0, 0
+            k[where, 0, 0] = 16.0
+            q = torch.from_numpy(p.rng.standard_normal((n, 8 if G == 8 else 4, 128)))
+            q[..., 0] = far * np.log(2) / 16 * 128 ** 0.5
+            p.append([340], k=k.bfloat16(), v=v.bfloat16())
+            q = q.bfloat16()
+            _, out, _ = p.attend(G, [n], q=q, check=False)
+            check_relative(p, 0, q, out)
