@@ -130,6 +130,7 @@ __device__ __forceinline__ bool kv8_seq(const hq_kv8_cache& c, const int32_t* cu
   return true;
 }
 
+// log2 within 2^-22 (below the normal numbers: -inf), for what needs no more
 __device__ __forceinline__ float lg2_approx(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

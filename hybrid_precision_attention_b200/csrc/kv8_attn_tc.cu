@@ -79,7 +79,7 @@ struct Lay {
   static constexpr int RAW = V + STAGES * 16384; // codes: slots of a page's K or V
   static constexpr int RK = NT == 2 ? 2 : 4;     // slots of K; as many of V
   static constexpr int RAWS = RAW + 2 * RK * HALF; // the two scales (16 bytes) of each K slot's page
-  static constexpr int AUX = RAWS + RK * 16;     // 8 pages x (s_k, s_v, log2 s_v, 1 / s_v); the tail's 64 K and 64 V scales
+  static constexpr int AUX = RAWS + RK * 16;     // 8 pages x (s_k, s_v, log2 s_v, -); the tail's 64 K and 64 V scales
   static constexpr int BARS = AUX + 8 * 16 + 512;
   static constexpr int MISC = BARS + 48 * 8;     // TMEM base, flags, units of all runs, walk and job
   static constexpr int JOIN = RAW;               // NT = 1: (m, E, l) of stream 1's rows, once the task's copies are done with
@@ -135,16 +135,6 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int32_t
       return false;
     }
   }
-}
-
-// Inverse (and logarithm, lg2_approx) of a value scale: their errors, 2^-22 of it, go to a page's
-// weights and their sum alone (a scale that is not a normal number takes the path
-// that uses neither), and one thread makes them on every page's way, where the exact
-// functions took 600 cycles.
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -490,7 +480,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           // least, so that the scales of eight pages before have been used.
           if (T >= STAGES && !await(st_empty + st, T / STAGES - 1)) return;
           if (!VAL && ct == 0)
-            *reinterpret_cast<float4*>(aux + (T & 7) * 4) = make_float4(sc.x, sc.y, lg2_approx(sc.y), rcp_approx(sc.y));
+            *reinterpret_cast<float4*>(aux + (T & 7) * 4) = make_float4(sc.x, sc.y, lg2_approx(sc.y), 0.f);
           const uint32_t dst = base + (VAL ? L::V : L::K) + st * 16384;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -544,7 +534,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
             for (int w = 0; w < 4; ++w) put(dst, cw * 8 + i * 4 + w, y[w]);
           }
           if (!VAL) {
-            if (ct == 0) *reinterpret_cast<float4*>(aux + (T & 7) * 4) = make_float4(1.f, 1.f, 0.f, 1.f);
+            if (ct == 0) *reinterpret_cast<float4*>(aux + (T & 7) * 4) = make_float4(1.f, 1.f, 0.f, 0.f);
             tail_sc[ct] = ct < held ? ts[ct] : 1.0f;
           }
           fence_proxy_async_smem();
@@ -609,9 +599,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       const uint32_t orow = trow + TM_O + 128 * g;
       // rows past the last have zero queries and see every key; their references
-      // stay at 1.  A warp without a row only keeps the barriers going.
+      // start at 1.  A warp without a row only keeps the barriers going.
       float m = real ? -INFINITY : 0.f, e = real ? -INFINITY : 0.f, l = 0.f;
-      float lef = real ? -INFINITY : 0.f, ref = real ? 0.f : 1.f;  // log2 of 2^(m - E + BIAS), and its inverse
       const bool idle = !__any_sync(0xffffffffu, real);
       int taken = 0;  // pages of the task
       for (int t = 0; t < nt; ++t) {
@@ -642,7 +631,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
         }
-        const float4 sc = *reinterpret_cast<const float4*>(aux + ((n_page + t) & 7) * 4);  // s_k, s_v, log2 s_v, 1 / s_v
+        const float4 sc = *reinterpret_cast<const float4*>(aux + ((n_page + t) & 7) * 4);  // s_k, s_v, log2 s_v, -
         // columns [lo, hi] of the page are seen by this row
         const int hi = real ? qpos - (page0 + t) * KV8_BLOCK : KV8_BLOCK, lo = real && a.window > 0 ? hi - a.window + 1 : 0;
         const bool seen = __all_sync(0xffffffffu, !tail && hi >= KV8_BLOCK - 1 && lo <= 0);  // all columns, by 16-bit rows none
@@ -682,8 +671,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           l *= ex2(m - mb);
           m = m_new;
           e = e_new;
-          lef = e_new == -INFINITY ? -INFINITY : mb - eb + BIAS;
-          ref = e_new == -INFINITY ? 0.f : ex2(-lef);
           if (taken > 1) {
             // the page before may still be being added
             ok = wait_for(o_done + (sb ^ 1), ((j - 1) >> 1) & 1, err, stop);
@@ -710,10 +697,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           const float mref = m == -INFINITY ? 0.f : m;
           // Weights of a page that is seen whole take the value scale into the
           // exponent, and their sum is divided by it: a product less per weight.
+          // (The logarithm's error, 2^-22 of it, goes to weights and sum alike.)
           // Not where it is so small that weights would underflow.
-          const float lw = lef + sc.z;
+          const float off = BIAS - e + sc.z, lw = m + off;
           if (__all_sync(0xffffffffu, seen && lw > -60.f)) {
-            const uint64_t mul2 = f32x2(mul, mul), off2 = f32x2(lw - mref, lw - mref);
+            const uint64_t mul2 = f32x2(mul, mul), off2 = f32x2(off, off);
             uint64_t a0 = 0, a1 = 0;
 #pragma unroll
             for (int i = 0; i < 64; i += 2) {
@@ -725,9 +713,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
             }
             const float2 b0 = f32x2_split(f32x2_add(a0, a1));
             s0 = b0.x + b0.y;
-            s1 = s0 * (ref * sc.w);
+            s1 = s0 * ex2(-lw);
           } else {
-            const float ef = ex2(lef), w = ef * sc.y;
+            const float ef = e == -INFINITY ? 0.f : ex2(m - e + BIAS), w = ef * sc.y;
             if (seen) {
 #pragma unroll
               for (int i = 0; i < 64; ++i) x[i] *= mul;
