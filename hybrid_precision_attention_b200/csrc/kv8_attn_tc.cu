@@ -536,6 +536,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           if (!VAL) {
             if (ct == 0) *reinterpret_cast<float4*>(aux + (T & 7) * 4) = make_float4(1.f, 1.f, 0.f, 0.f);
             tail_sc[ct] = ct < held ? ts[ct] : 1.0f;
+            // the block is scored once the scales of its values are there, too (a wait for them
+            // by the softmax warps cost every page's code: prompt chunk 542 us against 502)
+            if (!await(v_full + st, T / STAGES)) return;
           }
           fence_proxy_async_smem();
           mbar_arrive(st_full + st);
@@ -625,12 +628,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
         };
         load();
         const bool tail = t >= full;
-        if (tail) {
-          // the converters of its values have the rows' scales
-          ok = wait_for(v_full + (n_page + t) % STAGES, (n_page + t) / STAGES & 1, err, stop);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-        }
         const float4 sc = *reinterpret_cast<const float4*>(aux + ((n_page + t) & 7) * 4);  // s_k, s_v, log2 s_v, -
         // columns [lo, hi] of the page are seen by this row
         const int hi = real ? qpos - (page0 + t) * KV8_BLOCK : KV8_BLOCK, lo = real && a.window > 0 ? hi - a.window + 1 : 0;
