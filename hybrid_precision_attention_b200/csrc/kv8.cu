@@ -64,6 +64,41 @@ __device__ __forceinline__ uint32_t to_pair(float x, float y) {
   return w;
 }
 
+// A block whose earlier rows are no numbers of E (they came with calls of another element
+// type, or are not finite): every element in float32 from where it lies, a code word of the page at a time,
+// amax first.  Rare, and so not tiled.  new_row: the input's row of the block's first
+// position, `fresh` rows of it come from the tail.
+template <class E, int FMT>
+__device__ __noinline__ void append_mixed(const E* new_row, int64_t tok, const uint16_t* tail, const float* scales, int fresh, bool values,
+                                          uint8_t* codes, float* scale_out, uint32_t* sh_amax) {
+  auto at = [&](int r, int d) {
+    return r >= fresh ? to_float(new_row[r * tok + d])
+                      : __half2float(__ushort_as_half(tail[values ? HQ_KV8_V_INDEX(r, d) : HQ_KV8_K_INDEX(r, d)])) * scales[r];
+  };
+  __syncthreads();  // the last reader of sh_amax is done
+  if (threadIdx.x == 0) *sh_amax = 0;
+  __syncthreads();
+  uint32_t top = 0;
+  for (int i = threadIdx.x; i < KV8_BLOCK * D; i += 256) top = max(top, __float_as_uint(at(i / D, i % D)) & 0x7fffffffu);
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) atomicMax(sh_amax, top);
+  __syncthreads();
+  const float scale = kv8_scale(*sh_amax, FMT);
+  for (int i = threadIdx.x; i < KV8_BLOCK * D / 4; i += 256) {
+    float x[4];  // the word's elements: K four d of a position, V positions r, r + 1, r + 8, r + 9 of one d
+    if (values) {
+      const int r = i / 512 * 16 + i / 4 % 4 * 2, d = i / 128 % 4 * 32 + (i / 2 % 2) * 16 + (i % 2) * 8 + i / 16 % 8;
+      x[0] = at(r, d), x[1] = at(r + 1, d), x[2] = at(r + 8, d), x[3] = at(r + 9, d);
+    } else {
+      const int r = i / 256 * 8 + i / 16 % 8, d = i / 128 % 2 * 64 + i % 16 * 4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = at(r, d + j);
+    }
+    reinterpret_cast<uint32_t*>(codes)[i] = kv8_codes4<FMT>(x, scale);
+  }
+  if (threadIdx.x == 0) *scale_out = scale;
+}
+
 // One CTA per (block that new tokens touch, kv head), K and V: 32 KB of rows in
 // flight behind one chain of look-ups.  Sequence b's blocks are CTAs s_b, s_b + 1,
 // .. with s_b = cu[b] / 64 + 2 b: n tokens touch at most n / 64 + 2 blocks, so the
@@ -110,9 +145,10 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(const __grid_constan
 
   if (p0 + KV8_BLOCK <= s.len) {
     // the block is complete: its rows into the tiles, new ones from the input,
-    // earlier ones from the tail (whose values are numbers of E as they were)
+    // earlier ones from the tail
     const long long idx = kv8_page_index(c, bh, blk);
     uint4 v[2][4];
+    int lost = 0;  // earlier elements that E does not hold
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       const E* src = source(which);
@@ -129,6 +165,14 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(const __grid_constan
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             x[i] = from_float<E>(__half2float(__ushort_as_half(t[which ? HQ_KV8_V_INDEX(r, d + i) : HQ_KV8_K_INDEX(r, d + i)])) * sc);
+          // at another scale than 1 the row came as bf16, at 1 as fp16, or it is one for which both say the same
+          if (!IsBf16<E>::value) {
+            lost |= sc != 1.0f;
+          } else if (sc == 1.0f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              lost |= to_float(x[i]) != __half2float(__ushort_as_half(t[which ? HQ_KV8_V_INDEX(r, d + i) : HQ_KV8_K_INDEX(r, d + i)]));
+          }
           v[which][it] = *reinterpret_cast<const uint4*>(x);
         }
       }
@@ -151,7 +195,7 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(const __grid_constan
       const uint32_t top = __reduce_max_sync(0xffffffffu, max(hi >> 16, lo));
       if ((tid & 31) == 0) atomicMax(&sh_amax[which], top);
     }
-    __syncthreads();
+    const bool mixed = __syncthreads_or(lost);
     if (idx < 0) {
       if (tid == 0) kv8_err(c, b, HQ_DEVERR_PAGE);
     } else {
@@ -159,6 +203,13 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(const __grid_constan
       const int lane = tid & 31;
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
+        if (mixed) {
+          append_mixed<E, FMT>(source(which) + static_cast<int64_t>(p0) * a.tok[which], a.tok[which],
+                               tail_of(which) + half * KV8_BLOCK * D, scales_of(which) + half * KV8_BLOCK, s.first - p0, which,
+                               page + (which ? HQ_KV8_V : 0), reinterpret_cast<float*>(page + (which ? HQ_KV8_VSCALE : HQ_KV8_KSCALE)),
+                               &sh_amax[which]);
+          continue;
+        }
         const float scale = kv8_scale(__float_as_uint(pair_of<E>(sh_amax[which]).x), FMT);
         const bool plain = kv8_scale_plain(scale);
         const float r = 1.0f / scale;

@@ -953,3 +953,54 @@ def test_a_key_without_values_takes_the_weight(G, n, where):
             q = q.bfloat16()
             _, out, _ = p.attend(G, [n], q=q, check=False)
             check_relative(p, 0, q, out)
+
+
+# ----------------------------------------------------------------------------- element types in turn
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("first,then", [("f16", "bf16"), ("bf16", "f16")])
+@pytest.mark.parametrize("size", [1.0, 1e6, 1e-7])
+def test_element_types_in_turn(fmt, first, then, size):
+    """Rows of one element type completed by rows of the other: the codes come from the values as they were appended,
+    whether the later type holds them (bf16 rows of 1e6 are no fp16 numbers, fp16 rows have three bits more than bf16)."""
+    if first == "f16" and size != 1:
+        size = 1e4 if size > 1 else 1e-4
+    p = Pair(3, 2, 512, fmt, first, seed=52)
+
+    def append(n, dtype, scale):
+        p.dtype = dtype
+        p.append(n, k=(p.rows(sum(n)).double() * scale).to(TYPES[dtype]), v=(p.rows(sum(n)).double() * scale).to(TYPES[dtype]))
+        p.dtype = "both"
+        p.check_stored()
+
+    append([40, 100, 1], first, size)
+    append([24, 28, 200], then, 1.0)
+    append([10, 63, 1], first, size)
+    append([1, 1, 1], then, 1.0)
+    append([60, 64, 53], then, 1.0)
+    append([70, 1, 2], first, size)
+    append([1, 127, 64], then, 1.0)
+    assert not any(p.c.errors())
+
+
+def test_element_types_in_turn_and_a_row_that_is_not_finite():
+    p = Pair(1, 1, 256, "e4m3", "bf16", seed=53)
+    k, v = (p.rows(40).double() * 1e6).bfloat16(), p.rows(40)
+    k[7, 0, 3], v[9, 0, 1] = float("inf"), float("nan")
+    p.append([40], k=k, v=v)
+    p.dtype = "f16"
+    p.append([30])
+    p.dtype = "both"
+    p.check_stored()
+
+
+def test_attention_over_element_types_in_turn():
+    """Queries of either type over a cache whose tail holds rows of both."""
+    p = Pair(2, 1, 256, "int8", "f16", seed=54)
+    p.append([90, 70])
+    p.dtype = "bf16"
+    p.append([20, 25], k=(p.rows(45).double() * 4).bfloat16())
+    for dtype in ("bf16", "f16"):
+        p.dtype = dtype
+        p.attend(4, [1, 1])
+        p.attend(8, [20, 9])
