@@ -679,13 +679,14 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
       const int rr = k.row0 + r;
       if (rr >= rows) return;
       // accumulators are at 2^(P_BIAS - E), the sum at 2^-m: the quotient's exponent
-      const float f = m == -INFINITY ? 0.f : ex2(e - m - P_BIAS), inv = 1.0f / l;
+      // a row sees itself at least: no score above -inf means that its query is not finite
+      const float f = m == -INFINITY ? NAN : ex2(e - m - P_BIAS), inv = 1.0f / l;
       const int64_t tok = k.s.row0 + rr / a.G;
       const int head = k.h * a.G + rr % a.G;
       E y[4] = {from_float<E>(x.x * inv * f), from_float<E>(x.y * inv * f), from_float<E>(x.z * inv * f), from_float<E>(x.w * inv * f)};
       *reinterpret_cast<uint2*>(static_cast<E*>(a.out) + tok * a.o_tok + head * a.o_head + 4 * lane) =
           *reinterpret_cast<const uint2*>(y);
-      if (a.lse != nullptr && lane == 0) a.lse[tok * a.Hq + head] = m + log2f(l);
+      if (a.lse != nullptr && lane == 0) a.lse[tok * a.Hq + head] = m == -INFINITY ? NAN : m + log2f(l);
     };
     static_assert(8 % C::WARPS == 0 && C::WARPS % C::OW == 0, "as many of 8 rows to each warp; whole rounds");
     constexpr int RW = 8 / C::WARPS;  // rows 8 nb + warp + i WARPS, elements 4 lane .. 4 lane + 3

@@ -795,7 +795,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       const float f1 = ej == -INFINITY ? 1.f : ex2(e - eb), f2 = ej == -INFINITY ? 1.f : ex2(e2 - eb);
       auto write = [&](float m, float e, float l, auto cols) {  // the row's output from its accumulators
         // accumulators are at 2^(BIAS - E), the sum at 2^-m
-        const float f = m == -INFINITY ? 0.f : ex2(e - m - BIAS), inv = 1.0f / l;
+        // a row sees itself at least: no score above -inf means that its query is not finite
+        const float f = m == -INFINITY ? NAN : ex2(e - m - BIAS), inv = 1.0f / l;
         const int64_t tok = job.tok0 + rr / a.G;
         const int head = job.h * a.G + rr % a.G;
         E* dst = static_cast<E*>(a.out) + tok * a.o_tok + head * a.o_head;
@@ -813,7 +814,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
             }
           }
         }
-        if (real && a.lse != nullptr) a.lse[tok * a.Hq + head] = m + log2f(l);
+        if (real && a.lse != nullptr) a.lse[tok * a.Hq + head] = m == -INFINITY ? NAN : m + log2f(l);
       };
       if (owner && ok && !idle) {
         auto cols = [&](int c4, float (&x)[32]) {

@@ -1004,3 +1004,27 @@ def test_attention_over_element_types_in_turn():
         p.dtype = dtype
         p.attend(4, [1, 1])
         p.attend(8, [20, 9])
+
+
+# ----------------------------------------------------------------------------- queries that are not finite
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("L,n,G", [(40, 1, 4), (200, 1, 4), (200, 5, 8), (40, 8, 8), (300, 8, 8), (300, 40, 8)])
+def test_an_infinite_query_whose_scores_are_all_minus_infinity(dtype, L, n, G):
+    """Its softmax is 0 / 0, whichever pages it sees.  The other rows stay within their bound (not the same to the bit: the
+    rows of a warp have their references set anew together)."""
+    p = Pair(1, 1, 512, "e4m3", dtype, seed=55)
+    k = p.rows(L)
+    k[:, 0, 3] = -1.0
+    p.append([L], k=k)
+    q = torch.from_numpy(p.rng.standard_normal((n, G, 128))).to(TYPES[dtype])
+    fine = q.clone()
+    q[n // 2, 1, 3] = float("inf")
+    for window in (0, 30):
+        _, out, lse = p.attend(G, [n], q=q, window=window, check=False)
+        bad = torch.isnan(out).all(-1)
+        assert bad.nonzero().tolist() == [[n // 2, 1]] and torch.equal(torch.isnan(out).any(-1), bad)
+        assert torch.equal(torch.isnan(lse), bad)
+        _, want, wlse = p.attend(G, [n], q=fine, window=window)
+        out[bad], lse[bad] = want[bad], wlse[bad]
+        check_rows(out, lse, p.ref[0], fine.double().numpy(), 128 ** -0.5, window, dtype)
