@@ -902,9 +902,11 @@ hq_status device_sms(int* sms) {
   return cuda_status(e, "device query");
 }
 
+// Never less for more rows: 25 to 32 rows are two tasks of 16, whose pieces take less than
+// those of a task of 24.
 size_t attn_workspace(int64_t rows, int sms) {
   const size_t parts = rows > ROWS_MAX ? kv8_attn_tc_parts(rows, sms)
-                                       : static_cast<size_t>(2) * CTAS * sms * 8 * task_eights(rows) * (D + 4);
+                                       : static_cast<size_t>(2) * CTAS * sms * 8 * (rows > 24 ? 3 : task_eights(rows)) * (D + 4);
   return HQ_KV8_WS_ZERO + parts * sizeof(float);
 }
 

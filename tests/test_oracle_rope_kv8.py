@@ -220,3 +220,12 @@ def test_rope_call_refusals(mem):
                            (t(y=base, yh=72), None, {}, INVALID), (t(), None, dict(pos=None), INVALID),
                            (t(), None, dict(pos=base + 2), INVALID), (t(), None, dict(freqs=base + 4), INVALID)):
         assert call(q, k, **kw) == want, kw
+
+
+def test_kv8_workspace_for_more_tokens_serves_fewer(mem):
+    """A caller that sizes scratch for its largest max_new may call with any smaller one."""
+    from hybrid_precision_attention_b200 import hq
+    c = ctypes.byref(_cache(mem[1]))
+    for Hq in (4, 12, 20, 32, 64):
+        need = [hq._lib.hq_kv8_attn_workspace_bytes(c, Hq, n) for n in range(0, 300)]
+        assert all(a <= b for a, b in zip(need, need[1:])) and need[0] > 0
