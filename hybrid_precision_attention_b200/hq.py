@@ -475,6 +475,14 @@ def _ints(t, index, shape, name):
                       f"{tuple(t.shape)} on {t.device}")
 
 
+def _scratch(t, index, name, dtype=None, shape=None):
+    """Memory that a kernel writes as it lies: contiguous, on that CUDA device."""
+    if not t.is_cuda or t.get_device() != index or not t.is_contiguous() or (dtype is not None and t.dtype != dtype) or \
+            (shape is not None and tuple(t.shape) != shape):
+        raise HqError(f"{name}: expected contiguous {dtype or 'memory'} {shape or ''} on cuda:{index}, got {t.dtype} "
+                      f"{tuple(t.shape)} on {t.device}")
+
+
 class RopeTable:
     """Frequencies of ``rot`` rotated elements (include/hq.h, hq_rope_freqs), on the device."""
 
@@ -679,10 +687,12 @@ def hq_kv8_attn(cache: Kv8Cache, q, cu, kv_len, max_new: int, sm_scale: float = 
         if return_lse:
             lse = q.new_empty((N, Hq), dtype=torch.float32)
     else:
-        _need(lse, torch.float32, (N, Hq), "lse")
+        _scratch(lse, dev, "lse", torch.float32, (N, Hq))
     s = _raw_stream(dev)
     if ws is None:
         ws = cache.workspace(Hq, max_new, s)
+    else:
+        _scratch(ws, dev, "ws")
     qs, os_ = q.stride(), out.stride()
     st = _lib.hq_kv8_attn(cache.ref, _DTYPE[q.dtype], q.data_ptr(), qs[0], qs[1], Hq, N, cu.data_ptr(), kv_len.data_ptr(),
                           max_new, window, cache.D ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), os_[0], os_[1],

@@ -229,3 +229,41 @@ def test_kv8_workspace_for_more_tokens_serves_fewer(mem):
     for Hq in (4, 12, 20, 32, 64):
         need = [hq._lib.hq_kv8_attn_workspace_bytes(c, Hq, n) for n in range(0, 300)]
         assert all(a <= b for a, b in zip(need, need[1:])) and need[0] > 0
+
+
+class _Elsewhere:
+    """A tensor of another device."""
+    is_cuda, device = True, "cuda:1"
+
+    def __init__(self, t):
+        self.dtype, self.shape, self.nbytes = t.dtype, t.shape, t.nbytes
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return 1
+
+    def data_ptr(self):
+        return 0
+
+
+def test_attention_takes_scratch_and_lse_on_its_device_alone(monkeypatch):
+    """Checked before the library is called, which takes their addresses as they are."""
+    from types import SimpleNamespace
+
+    from hybrid_precision_attention_b200 import hq
+    import torch
+    called = []
+    for name, f in (("_rows", lambda *a, **k: None), ("_ints", lambda *a: None), ("_device", lambda: 0), ("_raw_stream", lambda d: 0)):
+        monkeypatch.setattr(hq, name, f)
+    monkeypatch.setattr(hq._lib, "hq_kv8_attn", lambda *a: called.append(a) or 0)
+    cache = SimpleNamespace(index=0, B=1, D=128, ref=None, workspace=lambda *a: torch.zeros(64, dtype=torch.uint8))
+    q, cu, n = torch.zeros(2, 4, 128).half(), torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    ws, lse = torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(2, 4)
+    hq.hq_kv8_attn(cache, q, cu, n, 1)
+    assert len(called) == 1
+    for kw in (dict(ws=ws), dict(ws=_Elsewhere(ws)), dict(lse=_Elsewhere(lse)), dict(lse=lse)):
+        with pytest.raises(hq.HqError):
+            hq.hq_kv8_attn(cache, q, cu, n, 1, **kw)
+    assert len(called) == 1
