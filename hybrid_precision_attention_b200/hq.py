@@ -483,6 +483,34 @@ def _scratch(t, index, name, dtype=None, shape=None):
                       f"{tuple(t.shape)} on {t.device}")
 
 
+class _Places:
+    """A tensor's bytes by address, for numpy, which does not look at them."""
+
+    def __init__(self, t):
+        n = t.element_size()
+        self.__array_interface__ = dict(version=3, data=(t.data_ptr(), False), typestr=f"|V{n}", shape=tuple(t.shape),
+                                        strides=tuple(s * n for s in t.stride()))
+
+
+def _overlap(a, b) -> bool:
+    """Whether two tensors (strides not negative) share an element's place, exactly."""
+    pa, pb = a.data_ptr(), b.data_ptr()
+    if pa > pb:
+        a, b, pa, pb = b, a, pb, pa
+    # mostly the one that begins first has ended where the other begins
+    if pb - pa >= (a.nbytes if a.is_contiguous() else (sum((n - 1) * s for n, s in zip(a.shape, a.stride())) + 1) * a.element_size()):
+        return False
+    return a.numel() > 0 and b.numel() > 0 and bool(np.shares_memory(np.asarray(_Places(a)), np.asarray(_Places(b))))
+
+
+def _output(call, t, name, other, x):
+    """An output of the caller's: each element in a place of its own, apart from those of x."""
+    if 0 in t.stride() and any(s == 0 and n > 1 for n, s in zip(t.shape, t.stride())):
+        raise HqError(f"{call}: elements of {name} share places, strides {t.stride()}")
+    if _overlap(t, x):
+        raise HqError(f"{call}: {name} overlaps {other}")
+
+
 class RopeTable:
     """Frequencies of ``rot`` rotated elements (include/hq.h, hq_rope_freqs), on the device."""
 
@@ -519,6 +547,8 @@ def hq_rope(q, k, pos, table: RopeTable, layout: int = ROPE_HALF, grad: bool = F
         q_out = torch.empty_like(q)
     else:
         _rows(q_out, dev, shape, "q_out", (dt,))
+        if q_out.data_ptr() != q.data_ptr():
+            _output("hq_rope", q_out, "q_out", "q", q)
     a = _rope_side(q, q_out, n)
     b = None
     if k is not None:
@@ -527,6 +557,8 @@ def hq_rope(q, k, pos, table: RopeTable, layout: int = ROPE_HALF, grad: bool = F
             k_out = torch.empty_like(k)
         else:
             _rows(k_out, dev, k.shape, "k_out", (dt,))
+            if k_out.data_ptr() != k.data_ptr():
+                _output("hq_rope", k_out, "k_out", "k", k)
         b = _rope_side(k, k_out, n)
     st = _lib.hq_rope(_DTYPE[dt], lead[0] if n == 4 else 1, lead[-1], D, table.rot, layout, 1 if grad else 0, a, b,
                       pos.data_ptr(), table._ptr, table.amp, _raw_stream(dev))
@@ -658,6 +690,7 @@ def hq_kv8_read(cache: Kv8Cache, kv_len, start: int = 0, n: int = None, dtype=to
         _rows(v_out, dev, k_out.shape, "v_out", (k_out.dtype,))
         if k_out.stride() != v_out.stride():
             raise HqError("hq_kv8_read: k_out and v_out need the same strides")
+        _output("hq_kv8_read", k_out, "k_out", "v_out", v_out)
     os_ = k_out.stride()
     st = _lib.hq_kv8_read(cache.ref, _DTYPE[k_out.dtype], kv_len.data_ptr(), start, n, k_out.data_ptr(), v_out.data_ptr(),
                           os_[0], os_[1], os_[2], 1 if zero_rest else 0, _raw_stream(dev))
@@ -683,6 +716,7 @@ def hq_kv8_attn(cache: Kv8Cache, q, cu, kv_len, max_new: int, sm_scale: float = 
         out = torch.empty_like(q)
     else:
         _rows(out, dev, q.shape, "out", (q.dtype,))
+        _output("hq_kv8_attn", out, "out", "q", q)
     if lse is None:
         if return_lse:
             lse = q.new_empty((N, Hq), dtype=torch.float32)

@@ -1028,3 +1028,39 @@ def test_an_infinite_query_whose_scores_are_all_minus_infinity(dtype, L, n, G):
         _, want, wlse = p.attend(G, [n], q=fine, window=window)
         out[bad], lse[bad] = want[bad], wlse[bad]
         check_rows(out, lse, p.ref[0], fine.double().numpy(), 128 ** -0.5, window, dtype)
+
+
+# ----------------------------------------------------------------------------- outputs in places of their own
+
+def test_outputs_that_share_places_are_refused():
+    """An output that overlaps the queries, the other output or itself; neighbours and interleaved views are taken."""
+    hq = _hq()
+    p = Pair(2, 2, 256, "e4m3", "f16", seed=56)
+    p.append([200, 100])
+    cu = _ints([0, 1, 2])
+    row = torch.randn(2, 26, 128, device="cuda").half()
+    want = hq.hq_kv8_attn(p.c, row[:, :8].clone(), cu, p.len, 1)
+    for out in (row[:, 4:12], row[:, :8], row.as_strided((2, 8, 128), row.stride(), 8), row.as_strided((2, 8, 128), (128, 256, 1), 512),
+                torch.empty(1, 8, 128, device="cuda").half().expand(2, 8, 128)):
+        with pytest.raises(hq.HqError):
+            hq.hq_kv8_attn(p.c, row[:, :8], cu, p.len, 1, out=out)
+    assert torch.equal(hq.hq_kv8_attn(p.c, row[:, :8], cu, p.len, 1, out=row[:, 8:16]), want)
+    kv = torch.zeros(2, 2, 2, 200, 128, device="cuda", dtype=torch.float16)
+    K, V = hq.hq_kv8_read(p.c, p.len, n=200)
+    whole = (2, 2, 200, 128)
+    for a, b in ((kv[:, 0], kv[:, 0]), (kv[:, :, 0], kv.as_strided(whole, kv[:, :, 0].stride(), 128 * 199)),
+                 (kv.view(-1)[:128].expand(whole), kv.view(-1)[128:256].expand(whole))):
+        with pytest.raises(hq.HqError):
+            hq.hq_kv8_read(p.c, p.len, n=200, k_out=a, v_out=b)
+    for a, b in ((kv[:, 0], kv[:, 1]), (kv[:, :, 0], kv[:, :, 1]), (kv.view(2, 200, 2, 2, 128)[:, :, 0].transpose(1, 2),
+                                                                  kv.view(2, 200, 2, 2, 128)[:, :, 1].transpose(1, 2))):
+        hq.hq_kv8_read(p.c, p.len, n=200, k_out=a, v_out=b)
+        assert torch.equal(a, K) and torch.equal(b, V)
+    x = torch.randn(4, 12, 128, device="cuda").half()
+    t, pos = hq.RopeTable(128), _ints([0, 1, 2, 3])
+    q, k = hq.hq_rope(x[:, :4].clone(), x[:, 4:6].clone(), pos, t)
+    for kw in (dict(q_out=x[:, 2:6]), dict(q_out=x[:, 6:10], k_out=x[:, 5:7]), dict(q_out=x[:1, 6:10].expand(4, 4, 128))):
+        with pytest.raises(hq.HqError):
+            hq.hq_rope(x[:, :4], x[:, 4:6], pos, t, **kw)
+    a, b = hq.hq_rope(x[:, :4], x[:, 4:6], pos, t, q_out=x[:, 6:10], k_out=x[:, 4:6])
+    assert torch.equal(a, q) and torch.equal(b, k)
