@@ -528,13 +528,18 @@ class RopeTable:
 def hq_rope(q, k, pos, table: RopeTable, layout: int = ROPE_HALF, grad: bool = False, q_out=None, k_out=None, stream=None):
     """Rotary positions of q [B, T, Hq, D] and k [B, T, Hkv, D] (or None) at pos int32 [B, T]; without a batch
     dimension [T, H, D] and [T].  Strided views are taken as they are; q_out, k_out may be q, k themselves.
-    ``grad``: the transposed rotation (gradients of q and k from those of the outputs).  Returns (q_out, k_out)."""
+    ``grad``: the transposed rotation (gradients of q and k from those of the outputs).  Returns (q_out, k_out).
+    Where q or k requires grad the outputs do, too, to any order; q_out and k_out are refused then."""
     dev = table.index
     if dev < 0:
         raise HqError("hq_rope: the table is not on a CUDA device")
     if stream is not None or _device() != dev:
         with _On(dev, stream):
             return hq_rope(q, k, pos, table, layout, grad, q_out, k_out)
+    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+        if q_out is not None or k_out is not None:
+            raise HqError("hq_rope: q_out and k_out have no gradient, and q or k requires one (torch.no_grad, or leave them out)")
+        return _Rope.apply(q, k, pos, table, layout, grad)
     shape = q.shape
     n = len(shape)
     if n != 4 and n != 3:
@@ -565,6 +570,29 @@ def hq_rope(q, k, pos, table: RopeTable, layout: int = ROPE_HALF, grad: bool = F
     if st:
         _check(st, "hq_rope")
     return q_out, k_out if k is not None else None
+
+
+class _Rope(torch.autograd.Function):
+    """hq_rope in a graph: its gradient is the call with the rotation transposed."""
+
+    @staticmethod
+    def forward(ctx, q, k, pos, table, layout, grad):
+        ctx.save_for_backward(pos)
+        ctx.how = table, layout, not grad
+        ctx.set_materialize_grads(False)
+        return hq_rope(q, k, pos, table, layout, grad)
+
+    @staticmethod
+    def backward(ctx, *g):
+        # of outputs that are used, for inputs that ask; expanded gradients (a sum's) have no rows
+        g = [x.contiguous() if x is not None and need and x.stride(-1) != 1 else x if need else None
+             for x, need in zip(g, ctx.needs_input_grad)]
+        pos, = ctx.saved_tensors
+        if g[0] is not None:
+            g = hq_rope(g[0], g[1], pos, *ctx.how)
+        elif g[1] is not None:
+            g[1] = hq_rope(g[1], None, pos, *ctx.how)[0]
+        return *g, None, None, None, None
 
 
 def _rope_side(x, y, n):

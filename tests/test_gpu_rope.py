@@ -219,3 +219,75 @@ def test_refusals_of_the_binding():
         hq.hq_rope(x, None, pos, t, q_out=x[:3])
     empty, _ = hq.hq_rope(x[:0], None, pos[:0], t)
     assert empty.shape == (0, 2, 64)
+
+
+# ----------------------------------------------------------------------------- in a graph
+
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_gradients_flow(layout, dtype):
+    """The gradient is the transposed call's, to the bit, whichever of q and k ask and however the gradients come."""
+    hq = _hq()
+    torch.manual_seed(11)
+    t, wa = _table(64, "yarn")
+    q, k = torch.randn(2, 9, 4, 96, device="cuda").to(TYPES[dtype]), torch.randn(2, 9, 2, 96, device="cuda").to(TYPES[dtype])
+    pos = torch.randint(0, 5000, (2, 9), dtype=torch.int32, device="cuda")
+    gq, gk = torch.randn_like(q), torch.randn_like(k)
+    plain = hq.hq_rope(q, k, pos, t, layout=layout)
+    want = hq.hq_rope(gq, gk, pos, t, layout=layout, grad=True)
+    _check(gq, want[0], pos, wa, ("half", "interleaved")[layout], dtype, grad=True)
+    for asks in ((True, True), (True, False), (False, True)):
+        a, b = q.clone().requires_grad_(asks[0]), k.clone().requires_grad_(asks[1])
+        yq, yk = hq.hq_rope(a, b, pos, t, layout=layout)
+        assert torch.equal(yq, plain[0]) and torch.equal(yk, plain[1]) and yq.requires_grad
+        torch.autograd.backward((yq, yk), (gq, gk))
+        for x, w, ask in ((a, want[0], asks[0]), (b, want[1], asks[1])):
+            assert torch.equal(x.grad, w) if ask else x.grad is None
+    for use in (0, 1):                     # one output unused; a sum's gradient, expanded
+        a, b = q.clone().requires_grad_(), k.clone().requires_grad_()
+        hq.hq_rope(a, b, pos, t, layout=layout)[use].sum().backward()
+        ones = hq.hq_rope(torch.ones_like(q), torch.ones_like(k), pos, t, layout=layout, grad=True)
+        assert torch.equal((a, b)[use].grad, ones[use]) and ((a, b)[1 - use].grad is None or not (a, b)[1 - use].grad.any())
+    a = q.clone().requires_grad_()         # without k, without a batch, and grad=True of it
+    y, none = hq.hq_rope(a[0], None, pos[0], t, layout=layout, grad=True)
+    assert none is None
+    y.backward(gq[0])
+    assert torch.equal(a.grad[0], hq.hq_rope(gq[0], None, pos[0], t, layout=layout)[0]) and not a.grad[1].any()
+
+
+def test_gradients_of_gradients_shared_heads_and_changed_positions():
+    hq = _hq()
+    t, _ = _table(64)
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")
+    one = torch.randn(5, 1, 64, device="cuda", requires_grad=True)
+    y, _ = hq.hq_rope(one.expand(5, 3, 64), None, pos, t)      # a head shared by three: its gradient is their sum
+    g = torch.randn(5, 3, 64, device="cuda", requires_grad=True)
+    d, = torch.autograd.grad(y, one, g, create_graph=True)
+    assert torch.equal(d, hq.hq_rope(g.detach(), None, pos, t, grad=True)[0].sum(1, keepdim=True))
+    z = torch.randn_like(d)
+    back, = torch.autograd.grad(d, g, z)                         # linear in g: the rotation of z
+    assert torch.equal(back, hq.hq_rope(z.expand(5, 3, 64), None, pos, t)[0])
+    y, _ = hq.hq_rope(one, None, pos, t)
+    pos += 1
+    with pytest.raises(RuntimeError):                            # the positions of the forward call are gone
+        y.sum().backward()
+
+
+def test_outputs_of_the_caller_have_no_gradient():
+    hq = _hq()
+    t, _ = _table(64)
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")
+    x = torch.randn(5, 2, 64, device="cuda", requires_grad=True)
+    for kw in (dict(q_out=torch.empty_like(x)), dict(q_out=x)):
+        with pytest.raises(hq.HqError):
+            hq.hq_rope(x, None, pos, t, **kw)
+    with torch.no_grad():
+        y, _ = hq.hq_rope(x, None, pos, t, q_out=torch.empty(5, 2, 64, device="cuda"))
+        assert not y.requires_grad and torch.equal(y, hq.hq_rope(x, None, pos, t)[0])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y, _ = hq.hq_rope(x, None, pos, t, stream=s)
+    with torch.cuda.stream(s):
+        y.sum().backward()
+    torch.cuda.synchronize()
+    assert torch.equal(x.grad, hq.hq_rope(torch.ones(5, 2, 64, device="cuda"), None, pos, t, grad=True)[0])
