@@ -549,7 +549,7 @@ def hq_rope(q, k, pos, table: RopeTable, layout: int = ROPE_HALF, grad: bool = F
     dt = q.dtype
     _rows(q, dev, shape, "q", _ALL)
     if q_out is None:
-        q_out = torch.empty_like(q)
+        q_out = _like(q)
     else:
         _rows(q_out, dev, shape, "q_out", (dt,))
         if q_out.data_ptr() != q.data_ptr():
@@ -559,7 +559,7 @@ def hq_rope(q, k, pos, table: RopeTable, layout: int = ROPE_HALF, grad: bool = F
     if k is not None:
         _rows(k, dev, (*lead, None, D), "k", (dt,))
         if k_out is None:
-            k_out = torch.empty_like(k)
+            k_out = _like(k)
         else:
             _rows(k_out, dev, k.shape, "k_out", (dt,))
             if k_out.data_ptr() != k.data_ptr():
@@ -593,6 +593,11 @@ class _Rope(torch.autograd.Function):
         elif g[1] is not None:
             g[1] = hq_rope(g[1], None, pos, *ctx.how)[0]
         return *g, None, None, None, None
+
+
+def _like(x):
+    y = torch.empty_like(x)  # in the order of x's strides, which for windows one element apart is not that of rows
+    return y if y.stride(-1) == 1 else x.new_empty(x.shape)
 
 
 def _rope_side(x, y, n):

@@ -291,3 +291,17 @@ def test_outputs_of_the_caller_have_no_gradient():
         y.sum().backward()
     torch.cuda.synchronize()
     assert torch.equal(x.grad, hq.hq_rope(torch.ones(5, 2, 64, device="cuda"), None, pos, t, grad=True)[0])
+
+
+def test_windows_over_one_another():
+    """Heads and tokens one element apart in memory: read as they are, the outputs rows of their own."""
+    hq = _hq()
+    t, wa = _table(8)
+    pos = torch.arange(5, dtype=torch.int32, device="cuda") * 100
+    x = torch.randn(200, device="cuda")
+    for strides in ((1, 1, 1), (1, 7, 1), (9, 1, 1), (0, 1, 1), (1, 0, 1), (0, 0, 1)):
+        q = x.as_strided((5, 3, 8), strides)
+        y, z = hq.hq_rope(q, q[:, :2], pos, t)
+        assert y.stride(-1) == 1 and z.stride(-1) == 1
+        _check(q, y, pos, wa, "half", "f32")
+        _check(q[:, :2], z, pos, wa, "half", "f32")
