@@ -426,6 +426,9 @@ hq_status hq_kv8_append(const hq_kv8_cache* c, int32_t dtype, const void* k, int
   if (st != HQ_OK) return st;
   if ((dtype != HQ_F16 && dtype != HQ_BF16) || N < 0 || !hq::aligned4(cu) || !hq::aligned4(kv_len)) return HQ_ERR_INVALID;
   if (N == 0) return HQ_OK;
+  // the stride of a dimension of one is never used, whatever it says
+  if (N == 1) k_tok = v_tok = 0;
+  if (c->Hkv == 1) k_head = v_head = 0;
   if (!hq::aligned16(k) || !hq::aligned16(v) || (k_tok | k_head | v_tok | v_head) % 8) return HQ_ERR_INVALID;
   hq::AppendArgs a = {*c, {k, v}, {k_tok, v_tok}, {k_head, v_head}, N, cu, kv_len};
   const dim3 grid(static_cast<unsigned>(N) / hq::KV8_BLOCK + 2u * c->B, c->Hkv);
@@ -444,6 +447,9 @@ hq_status hq_kv8_read(const hq_kv8_cache* c, int32_t dtype, const int32_t* kv_le
   if (dtype < HQ_F16 || dtype > HQ_F32 || start < 0 || n < 0 || !hq::aligned4(kv_len)) return HQ_ERR_INVALID;
   if (n == 0) return HQ_OK;
   if (start > c->cap || n > c->cap - start) return HQ_ERR_CAPACITY;
+  if (c->B == 1) o_batch = 0;
+  if (c->Hkv == 1) o_head = 0;
+  if (n == 1) o_tok = 0;
   if (!hq::aligned16(k_out) || !hq::aligned16(v_out) || (o_batch | o_head | o_tok) % 8) return HQ_ERR_INVALID;
   hq::ReadArgs a = {*c, kv_len, start, n, zero_rest, {k_out, v_out}, o_batch, o_head, o_tok};
   const dim3 grid((start + n - 1) / hq::KV8_BLOCK - start / hq::KV8_BLOCK + 1, 2 * c->Hkv, c->B);

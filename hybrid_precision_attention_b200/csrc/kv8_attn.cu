@@ -938,6 +938,9 @@ hq_status hq_kv8_attn(const hq_kv8_cache* c, int32_t dtype, const void* q, int64
     return HQ_ERR_INVALID;
   if (!hq::aligned4(cu) || !hq::aligned4(kv_len) || (lse != nullptr && !hq::aligned4(lse))) return HQ_ERR_INVALID;
   if (N == 0 || max_new == 0) return HQ_OK;
+  // the stride of a dimension of one is never used, whatever it says
+  if (N == 1) q_tok = o_tok = 0;
+  if (Hq == 1) q_head = o_head = 0;
   if (!hq::aligned16(q) || !hq::aligned16(out) || q == out || (q_tok | q_head | o_tok | o_head) % 8) return HQ_ERR_INVALID;
   // scratch is sized from the caller's max_new; fewer rows than that never need more
   int sms = 0;

@@ -1064,3 +1064,28 @@ def test_outputs_that_share_places_are_refused():
             hq.hq_rope(x[:, :4], x[:, 4:6], pos, t, **kw)
     a, b = hq.hq_rope(x[:, :4], x[:, 4:6], pos, t, q_out=x[:, 6:10], k_out=x[:, 4:6])
     assert torch.equal(a, q) and torch.equal(b, k)
+
+
+def test_strides_of_dimensions_of_one():
+    """A single token, kv head or query head may have any stride there (torch gives such tensors odd ones)."""
+    hq = _hq()
+    odd = lambda x, dim: x.as_strided(x.shape, [s if i != dim else 3 for i, s in enumerate(x.stride())])
+    for H, N in ((1, 5), (2, 1), (1, 1)):
+        k, v = torch.randn(N, H, 128, device="cuda").half(), torch.randn(N, H, 128, device="cuda").half()
+        q = torch.randn(N, H, 128, device="cuda").half()
+        cu, n = _ints([0, N]), _ints([N])
+        c, d = hq.Kv8Cache(1, H, 128), hq.Kv8Cache(1, H, 128)
+        hq.hq_kv8_append(c, k, v, cu, n)
+        K, V = hq.hq_kv8_read(c, n, n=N)
+        want = hq.hq_kv8_attn(c, q, cu, n, N)
+        dims = [i for i, m in enumerate((N, H)) if m == 1]
+        for i in dims:
+            k, v, q = odd(k, i), odd(v, i), odd(q, i)
+        out, K2, V2 = torch.empty(N, H, 128, device="cuda").half(), odd(torch.empty_like(K), 0), odd(torch.empty_like(V), 0)
+        for i in dims:
+            out = odd(out, i)
+            K2, V2 = odd(K2, 2 - i), odd(V2, 2 - i)
+        hq.hq_kv8_append(d, k, v, cu, n)
+        assert torch.equal(hq.hq_kv8_attn(d, q, cu, n, N, out=out), want)
+        hq.hq_kv8_read(d, n, n=N, k_out=K2, v_out=V2)
+        assert torch.equal(K, K2) and torch.equal(V, V2)
