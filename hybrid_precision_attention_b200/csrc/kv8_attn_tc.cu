@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       const int cw = (warp - W_CONV) & 1, ct = cw * 32 + lane;  // warp of two, thread of 64
       const int g = lane >> 2, t4 = lane & 3;
       auto await = [&](uint64_t* bar, int parity) {
-        if (__any_sync(0xffffffffu, mbar_try_wait(bar, parity & 1))) return true;
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1))) return true;  // each lane has acquired the phase itself
         ok = wait_for(bar, parity & 1, err, stop);
         ok = __all_sync(0xffffffffu, ok);
         return ok;
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
       const int g = warp - W_MMA;
       const uint32_t leader = elect_leader();
       auto await = [&](uint64_t* bar, int parity) {
-        if (__any_sync(0xffffffffu, mbar_try_wait(bar, parity & 1))) return true;
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1))) return true;  // each lane has acquired the phase itself
         ok = wait_for(bar, parity & 1, err, stop);
         ok = __all_sync(0xffffffffu, ok);
         return ok;
