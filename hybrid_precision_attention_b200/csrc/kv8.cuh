@@ -11,7 +11,6 @@
 namespace hq {
 
 constexpr int KV8_BLOCK = 64;                      // positions of a page
-constexpr int KV8_COPY = HQ_KV8_KSCALE + 16;       // bytes of a page that are copied: codes, scales, padding to 16
 
 // ----------------------------------------------------------------- pairs of floats in one register pair
 
