@@ -650,6 +650,8 @@ __global__ void __launch_bounds__(Cfg<NB, W>::THREADS, Cfg<NB, W>::CTAS) kv8_att
       release();
     }
 
+    // after a wait that gave up the warp's part of this task, and of all that follow in the run, is missing
+    if (!ok && lane == 0) kv8_err(c, k.b, HQ_DEVERR_TIMEOUT);
     const uint32_t u_next = u + k.units;
     Task k_next = k;
     if (u_next < u1) {

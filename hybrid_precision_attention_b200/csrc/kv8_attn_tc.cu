@@ -877,7 +877,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
     tc_fence_after();
     if (threadIdx.x == 0) {
       next_task<NT>(a, walk, units_all, job);
-      if (*stop) job.nt = 0;
+      // after a wait that gave up: the sequences of the tasks that are not begun
+      if (*stop) {
+        for (; job.nt != 0; next_task<NT>(a, walk, units_all, job)) kv8_err(c, job.b, HQ_DEVERR_TIMEOUT);
+      }
     }
     __syncthreads();
     if (job.nt == 0) break;

@@ -528,7 +528,9 @@ HQ_API size_t hq_kv8_attn_workspace_bytes(const hq_kv8_cache* c, int32_t Hq, int
  *   lse    float [N, Hq] contiguous or NULL: log2 of the softmax's denominator,
  *          log2 sum_j 2^(s_j), s_j = q.k_j * sm_scale * log2 e
  * Rows outside [cu[0], cu[B]) and rows of a sequence that is skipped
- * (HQ_DEVERR_CAPACITY, HQ_DEVERR_ROWS) are left as they are.
+ * (HQ_DEVERR_CAPACITY, HQ_DEVERR_ROWS) are left as they are.  A copy that does not land
+ * within about a second ends its block's work: every sequence whose output lacks a part
+ * for it, or was not begun, has HQ_DEVERR_TIMEOUT.
  */
 HQ_API hq_status hq_kv8_attn(const hq_kv8_cache* c, int32_t dtype, const void* q, int64_t q_tok, int64_t q_head,
                              int32_t Hq, int32_t N, const int32_t* cu, const int32_t* kv_len, int32_t max_new,
