@@ -877,9 +877,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
     tc_fence_after();
     if (threadIdx.x == 0) {
       next_task<NT>(a, walk, units_all, job);
-      // after a wait that gave up: the sequences of the tasks that are not begun
+      // after a wait that gave up: the sequences of the tasks that are not begun are marked, and
+      // their pieces counted, so that the counters go back to zero all the same
       if (*stop) {
-        for (; job.nt != 0; next_task<NT>(a, walk, units_all, job)) kv8_err(c, job.b, HQ_DEVERR_TIMEOUT);
+        for (; job.nt != 0; next_task<NT>(a, walk, units_all, job)) {
+          kv8_err(c, job.b, HQ_DEVERR_TIMEOUT);
+          if (!job.whole && atom_add_acq_rel_gpu(a.counters + job.c0, 1u) == static_cast<unsigned int>(job.c1 - job.c0))
+            a.counters[job.c0] = 0u;
+        }
       }
     }
     __syncthreads();

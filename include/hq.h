@@ -510,8 +510,8 @@ HQ_API hq_status hq_kv8_read(const hq_kv8_cache* c, int32_t dtype, const int32_t
 
 /* Device workspace of hq_kv8_attn for these sizes (0: invalid).  Its first
  * HQ_KV8_WS_ZERO bytes are counters: zero them once before its first use; the kernels
- * return them to zero (after a HQ_DEVERR_TIMEOUT they may not be: zero them again).  A
- * workspace must not be shared by calls that can run at the same time. */
+ * return them to zero.  Calls that follow one another may share a workspace, whatever
+ * their caches and sizes; calls that can run at the same time must not. */
 #define HQ_KV8_WS_ZERO 4096
 HQ_API size_t hq_kv8_attn_workspace_bytes(const hq_kv8_cache* c, int32_t Hq, int32_t max_new);
 
