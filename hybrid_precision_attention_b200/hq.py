@@ -607,6 +607,9 @@ def _rope_side(x, y, n):
     return HqRopeTensor(x.data_ptr(), y.data_ptr(), xs[0], xs[1], xs[2], ys[0], ys[1], ys[2], x.shape[2], 0)
 
 
+_SCRATCH = {}  # hq_kv8_attn's, by device and launch stream
+
+
 class Kv8Cache:
     """Device buffers of one layer's 8-bit block cache (layout: include/hq.h, struct hq_kv8_cache).
 
@@ -657,13 +660,16 @@ class Kv8Cache:
         """Every sequence's DEVERR_* bits."""
         bits = self.err.cpu().tolist()
         if any(b & DEVERR_TIMEOUT for b in bits):
-            self._ws.clear()  # a call that gave up may have left counts in its scratch
+            for stream_ptr in self._ws:  # nothing of a call that gave up is used again
+                _SCRATCH.pop((self.index, stream_ptr), None)
+            self._ws.clear()
         return bits
 
     def workspace(self, Hq: int, max_new: int, stream_ptr: int) -> torch.Tensor:
-        """Scratch of an attention call with zeroed counters, one per launch stream: calls on different streams may run
-        at the same time.  A captured call gets its own from the graph's memory pool, its counters cleared in the graph:
-        replays of two graphs share nothing."""
+        """Scratch of an attention call with zeroed counters, one per launch stream for the caches of all layers: calls on
+        different streams may run at the same time.  A captured call gets its own from the graph's memory pool, its
+        counters cleared in the graph by a fill in front of the kernel: replays of two graphs share nothing.  (Scratch
+        of the caller's, zeroed once and kept for the graph, spares the fill.)"""
         n = self._ws_bytes.get((Hq, max_new))
         if n is None:
             n = int(_lib.hq_kv8_attn_workspace_bytes(self.ref, Hq, max_new))
@@ -671,12 +677,14 @@ class Kv8Cache:
                 raise HqError(f"hq_kv8_attn: {Hq} query heads over {self.Hkv} kv heads, {max_new} new tokens")
             self._ws_bytes[(Hq, max_new)] = n
         capturing = torch._C._cuda_isCurrentStreamCapturing()
-        w = None if capturing else self._ws.get(stream_ptr)
+        w = None if capturing else _SCRATCH.get((self.index, stream_ptr))
         if w is None or w.numel() < n:
             w = torch.empty(n, dtype=torch.uint8, device=self.device)
             w[:KV8_WS_ZERO].zero_()
             if not capturing:
-                self._ws[stream_ptr] = w
+                _SCRATCH[(self.index, stream_ptr)] = w
+        if not capturing:
+            self._ws[stream_ptr] = w
         return w
 
 

@@ -1089,3 +1089,35 @@ def test_strides_of_dimensions_of_one():
         assert torch.equal(hq.hq_kv8_attn(d, q, cu, n, N, out=out), want)
         hq.hq_kv8_read(d, n, n=N, k_out=K2, v_out=V2)
         assert torch.equal(K, K2) and torch.equal(V, V2)
+
+
+def test_layers_share_one_scratch_of_a_stream():
+    """The scratch of a prompt chunk is kept once for the stream, not once for each layer's cache; calls of the layers in
+    turn, and on another stream, give what they give alone."""
+    hq = _hq()
+    layers = [Pair(1, 2, 2048, "e4m3", "f16", seed=60 + i) for i in range(4)]
+    q = torch.randn(300, 8, 128, device="cuda").half()
+    calls, want = [], []
+    for p in layers:
+        p.append([2000])
+        for n in (1, 20, 300):
+            calls.append((p.c, q[:n].contiguous(), _ints([0, n]), p.len, n))
+            need = hq._lib.hq_kv8_attn_workspace_bytes(p.c.ref, 8, n)
+            want.append(hq.hq_kv8_attn(*calls[-1], ws=torch.zeros(need, dtype=torch.uint8, device="cuda")))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for stream in (None, s):
+        for _ in range(3):
+            for a, w in zip(calls, want):
+                out = hq.hq_kv8_attn(*a, stream=stream)
+                torch.cuda.synchronize()
+                assert torch.equal(out, w)
+    del out
+    most = hq._lib.hq_kv8_attn_workspace_bytes(layers[0].c.ref, 8, 300)
+    assert torch.cuda.memory_allocated() - before <= 2 * most + (1 << 20)
+    layers[0].c.err[0] = hq.DEVERR_TIMEOUT   # scratch of a call that gave up goes, the other layers' calls get new
+    assert layers[0].c.errors() == [hq.DEVERR_TIMEOUT]
+    layers[0].c.err.zero_()
+    for a, w in zip(calls, want):
+        assert torch.equal(hq.hq_kv8_attn(*a), w)
