@@ -5,8 +5,11 @@
 // fraction of a turn in 64-bit fixed point: position * freqs[i] modulo 2^64 is
 // exact modulo one turn for every int32 position, where float32 angles are off
 // by whole radians at the far end of long contexts and float64 ones cost 1/64
-// of the float32 rate.  Its top 32 bits, taken as signed half-turns, go to
-// sincospif: the angle's own error is at most pi * 2^-25.
+// of the float32 rate.  Its top 32 bits are signed half-turns, of which 24 go to
+// sincospif: for 16-bit rows rounded, an error of at most pi * 2^-25 in the angle.  For
+// float32 rows the other 8 turn its results on by a first-order step (their angle is below
+// 2^-22), so that the angle's error is what is cut off, pi * 2^-31, and sines near 0 are
+// right to their own last bits.
 //
 // Bound by memory: every element is read and written once.  A thread owns V
 // pairs of one token (two V-element accesses, 16 bytes each on the vector path,
@@ -63,10 +66,19 @@ struct Place {
   __device__ __forceinline__ int pair(int i) const { return HALF || V == 1 ? (V == 1 && !HALF ? d0 / 2 : d0 + i) : (i < V / 2 ? d0 / 2 + i : d1 / 2 + i - V / 2); }
 };
 
+template <class E>
 __device__ __forceinline__ float2 sine(const RopeArgs& a, long long tok, int pair) {  // (cos, sin) with their factors
   const uint64_t turns = static_cast<uint64_t>(static_cast<long long>(a.pos[tok])) * a.freqs[pair];
+  const uint32_t t = static_cast<uint32_t>(turns >> 32);
+  // float32: to a multiple of 256 (past the last one a whole turn on)
+  const uint32_t top = sizeof(E) == 4 ? (t + 128u) & ~255u : t;
   float c, s;
-  sincospif(static_cast<float>(static_cast<int32_t>(turns >> 32)) * 4.656612873077393e-10f /* 2^-31 */, &s, &c);
+  sincospif(static_cast<float>(static_cast<int32_t>(top)) * 0x1p-31f, &s, &c);
+  if (sizeof(E) == 4) {
+    const float rest = static_cast<float>(static_cast<int32_t>(t - top)) * 1.46291808e-9f /* pi 2^-31 */, c0 = c;
+    c = fmaf(-s, rest, c);
+    s = fmaf(c0, rest, s);
+  }
   return make_float2(c * a.amp, s * a.sign);
 }
 
@@ -140,7 +152,7 @@ __global__ void __launch_bounds__(256) rope_few_kernel(const __grid_constant__ R
   if (at.turn) {
     float2 cs[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) cs[i] = sine(a, tok, at.pair(i));
+    for (int i = 0; i < V; ++i) cs[i] = sine<E>(a, tok, at.pair(i));
     rotate<E, V, HALF>(u, w, cs);
   }
   E* q = row_of<E>(a, h, b, t, false);
@@ -180,7 +192,7 @@ __global__ void __launch_bounds__(256) rope_many_kernel(const __grid_constant__ 
   const int here = static_cast<int>(min(static_cast<long long>(a.TB), a.tokens - tok0));
   for (int i = threadIdx.x; i < here * pairs; i += 256) {
     const int q = i / pairs;
-    table[i] = sine(a, tok0 + q, i - q * pairs);
+    table[i] = sine<E>(a, tok0 + q, i - q * pairs);
   }
   __syncthreads();
   if (!mine) return;

@@ -305,3 +305,26 @@ def test_windows_over_one_another():
         assert y.stride(-1) == 1 and z.stride(-1) == 1
         _check(q, y, pos, wa, "half", "f32")
         _check(q[:, :2], z, pos, wa, "half", "f32")
+
+
+@pytest.mark.parametrize("T", [50, 20000])
+@pytest.mark.parametrize("layout", [0, 1])
+def test_sines_to_their_last_bits(T, layout):
+    """Pairs (1, 0) become (cos a, sin a) in float32: sincospif is good to 2 ulp (2^-22 of the value), the factor's and the
+    sum's roundings add 2^-23 of it, and the angle is cut off at 2^-31 half-turns (pi 2^-31 < 2^-29, twice that for the
+    first-order step): also where the value is near 0 nothing else is lost."""
+    hq = _hq()
+    g = torch.Generator(device="cuda").manual_seed(5)
+    pos = torch.randint(-2 ** 31, 2 ** 31 - 1, (T,), dtype=torch.int64, device="cuda", generator=g)
+    pos[::3] = torch.arange(pos[::3].numel(), device="cuda")
+    pos[:8] = torch.tensor([0, 1, -1, 355, 710, 103993, 2 ** 31 - 1, -2 ** 31])  # numerators of pi's convergents among them
+    pos = pos.int()
+    t, (w, amp) = _table(16, "plain", base=10000.0)
+    x = torch.zeros(T, 1, 16, device="cuda")
+    first = torch.arange(8) if layout == 0 else torch.arange(8) * 2
+    x[..., first] = 1
+    y, _ = hq.hq_rope(x, None, pos, t, layout=layout)
+    want = orope.rotate(x.double().cpu().numpy(), pos.cpu().numpy(), w, amp, ("half", "interleaved")[layout])
+    err = np.abs(y.double().cpu().numpy() - want)
+    tol = (2.0 ** -22 + 2.0 ** -23) * np.abs(want) + 2.0 ** -28
+    assert (err <= tol).all(), (err / tol).max()
