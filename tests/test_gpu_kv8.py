@@ -1121,3 +1121,24 @@ def test_layers_share_one_scratch_of_a_stream():
     layers[0].c.err.zero_()
     for a, w in zip(calls, want):
         assert torch.equal(hq.hq_kv8_attn(*a), w)
+
+
+@pytest.mark.parametrize("G,n", [(8, 8), (8, 17)])
+def test_many_sequences_of_many_rows(G, n):
+    """More sequences than threads that plan the work, one and two row tiles; every ninth against the oracle."""
+    lens = [(37 * i) % 150 for i in range(700)]
+    p = Pair(700, 1, 256, "e4m3", "bf16", seed=61)
+    p.append(lens)
+    news = [min(m, 1 + (n + i) % n) if i % 3 else min(m, n) for i, m in enumerate(lens)]
+    q, out, lse = p.attend(G, news, check=False)
+    cu = np.concatenate(([0], np.cumsum(news)))
+    for b in range(0, 700, 9):
+        if news[b]:
+            check_rows(out[cu[b]:cu[b + 1]], lse[cu[b]:cu[b + 1]], p.ref[b], q[cu[b]:cu[b + 1]].double().numpy(), 128 ** -0.5, 0, "bf16")
+    again = hq_again(p, q, news, n)
+    assert torch.equal(out, again)
+
+
+def hq_again(p, q, news, n):
+    cu = np.concatenate(([0], np.cumsum(news)))
+    return _hq().hq_kv8_attn(p.c, q.cuda(), _ints(cu.tolist()), p.len, n)

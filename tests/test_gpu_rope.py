@@ -328,3 +328,56 @@ def test_sines_to_their_last_bits(T, layout):
     err = np.abs(y.double().cpu().numpy() - want)
     tol = (2.0 ** -22 + 2.0 ** -23) * np.abs(want) + 2.0 ** -28
     assert (err <= tol).all(), (err / tol).max()
+
+
+# ----------------------------------------------------------------------------- many tokens: heads that share their sines
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("D,rot", [(128, 128), (128, 64), (256, 32), (80, 20), (80, 40), (96, 24), (64, 18), (34, 34), (66, 2), (7, 6), (512, 256)])
+def test_many_tokens(dtype, layout, D, rot):
+    """The block's tokens and heads in every access width: out of views into fused rows with a copied rest, into a
+    transposed output, in place, and one tensor in place beside one that is copied."""
+    hq = _hq()
+    B, T, Hq, Hkv = 2, 2503, 5, 2
+    torch.manual_seed(D * rot)
+    row = torch.randn(B, T, Hq + 2 * Hkv, D, device="cuda").to(TYPES[dtype])
+    q, k, v = row[:, :, :Hq], row[:, :, Hq:Hq + Hkv], row[:, :, Hq + Hkv:]
+    pos = torch.randint(0, 100000, (B, T), dtype=torch.int32, device="cuda")
+    t, wa = _table(rot, "bands" if rot > 2 else "plain")
+    lay = ("half", "interleaved").index(layout)
+    yq, yk = hq.hq_rope(q, k, pos, t, layout=lay)
+    _check(q, yq, pos, wa, layout, dtype)
+    _check(k, yk, pos, wa, layout, dtype)
+    out = torch.full((B, Hq + 1, T, D), 7.0, device="cuda", dtype=TYPES[dtype])
+    hq.hq_rope(q, None, pos, t, layout=lay, q_out=out[:, :Hq].transpose(1, 2))
+    # (not the same to the bit: the kernels for few and for many tokens fuse a product each with their sum)
+    _check(q, out[:, :Hq].transpose(1, 2), pos, wa, layout, dtype)
+    assert (out[:, Hq] == 7).all()
+    v0, q0, k0 = v.clone(), q.clone(), k.clone()
+    z, _ = hq.hq_rope(q, k, pos, t, layout=lay, k_out=k)            # k in place, q copied
+    _check(q, z, pos, wa, layout, dtype)
+    _check(k0, k, pos, wa, layout, dtype)
+    assert torch.equal(q, q0) and torch.equal(v, v0)
+    hq.hq_rope(q, None, pos, t, layout=lay, q_out=q)                  # in place
+    _check(q0, q, pos, wa, layout, dtype)
+    _check(k0, k, pos, wa, layout, dtype)
+    assert torch.equal(v, v0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 0), (8, 1), (9, 8), (33, 8), (70, 10)])
+def test_many_tokens_of_many_heads(dtype, Hq, Hkv):
+    """Heads that the block's threads share out unevenly, rows at an odd offset (single elements), the gradient."""
+    hq = _hq()
+    T = 1501
+    torch.manual_seed(Hq)
+    wide = torch.randn(T, Hq + Hkv, 131, device="cuda").to(TYPES[dtype])
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 37
+    t, wa = _table(96)
+    for x in (wide[..., :128], wide[..., 1:129], wide[..., :128].contiguous()):
+        for grad in (False, True):
+            yq, yk = hq.hq_rope(x[:, :Hq], x[:, Hq:] if Hkv else None, pos, t, grad=grad)
+            _check(x[:, :Hq], yq, pos, wa, "half", dtype, grad)
+            if Hkv:
+                _check(x[:, Hq:], yk, pos, wa, "half", dtype, grad)
