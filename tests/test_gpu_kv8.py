@@ -1142,3 +1142,47 @@ def test_many_sequences_of_many_rows(G, n):
 def hq_again(p, q, news, n):
     cu = np.concatenate(([0], np.cumsum(news)))
     return _hq().hq_kv8_attn(p.c, q.cuda(), _ints(cu.tolist()), p.len, n)
+
+
+@pytest.mark.parametrize("G,n", ROWS)
+@pytest.mark.parametrize("fmt,dtype", [("e4m3", "bf16"), ("int8", "f16")])
+def test_pieces_of_unlike_magnitude(G, n, fmt, dtype):
+    """A long context cut over the grid whose pieces lie far apart: values of 2^-60 to 1 (2^-8 to 1) by turns of 11 blocks,
+    zero blocks among them, a tail of small values with a zero row; the weight on the small ones too."""
+    p = Pair(1, 1, 9088, fmt, dtype, seed=62)
+    L, far = 9011, 60.0 if dtype == "bf16" else 8.0
+    at = torch.arange(L) // 64
+    k, v = p.rows(L).double(), p.rows(L).double() * 2.0 ** (-far * (at // 11 % 5) / 4)[:, None, None]
+    v[at % 17 == 3] = 0
+    v[-19:] *= 2.0 ** -10
+    v[-4] = 0
+    k[:, 0, 0] = torch.where(at // 11 % 5 == 4, 12.0, -12.0)
+    p.append([L], k=k.to(TYPES[dtype]), v=v.to(TYPES[dtype]))
+    q = torch.from_numpy(p.rng.standard_normal((n, G, 128)))
+    q[:, ::2, 0] = 6.0
+    q = q.to(TYPES[dtype])
+    for window in (0, 5000):
+        _, out, _ = p.attend(G, [n], q=q, window=window, check=False)
+        check_relative(p, 0, q, out, window=window)
+        _, again, _ = p.attend(G, [n], q=q, window=window, check=False)
+        assert torch.equal(out, again)
+
+
+def test_taken_back_again_and_started_again():
+    """Drafted tokens taken back several times, up to 64 positions before the furthest one; a slot started again at a
+    multiple of 64 far before its end, and taken back from there."""
+    for dtype in ("f16", "bf16"):
+        p = Pair(3, 2, 512, "e4m3", dtype, seed=63)
+        p.append([130, 300, 191])
+        p.append([30, 40, 10])                                   # 160, 340, 201 the furthest
+        for at, n in (([140, 300, 190], [3, 1, 2]), ([100, 277, 137], [1, 5, 1]), ([96, 276, 138], [64, 64, 64]), ([128, 280, 201], [2, 1, 7])):
+            p.append(n, at=at)
+            p.check_stored()
+        p.append([70, 10, 65], at=[0, 64, 128])
+        p.check_stored()
+        p.append([9, 30, 1], at=[61, 70, 192])
+        p.check_stored()
+        p.append([100, 1, 64])
+        p.check_stored()
+        p.attend(4, [1, 1, 1])
+        assert not any(p.c.errors())
