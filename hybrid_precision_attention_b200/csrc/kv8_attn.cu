@@ -31,7 +31,9 @@
 // Two running references per row: m for the scores and, for the accumulators, E
 // for score + log2(value scale), so that blocks whose scales lie far apart keep
 // their precision.  A weight 2^(s - m) is summed in float32; its product with the
-// value scale enters the matrix product as fp16 at 2^(s + log2 vscale - E + 6).
+// value scale enters the matrix product as fp16 at 2^(s + log2 vscale - E + 6): the type
+// in which codes are exact and a product with them is one instruction.  That rounding adds a
+// quarter to the error of fp16 outputs (2.6e-4 of their size, their own rounding is 2.1e-4).
 // The references are the exact maxima when they are set and stay as they are
 // until a score passes m by 2^8 or a weight E by 2^9: the common block
 // costs one comparison per score and one vote, and no cross-lane maximum.  The
@@ -40,11 +42,13 @@
 // set anew on page after page where the largest score belonged to a small value: 24 rows
 // 143 us against 135.)
 //
-// Measured (8 kv heads): 64 sequences of 1K to 16K, a token each, 8 rows: 182 us, 6.4 TB/s of
-// codes, the copy rate; 16 rows, 64 of 4K to 8K: 135 us, 6.0 TB/s; 24 rows, 64 of 1K to 8K:
-// 131 us, 4.6 TB/s; 16 windows of 4096, 20 rows: 44 us, 3.1 TB/s, bound by the latencies of a
-// step (two warps a scheduler) and by the tasks' ends.  One sequence of 32K: 18.6 us, 3.6 TB/s:
-// 6 us of it are a CTA's 28 pages, the others launch, plan, first copies and the join of 19 pieces.
+// Measured (8 kv heads): 64 sequences of 1K to 16K, a token each, 8 rows: 183 us, 6.3 TB/s of
+// codes, the copy rate; 64 of 1K to 8K: 8 rows 98 us, 6.0 TB/s, 16 rows 106 us, 24 rows 135 us,
+// 4.4 TB/s; 16 windows of 4096, 20 rows: 45 us, 3.0 TB/s, bound by the latencies of a
+// step (two warps a scheduler) and by the tasks' ends.  24 rows take 255 registers and spill 290
+// to 360 bytes a thread; where in the code is not known.  One sequence of 32K: 18.8 us,
+// 3.6 TB/s: 10.4 us of it are the pages at the copy rate, the others launch, plan, first copies
+// and the join of 19 pieces.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -859,10 +863,10 @@ hq_status launch(Kv8AttnArgs& a, int sms, cudaStream_t st) {
 
 // Rows of a kv head, and rows of a task in eights: up to 24 rows in one task, up to 48 in
 // two, which read the pages one after the other, the second mostly from L2.  More go
-// to the tcgen05 kernel, whose pages take the same time for up to 128 rows.  8 kv heads,
-// here and there: 32 rows, 64 sequences of 1K-8K 196 and 296 us, one of 32K 31 and 71, 64 of
-// 100-700 45 and 122; 48 rows 247 and 313, 40 and 71, 67 and 134; from 64 rows on three tasks would
-// take 370 us against 303 where batches are large.
+// to the tcgen05 kernel, whose pages take much the same time for up to 128 rows.  8 kv heads:
+// 64 sequences of 1K-8K, 32 rows here 193 us, 48 rows 248, there 49 rows 274, 64 rows 269; one of
+// 32K 36, 43, 73, 74; 64 of 100-700 47, 72, 106, 104.  From 64 rows on three tasks would
+// take 370 us where batches are large.
 constexpr int ROWS_MAX = 48;
 int task_eights(int64_t rows) {
   const int n = static_cast<int>((rows + 7) / 8);

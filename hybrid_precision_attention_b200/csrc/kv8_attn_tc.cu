@@ -29,9 +29,15 @@
 // Bound: two row tiles and 128 keys take 2048 cycles of products, 2048 of
 // exponentials and, at 128 bytes a cycle, 3000 of shared memory (256 KB of
 // operands, 64 KB converted, 64 KB of codes in and out).
-// Measured: the last 2048 tokens of 16K, 32 query heads over 8: 469 us in a short run,
-// 1100 TFLOP/s, 550 us, 936 TFLOP/s, where runs go on and power bounds the clock; 64
-// sequences x 8 tokens x 8 query heads a kv head over 1K-8K: 300 us, one row tile of 64 rows.
+// They take 4200 cycles by the counters: products 49 % of them, the tensor unit with its
+// operands' traffic 65 %, exponentials 50 %, shared memory 41 %.  No unit is full, and what
+// bounds them (the chain of scores, weights and products with two pages of a stream in
+// flight, by the look of it) is not settled.
+// Measured: the last 2048 tokens of 16K, 32 query heads over 8: 496 us in a short run,
+// 1040 TFLOP/s, 530 us, 972 TFLOP/s, in a long one, where the power limit holds the clock at
+// 1.85 GHz; 64
+// sequences x 8 tokens x 8 query heads a kv head over 1K-8K: 269 us, one row tile of 64 rows.
+// Spills: 16 to 40 bytes a thread.
 //
 // Work: runs of equal units (pages) as in kv8_attn.cu; pieces of a task that
 // CTAs share are joined by the CTA that delivers the last one, in order.
@@ -694,7 +700,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_attn_tc_kernel(const __grid_co
           const float mref = m == -INFINITY ? 0.f : m;
           // Weights of a page that is seen whole take the value scale into the
           // exponent, and their sum is divided by it: a product less per weight.
-          // (The logarithm's error, 2^-22 of it, goes to weights and sum alike.)
+          // (The logarithm's error, 2^-22, goes to the page's weights and not to their sum.)
           // Not where it is so small that weights would underflow.
           const float off = BIAS - e + sc.z, lw = m + off;
           if (__all_sync(0xffffffffu, seen && lw > -60.f)) {

@@ -750,7 +750,9 @@ def hq_kv8_attn(cache: Kv8Cache, q, cu, kv_len, max_new: int, sm_scale: float = 
                 lse=None, return_lse: bool = False, ws=None, stream=None):
     """Attention of the newest tokens (appended before): q [N, Hq, D] holds sequence b's queries as rows
     cu[b] .. cu[b+1]-1, at most max_new of them, at its last positions; causal, with window > 0 over that many
-    positions.  Returns out [N, Hq, D] (``out`` must not overlap q), with return_lse (out, lse float [N, Hq], base 2)."""
+    positions.  Returns out [N, Hq, D] (``out`` must not overlap q), with return_lse (out, lse float [N, Hq], base 2).
+    ``ws``: scratch of the caller's (hq_kv8_attn_workspace_bytes, its first KV8_WS_ZERO bytes zeroed once), in place of
+    the stream's: not for two calls that can run at once, nor for two graphs that can."""
     dev = cache.index
     if stream is not None or _device() != dev:
         with _On(dev, stream):

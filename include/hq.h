@@ -488,9 +488,12 @@ HQ_API hq_status hq_kv8_validate(const hq_kv8_cache* c);
  * (HQ_F16 or HQ_BF16; strides in elements, multiples of 8; D contiguous) and take
  * positions kv_len[b] - n_b .. kv_len[b] - 1, n_b = cu[b+1] - cu[b]: kv_len counts the
  * new tokens.  Blocks that become complete are quantised into their pages, the newest
- * two blocks' rows stand in the tail.  A call may start up to 64 positions before the
- * end of what was appended (drafted tokens that were rejected): the rows from there on
- * are replaced.  cu int32 [B+1], kv_len int32 [B] (device).  A sequence with
+ * two blocks' rows stand in the tail.  A call goes on where the last one ended, or up to
+ * 64 positions before the furthest one appended (drafted tokens that were rejected, more
+ * than once if need be): the rows from there on are replaced; or it starts the sequence
+ * anew at any multiple of 64 (a slot used again), and the furthest one counts from there.
+ * Elsewhere a block's earlier 16-bit rows are gone, which no call can tell.  Rows of both
+ * element types may follow one another.  cu int32 [B+1], kv_len int32 [B] (device).  A sequence with
  * kv_len > cap (HQ_DEVERR_CAPACITY) or inconsistent rows (HQ_DEVERR_ROWS) is left as it is;
  * where cu descends, so that rows belong to two sequences, so may others be.
  */
@@ -527,6 +530,13 @@ HQ_API size_t hq_kv8_attn_workspace_bytes(const hq_kv8_cache* c, int32_t Hq, int
  *          contiguous; they must not overlap
  *   lse    float [N, Hq] contiguous or NULL: log2 of the softmax's denominator,
  *          log2 sum_j 2^(s_j), s_j = q.k_j * sm_scale * log2 e
+ * Sums, softmax and accumulators are float32.  Weights times value scales enter the value
+ * product as fp16 beside the largest of them: to 2^-11 of each, down to 2^-20 of that
+ * largest one, below in steps of 2^-30 of it; keys whose p_j lies below 2^-126 of the
+ * largest count as 0.  A bf16 query enters as fp16 at a power of two of its row: elements
+ * below 2^-29 of the row's largest lose bits.  A row of q that is not finite gives NaN.
+ * HQ_ERR_UNSUPPORTED where the blocks of all tasks may pass 32 bits: a call is taken while
+ * B * Hkv * (cap / 64 + 14) * max(2, Hq / Hkv * max_new / 256 + 1) is below 4e9.
  * Rows outside [cu[0], cu[B]) and rows of a sequence that is skipped
  * (HQ_DEVERR_CAPACITY, HQ_DEVERR_ROWS) are left as they are.  A copy that does not land
  * within about a second ends its block's work: every sequence whose output lacks a part
