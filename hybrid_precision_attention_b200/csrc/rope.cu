@@ -337,7 +337,7 @@ hq_status hq_rope(int32_t dtype, int32_t B, int32_t T, int32_t D, int32_t rot, i
     if (y.H <= 1) y.x_head = y.y_head = 0;
     a.inplace[z] = y.x == y.y;
     // in place, every element must be read where it is written
-    if (a.inplace[z] && (y.x_batch != y.y_batch || y.x_tok != y.y_tok || y.x_head != y.y_head)) return HQ_ERR_INVALID;
+    if (a.inplace[z] && B > 0 && T > 0 && x->H > 0 && (y.x_batch != y.y_batch || y.x_tok != y.y_tok || y.x_head != y.y_head)) return HQ_ERR_INVALID;
   }
   a.H0 = q->H;
   a.H = q->H + (k ? k->H : 0);

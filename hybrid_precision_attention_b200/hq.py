@@ -459,7 +459,7 @@ def _rows(t, index, shape, name, dtypes=_HALVES):
     """A tensor of that shape (None: any size) on that CUDA device, its last dimension contiguous."""
     have = t.shape
     ok = len(have) == len(shape) and t.dtype in dtypes and t.is_cuda and t.get_device() == index and \
-        (t.stride(-1) == 1 or have[-1] <= 1)
+        (t.stride(-1) == 1 or have[-1] <= 1 or t.numel() == 0)
     if ok:
         for n, m in zip(shape, have):
             if n != m and n is not None:

@@ -1186,3 +1186,15 @@ def test_taken_back_again_and_started_again():
         p.check_stored()
         p.attend(4, [1, 1, 1])
         assert not any(p.c.errors())
+
+
+def test_empty_rows_of_any_stride():
+    """No new rows, as torch makes them out of an empty array (strides of 0)."""
+    hq = _hq()
+    c = hq.Kv8Cache(2, 3, 128)
+    none = torch.empty(0, 3, 128, device="cuda").half().as_strided((0, 3, 128), (0, 0, 0))
+    cu, n = _ints([0, 0, 0]), _ints([0, 0])
+    hq.hq_kv8_append(c, none, none, cu, n)
+    assert hq.hq_kv8_attn(c, none, cu, n, 1).shape == (0, 3, 128) and not any(c.errors())
+    y, _ = hq.hq_rope(none, none, _ints([]), hq.RopeTable(64))
+    assert y.shape == (0, 3, 128)
