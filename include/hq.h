@@ -491,7 +491,8 @@ HQ_API hq_status hq_kv8_validate(const hq_kv8_cache* c);
  * two blocks' rows stand in the tail.  A call goes on where the last one ended, or up to
  * 64 positions before the furthest one appended (drafted tokens that were rejected, more
  * than once if need be): the rows from there on are replaced; or it starts the sequence
- * anew at any multiple of 64 (a slot used again), and the furthest one counts from there.
+ * anew at any multiple of 64 (a slot used again): the furthest one then counts from there,
+ * and no later call goes back past that start but to start anew again.
  * Elsewhere a block's earlier 16-bit rows are gone, which no call can tell.  Rows of both
  * element types may follow one another.  cu int32 [B+1], kv_len int32 [B] (device).  A sequence with
  * kv_len > cap (HQ_DEVERR_CAPACITY) or inconsistent rows (HQ_DEVERR_ROWS) is left as it is;
