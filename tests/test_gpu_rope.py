@@ -381,3 +381,31 @@ def test_many_tokens_of_many_heads(dtype, Hq, Hkv):
             _check(x[:, :Hq], yq, pos, wa, "half", dtype, grad)
             if Hkv:
                 _check(x[:, Hq:], yk, pos, wa, "half", dtype, grad)
+
+
+def test_a_captured_step_with_its_gradient():
+    """Forward and gradient captured into a graph, and replayed on other inputs.  (While an eager graph of the same leaf
+    lives, torch itself ends such a capture, whatever the operators: it synchronises with the leaf's stream.)"""
+    hq = _hq()
+    t, wa = _table(64)
+    pos = torch.arange(7, dtype=torch.int32, device="cuda")
+    x = torch.randn(7, 2, 64, device="cuda", requires_grad=True)
+    g = torch.randn(7, 2, 64, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.autograd.grad(hq.hq_rope(x, None, pos, t)[0], x, g)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, _ = hq.hq_rope(x, None, pos, t)
+        d, = torch.autograd.grad(y, x, g)
+    for i in range(3):
+        with torch.no_grad():
+            x.copy_(torch.randn_like(x))
+        g.copy_(torch.randn_like(g))
+        pos += 1000
+        graph.replay()
+        torch.cuda.synchronize()
+        _check(x.detach(), y.detach(), pos, wa, "half", "f32")
+        _check(g, d, pos, wa, "half", "f32", grad=True)
