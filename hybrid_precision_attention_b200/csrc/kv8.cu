@@ -198,18 +198,19 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(const __grid_constan
     const bool mixed = __syncthreads_or(lost);
     if (idx < 0) {
       if (tid == 0) kv8_err(c, b, HQ_DEVERR_PAGE);
+    } else if (mixed) {
+      uint8_t* page = c.pages + static_cast<size_t>(idx) * HQ_KV8_PAGE_BYTES;
+#pragma unroll 1
+      for (int which = 0; which < 2; ++which)
+        append_mixed<E, FMT>(source(which) + static_cast<int64_t>(p0) * a.tok[which], a.tok[which],
+                             tail_of(which) + half * KV8_BLOCK * D, scales_of(which) + half * KV8_BLOCK, s.first - p0, which,
+                             page + (which ? HQ_KV8_V : 0), reinterpret_cast<float*>(page + (which ? HQ_KV8_VSCALE : HQ_KV8_KSCALE)),
+                             &sh_amax[which]);
     } else {
       uint8_t* page = c.pages + static_cast<size_t>(idx) * HQ_KV8_PAGE_BYTES;
       const int lane = tid & 31;
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
-        if (mixed) {
-          append_mixed<E, FMT>(source(which) + static_cast<int64_t>(p0) * a.tok[which], a.tok[which],
-                               tail_of(which) + half * KV8_BLOCK * D, scales_of(which) + half * KV8_BLOCK, s.first - p0, which,
-                               page + (which ? HQ_KV8_V : 0), reinterpret_cast<float*>(page + (which ? HQ_KV8_VSCALE : HQ_KV8_KSCALE)),
-                               &sh_amax[which]);
-          continue;
-        }
         const float scale = kv8_scale(__float_as_uint(pair_of<E>(sh_amax[which]).x), FMT);
         const bool plain = kv8_scale_plain(scale);
         const float r = 1.0f / scale;
