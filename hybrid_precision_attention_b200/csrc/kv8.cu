@@ -12,7 +12,7 @@
 // of one d, is what the transposed 8x8 matrix loads and stores (ldmatrix,
 // stmatrix) exchange, so that no element moves by itself.
 // Measured (8 kv heads): 5 prompts of 8191 appended in 61 us, 3.9 TB/s (elements moved
-// one by one and each divided: 101 us), a token to each of 64 sequences in 8.2 us (a chain of
+// one by one and each divided: 101 us), a token to each of 64 sequences in 8.1 us (a chain of
 // look-ups, tail, block); two sequences of 32K read back in 71 us, 5.7 TB/s (115 us), as float32
 // in 113 us, 5.9 TB/s; three short ones in 6.0 us.
 #include <cuda_runtime.h>

@@ -542,7 +542,7 @@ def hq_rope(q, k, pos, table: RopeTable, layout: int = ROPE_HALF, grad: bool = F
     if stream is not None or _device() != dev:
         with _On(dev, stream):
             return hq_rope(q, k, pos, table, layout, grad, q_out, k_out)
-    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+    if (q.requires_grad or (k is not None and k.requires_grad)) and torch.is_grad_enabled():
         if q_out is not None or k_out is not None:
             raise HqError("hq_rope: q_out and k_out have no gradient, and q or k requires one (torch.no_grad, or leave them out)")
         return _Rope.apply(q, k, pos, table, layout, grad)
@@ -555,22 +555,22 @@ def hq_rope(q, k, pos, table: RopeTable, layout: int = ROPE_HALF, grad: bool = F
     dt = q.dtype
     _rows(q, dev, shape, "q", _ALL)
     if q_out is None:
-        q_out = _like(q)
+        q_out = torch.empty_like(q)
     else:
         _rows(q_out, dev, shape, "q_out", (dt,))
         if q_out.data_ptr() != q.data_ptr():
             _output("hq_rope", q_out, "q_out", "q", q)
-    a = _rope_side(q, q_out, n)
+    a, q_out = _rope_side(q, q_out, n)
     b = None
     if k is not None:
         _rows(k, dev, (*lead, None, D), "k", (dt,))
         if k_out is None:
-            k_out = _like(k)
+            k_out = torch.empty_like(k)
         else:
             _rows(k_out, dev, k.shape, "k_out", (dt,))
             if k_out.data_ptr() != k.data_ptr():
                 _output("hq_rope", k_out, "k_out", "k", k)
-        b = _rope_side(k, k_out, n)
+        b, k_out = _rope_side(k, k_out, n)
     st = _lib.hq_rope(_DTYPE[dt], lead[0] if n == 4 else 1, lead[-1], D, table.rot, layout, 1 if grad else 0, a, b,
                       pos.data_ptr(), table._ptr, table.amp, _raw_stream(dev))
     if st:
@@ -601,16 +601,16 @@ class _Rope(torch.autograd.Function):
         return *g, None, None, None, None
 
 
-def _like(x):
-    y = torch.empty_like(x)  # in the order of x's strides, which for windows one element apart is not that of rows
-    return y if y.stride(-1) == 1 else x.new_empty(x.shape)
-
-
 def _rope_side(x, y, n):
+    """A tensor's part of the call, and its output: empty_like's follows the order of x's strides, which for windows one
+    element apart is not that of rows, and is made anew then."""
     xs, ys = x.stride(), y.stride()
+    if ys[-1] != 1 and y.shape[-1] > 1 and y.numel():
+        y = x.new_empty(x.shape)
+        ys = y.stride()
     if n == 3:
-        return HqRopeTensor(x.data_ptr(), y.data_ptr(), 0, xs[0], xs[1], 0, ys[0], ys[1], x.shape[1], 0)
-    return HqRopeTensor(x.data_ptr(), y.data_ptr(), xs[0], xs[1], xs[2], ys[0], ys[1], ys[2], x.shape[2], 0)
+        return HqRopeTensor(x.data_ptr(), y.data_ptr(), 0, xs[0], xs[1], 0, ys[0], ys[1], x.shape[1], 0), y
+    return HqRopeTensor(x.data_ptr(), y.data_ptr(), xs[0], xs[1], xs[2], ys[0], ys[1], ys[2], x.shape[2], 0), y
 
 
 _SCRATCH = {}  # hq_kv8_attn's, by device and launch stream
