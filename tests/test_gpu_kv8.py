@@ -1198,3 +1198,47 @@ def test_empty_rows_of_any_stride():
     assert hq.hq_kv8_attn(c, none, cu, n, 1).shape == (0, 3, 128) and not any(c.errors())
     y, _ = hq.hq_rope(none, none, _ints([]), hq.RopeTable(64))
     assert y.shape == (0, 3, 128)
+
+
+def test_strides_beyond_32_bits():
+    """Tokens 2^30 elements apart: rows of every call (rotary positions, append, read back, queries and outputs of both
+    kernels) at offsets past 2^31 elements."""
+    hq = _hq()
+    far, n, G = 1 << 30, 3, 17
+    buf = torch.empty((n - 1) * far + 6 * (G + 2) * 128, dtype=torch.bfloat16, device="cuda")
+    at = lambda i, h: buf.as_strided((n, h, 128), (far, 128, 1), i * (G + 2) * 128)
+    small = lambda h: torch.randn(n, h, 128, device="cuda").bfloat16()
+    q, k, v = small(G), small(1), small(1)
+    qf, kf, vf = at(0, G), at(1, 1), at(2, 1)
+    t, pos = hq.RopeTable(128), _ints([5, 6, 7])
+    cu, L = _ints([0, n]), _ints([n])
+    for x, y in ((qf, q), (kf, k), (vf, v)):
+        x.copy_(y)
+    q2, k2 = hq.hq_rope(q, k, pos, t)
+    hq.hq_rope(qf, kf, pos, t, q_out=at(3, G), k_out=kf)
+    assert torch.equal(at(3, G), q2) and torch.equal(kf, k2) and torch.equal(qf, q)
+    a, b = hq.Kv8Cache(1, 1, 128), hq.Kv8Cache(1, 1, 128)
+    hq.hq_kv8_append(a, k2, v, cu, L)
+    hq.hq_kv8_append(b, kf, vf, cu, L)
+    assert torch.equal(a.tail_k, b.tail_k) and torch.equal(a.tail_v, b.tail_v) and torch.equal(a.tail_scale, b.tail_scale)
+    for h in (G, 5, 1):                                       # 51 rows, 15, 3
+        want = hq.hq_kv8_attn(a, q2[:, :h].contiguous(), cu, L, n)
+        out = hq.hq_kv8_attn(b, at(3, h), cu, L, n, out=at(4, h))
+        assert torch.equal(out, want)
+    K, V = hq.hq_kv8_read(a, L, n=n, dtype=torch.bfloat16)
+    shape, strides = (1, 1, n, 128), (128, 128, far, 1)
+    K2, V2 = (buf.as_strided(shape, strides, i * (G + 2) * 128) for i in (4, 5))
+    hq.hq_kv8_read(b, L, n=n, k_out=K2, v_out=V2)
+    assert torch.equal(K, K2) and torch.equal(V, V2)
+
+
+def test_the_largest_batch():
+    """1024 sequences, one to three tokens each, and 20 of some: every plan's last entries."""
+    lens = [1 + (53 * i) % 90 for i in range(1024)]
+    p = Pair(1024, 1, 128, "int8", "f16", seed=64)
+    p.append(lens)
+    for G, news in ((3, [1 + i % min(3, m) for i, m in enumerate(lens)]), (8, [min(m, 20 if i % 7 == 0 else 1) for i, m in enumerate(lens)])):
+        q, out, lse = p.attend(G, news, check=False)
+        cu = np.concatenate(([0], np.cumsum(news)))
+        for b in list(range(0, 1024, 23)) + [1022, 1023]:
+            check_rows(out[cu[b]:cu[b + 1]], lse[cu[b]:cu[b + 1]], p.ref[b], q[cu[b]:cu[b + 1]].double().numpy(), 128 ** -0.5, 0, "f16")
