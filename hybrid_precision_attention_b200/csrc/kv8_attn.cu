@@ -33,7 +33,8 @@
 // their precision.  A weight 2^(s - m) is summed in float32; its product with the
 // value scale enters the matrix product as fp16 at 2^(s + log2 vscale - E + 6): the type
 // in which codes are exact and a product with them is one instruction.  That rounding adds a
-// quarter to the error of fp16 outputs (2.6e-4 of their size, their own rounding is 2.1e-4).
+// quarter to a third to the error of fp16 outputs (2.6e-4 to 2.9e-4 of their size, their own
+// rounding is 2.1e-4).
 // The references are the exact maxima when they are set and stay as they are
 // until a score passes m by 2^8 or a weight E by 2^9: the common block
 // costs one comparison per score and one vote, and no cross-lane maximum.  The
